@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libhla.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["chunk.hip", "scan.hip", "prefill.hip", "route.hip", "compose.hip", "decode.hip", "reps.hip", "reps_bwd.hip", "gdn2.hip", "compose_bwd.hip", "chunk_bwd.hip", "gdn2_bwd.hip", "router_bwd.hip", "abi.cpp", "timing.cpp"]
+SOURCES = ["chunk.hip", "scan.hip", "prefill.hip", "route.hip", "compose.hip", "decode.hip", "reps.hip", "reps_bwd.hip", "gdn2.hip", "compose_bwd.hip", "chunk_bwd.hip", "gdn2_bwd.hip", "router_bwd.hip", "cache8.hip", "cache8_fill.hip", "abi.cpp", "abi_cache8.cpp", "timing.cpp"]
 
 # Packed fp32 VALU ops are disabled for the device: the kernels are written with scalar
 # fp32 arithmetic and must not be turned into v_pk_* instructions.
@@ -66,7 +66,7 @@ def build_library(verbose: bool = False) -> str:
 
 # Host code only (the C ABI's argument checks, workspace sizing and launch set-up) under
 # AddressSanitizer and UndefinedBehaviorSanitizer; every flag is scoped to the host pass.
-HOST_SOURCES = ("abi.cpp", "timing.cpp")
+HOST_SOURCES = ("abi.cpp", "abi_cache8.cpp", "timing.cpp")
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer"]
 

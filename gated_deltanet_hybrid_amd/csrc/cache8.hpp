@@ -1,0 +1,119 @@
+// The 8-bit chunk cache: its device view, the two stored formats, and the launchers.
+#pragma once
+#include "common.hpp"
+
+namespace hla {
+
+// hla_cache8_t as the kernels take it (include/hla.h describes the arrays).
+struct Cache8View {
+  uint8_t* maps;    // [Bs,H,n_cap,dk+dv,dk]
+  uint8_t* reps;    // [Bs,H,n_cap,n_rep,dk]
+  float4* scale;    // [Bs,H,n_cap]: of A - I, of B, of the representatives, 0
+  int32_t* order;   // [Bs,H,n_cap]
+  int32_t* count;   // [Bs,H]
+  float* weight;    // [Bs,H,n_cap] or null
+  int64_t rows;     // Bs H
+  int32_t n_cap, n_rep;
+};
+
+// What the caller's memory holds is clamped before it becomes an address: a count to the
+// capacity, a slot to the cache.
+__device__ __forceinline__ int cache8_count(const Cache8View& c, int64_t row) {
+  const int n = c.count[row];
+  return n < 0 ? 0 : (n > c.n_cap ? c.n_cap : n);
+}
+__device__ __forceinline__ int cache8_slot(const Cache8View& c, int64_t row, int pos) {
+  const unsigned s = (unsigned)c.order[row * c.n_cap + pos];
+  return s < (unsigned)c.n_cap ? (int)s : c.n_cap - 1;
+}
+
+// The stored formats.  Quantising multiplies by top / max (rounded to nearest, ties to even)
+// so that the largest magnitude lands on `top`; a block whose largest magnitude is below
+// 2^-100 is stored as zeros with scale 0, since top / max would overflow.
+constexpr int kI8 = 0, kE4M3 = 1;
+constexpr float kCache8Tiny = 0x1p-100f;
+template <int FMT> struct Stored;
+template <> struct Stored<kI8> {
+  static constexpr float top = 127.f;
+  // the four bytes of a word, exactly
+  __device__ __forceinline__ static void unpack(unsigned w, float (&f)[4]) {
+    f[0] = (float)(int8_t)w; f[1] = (float)(int8_t)(w >> 8); f[2] = (float)(int8_t)(w >> 16); f[3] = (float)(int8_t)(w >> 24);
+  }
+  __device__ __forceinline__ static unsigned pack(float a, float b, float c, float d) {
+    auto q = [](float x) { return (unsigned)(int)fminf(fmaxf(rintf(x), -127.f), 127.f) & 0xffu; };
+    return q(a) | q(b) << 8 | q(c) << 16 | q(d) << 24;
+  }
+};
+template <> struct Stored<kE4M3> {
+  static constexpr float top = 448.f;
+  __device__ __forceinline__ static void unpack(unsigned w, float (&f)[4]) {
+    f[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0); f[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1);
+    f[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2); f[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3);
+  }
+  __device__ __forceinline__ static unsigned pack(float a, float b, float c, float d) {
+    // rounding may leave x (top / max) one step above top: clamped, it stores top
+    auto cl = [](float x) { return fminf(fmaxf(x, -448.f), 448.f); };
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(cl(a), cl(b), 0, false);
+    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(cl(c), cl(d), w, true);
+  }
+};
+
+struct Decode8Args {
+  Cache8View c;
+  const void* q;          // [Bs,H,dk] (dtype)
+  const void* k;
+  const void* v;          // [Bs,H,dv]
+  const float* beta;      // [Bs,H], Gated DeltaNet
+  const float* alpha;
+  const float* ga;        // [Bs,H,dk], Gated DeltaNet-2 (ga set): decay, erase gate
+  const float* gb;
+  const float* gw;        // [Bs,H,dv]: write gate
+  float* S_cur;           // [Bs,H,dk,dv]
+  float* At_cur;          // [Bs,H,dk,dk]
+  const float* gates_in;  // [Bs,H,n_cap] or null
+  float* o;               // [Bs,H,dv]
+  float* gates_out;       // [Bs,H,n_cap] or null
+  float tau;
+};
+hipError_t launch_decode8(const Decode8Args& a, int fmt, int dtype, int dk, int dv, hipStream_t s);
+
+struct Append8Args {
+  Cache8View c;
+  void* At;               // [Bs,H,ld_src,dk,dk] (dtype), state orientation
+  void* Bc;               // [Bs,H,ld_src,dk,dv]
+  const void* reps;       // [Bs,ld_R,H,dk]: source chunk i's rows are [i n_rep, (i+1) n_rep)
+  int64_t H, ld_R;
+  const int32_t* src;     // [Bs,H,ld_src] source chunk of each appended one, or null (i)
+  const int32_t* n_new;   // [Bs,H] or null (n_src)
+  const float* weight_in; // [Bs,H,ld_src] or null (0)
+  int32_t n_src, ld_src;
+  int32_t reset, reset_live;
+};
+hipError_t launch_append8(const Append8Args& a, int fmt, int dtype, int dk, int dv, hipStream_t s);
+
+struct GateWeightsArgs {
+  const float* gates;       // [B,H,N,N]
+  const int32_t* n_chunks;  // [B] or null (N)
+  float* weight;            // [B,H,N]
+  int64_t B, H;
+  int32_t N;
+  float tau;
+};
+hipError_t launch_gate_weights(const GateWeightsArgs& a, hipStream_t s);
+
+struct EvictArgs {
+  const float* weight;     // [rows,n]
+  const int32_t* order;    // [rows,n] or null (identity)
+  const int32_t* count;    // [rows]
+  int32_t* order_out;
+  float* weight_out;
+  int32_t* count_out;
+  int64_t rows;
+  int32_t n, budget, n_recent;
+};
+hipError_t launch_evict(const EvictArgs& a, hipStream_t s);
+
+// Gate of one chunk as it counts for its weight.
+__device__ __forceinline__ float gate_mass(float g) { return fminf(fmaxf(g, 0.f), 1.f); }
+
+}  // namespace hla

@@ -43,7 +43,14 @@ class Dims(ctypes.Structure):
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class _Cache8Struct(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("Bs", "H")]
+                + [(n, ctypes.c_int32) for n in ("dk", "dv", "n_cap", "n_rep", "format")]
+                + [(n, ctypes.c_void_p) for n in ("maps", "reps", "scale", "order", "count", "weight")])
+
+
 _P = ctypes.c_void_p
+_C8 = ctypes.POINTER(_Cache8Struct)
 _SIGS = {
     "hla_abi_version": (ctypes.c_int32, []),
     "hla_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
@@ -79,6 +86,17 @@ _SIGS = {
     "hla_chunk_reps_backward": (ctypes.c_int32, [ctypes.POINTER(Dims), _P, ctypes.c_int32, _P, _P, _P, _P, _P,
                                                  ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
                                                  _P]),
+    "hla_cache8_append": (ctypes.c_int32, [_C8, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P,
+                                           ctypes.c_int64, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P]),
+    "hla_gdn_decode8": (ctypes.c_int32, [_C8, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P,
+                                         _P, ctypes.c_size_t, _P]),
+    "hla_gdn2_decode8": (ctypes.c_int32, [_C8, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P,
+                                          _P, _P, ctypes.c_size_t, _P]),
+    "hla_decode8_workspace_bytes": (ctypes.c_int32, [_C8, ctypes.POINTER(ctypes.c_size_t)]),
+    "hla_gate_weights": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P, _P, ctypes.c_float, _P,
+                                          _P]),
+    "hla_evict_chunks": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, ctypes.c_int32,
+                                          ctypes.c_int32, _P, _P, _P, _P]),
     "hla_timing_enable": (ctypes.c_int32, [ctypes.c_int32]),
     "hla_timing_read": (ctypes.c_int32, [ctypes.c_int32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]),
     "hla_gdn_decode": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
@@ -683,6 +701,224 @@ def _decode(fn, gates, q, k, v, S_cur, At_cur, At_cache, Bc_cache, reps_cache, n
                                   _ptr(n_cache), n_cap, _ptr(gates_in), ctypes.c_float(tau), _ptr(o),
                                   _ptr(gates_out), 1 if commit else 0, _stream(dev)), fn)
     return o
+
+
+# ------------------------------------------------------------------ the 8-bit chunk cache
+CACHE_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
+MAX_CACHE_REPS = 256
+
+
+def _need_on(t, shape, dtype, device, name):
+    if t is None:
+        return
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _call(name, device, *args):
+    """Library call on `device`'s current stream (whatever device is current)."""
+    fn = getattr(library(), name)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _check(fn(*args, _stream(device)), name)
+    _check(fn(*args, _stream(device)), name)
+
+
+class Cache8:
+    """Chunk maps and representatives of every (sequence, head) in 8 bits: a fixed set of
+    device tensors, checked once here (cache8_alloc makes an empty one).
+
+    maps [Bs, H, n_cap, dk + dv, dk] (int8 or float8_e4m3fn; rows of A - I, then of B), reps
+    [Bs, H, n_cap, n_rep, dk] or None, scale [Bs, H, n_cap, 4], order [Bs, H, n_cap] int32 (slot
+    of every position in time), count [Bs, H] int32, weight [Bs, H, n_cap] or None."""
+    __slots__ = ("maps", "reps", "scale", "order", "count", "weight", "Bs", "H", "n_cap", "n_rep", "dk", "dv",
+                 "device", "_struct", "_ref", "_ws_bytes")
+
+    def __init__(self, maps, reps, scale, order, count, weight=None):
+        if maps.dim() != 5 or not maps.is_cuda:
+            raise ValueError("maps must be a CUDA tensor [Bs, H, n_cap, dk + dv, dk]")
+        Bs, H, n_cap, rows, dk = maps.shape
+        dv, dev = rows - dk, maps.device
+        fmt = [code for code, dt in CACHE_FORMATS.values() if dt == maps.dtype]
+        if not fmt:
+            raise TypeError(f"unsupported cache dtype {maps.dtype} (int8 or float8_e4m3fn)")
+        n_rep = 0 if reps is None else reps.shape[3] if reps.dim() == 5 else -1
+        _need_on(maps, (Bs, H, n_cap, rows, dk), maps.dtype, dev, "maps")
+        _need_on(reps, (Bs, H, n_cap, n_rep, dk), maps.dtype, dev, "reps")
+        for t, shape, dtype, name in ((scale, (Bs, H, n_cap, 4), torch.float32, "scale"),
+                                      (order, (Bs, H, n_cap), torch.int32, "order"),
+                                      (count, (Bs, H), torch.int32, "count")):
+            if t is None:
+                raise ValueError(f"{name} is required")
+            _need_on(t, shape, dtype, dev, name)
+        _need_on(weight, (Bs, H, n_cap), torch.float32, dev, "weight")
+        self.maps, self.reps, self.scale, self.order, self.count, self.weight = maps, reps, scale, order, count, weight
+        self.Bs, self.H, self.n_cap, self.n_rep, self.dk, self.dv, self.device = Bs, H, n_cap, n_rep, dk, dv, dev
+        self._struct = _Cache8Struct(Bs, H, dk, dv, n_cap, n_rep, fmt[0],
+                                     *(None if t is None else t.data_ptr()
+                                       for t in (maps, reps, scale, order, count, weight)))
+        self._ref = ctypes.byref(self._struct)
+        out = ctypes.c_size_t(0)
+        _check(library().hla_decode8_workspace_bytes(self._ref, ctypes.byref(out)), "hla_decode8_workspace_bytes")
+        self._ws_bytes = out.value
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "_ws_bytes"):
+            raise AttributeError("a cache's tensors are fixed: make another Cache8")
+        object.__setattr__(self, name, value)
+
+
+def cache8_alloc(Bs, H, n_cap, dk, dv, n_rep=0, fmt="int8", weights=True, device="cuda"):
+    """An empty 8-bit chunk cache (fmt "int8" or "e4m3")."""
+    dtype = CACHE_FORMATS[fmt][1]
+    e = lambda *s, dt: torch.zeros(s, dtype=dt, device=device)  # noqa: E731
+    return Cache8(maps=e(Bs, H, n_cap, dk + dv, dk, dt=torch.uint8).view(dtype),
+                  reps=e(Bs, H, n_cap, n_rep, dk, dt=torch.uint8).view(dtype) if n_rep else None,
+                  scale=e(Bs, H, n_cap, 4, dt=torch.float32),
+                  order=torch.arange(n_cap, dtype=torch.int32, device=device).repeat(Bs, H, 1),
+                  count=e(Bs, H, dt=torch.int32), weight=e(Bs, H, n_cap, dt=torch.float32) if weights else None)
+
+
+def cache8_workspace_bytes(cache: Cache8) -> int:
+    """Bytes of the workspace a decode step over `cache` takes (its ws argument)."""
+    return cache._ws_bytes
+
+
+def cache8_append(cache, At, Bc, reps=None, src=None, n_new=None, weight_in=None, reset=False, reset_live=False,
+                  n=None):
+    """Quantise chunks and append them to every row of the cache.
+
+    At [Bs, H, L, dk, dk], Bc [Bs, H, L, dk, dv] (bf16 or float32) as chunk_transitions gives
+    them, or a live chunk ([Bs, H, dk, dk] and [Bs, H, dk, dv], float32); the first n of them
+    (all by default) are complete chunks.  reps [Bs, at least n * n_rep, H, dk] in their dtype,
+    chunk i's rows [i n_rep, (i + 1) n_rep).  src [Bs, H, L] int32 names the source chunk of
+    every appended one, n_new [Bs, H] int32 how many to append, weight_in [Bs, H, L] their
+    weights.  reset empties the cache first; reset_live sets the source maps to A = I, B = 0
+    where they were appended.  Chunks past the cache's room are dropped."""
+    c = cache
+    if At.dim() == 4:
+        At, Bc = At.unsqueeze(2), Bc.unsqueeze(2)
+    L = At.shape[2]
+    n = L if n is None else n
+    dt = _dtype_code(At)
+    _need_on(At, (c.Bs, c.H, L, c.dk, c.dk), At.dtype, c.device, "At")
+    _need_on(Bc, (c.Bs, c.H, L, c.dk, c.dv), At.dtype, c.device, "Bc")
+    ld_R = 0
+    if c.n_rep:
+        if reps is None:
+            raise ValueError("reps is required: the cache holds representatives")
+        Br, R, Hr, dr, ld_R = _token_view(reps, "reps")
+        if (Br, Hr, dr) != (c.Bs, c.H, c.dk) or R < n * c.n_rep or reps.dtype != At.dtype or reps.device != c.device:
+            raise ValueError("reps must be [Bs, at least n * n_rep, H, dk] in At's dtype on the cache's device")
+    _need_on(src, (c.Bs, c.H, L), torch.int32, c.device, "src")
+    _need_on(n_new, (c.Bs, c.H), torch.int32, c.device, "n_new")
+    _need_on(weight_in, (c.Bs, c.H, L), torch.float32, c.device, "weight_in")
+    _call("hla_cache8_append", c.device, c._ref, dt, n, L, _ptr(At), _ptr(Bc), _ptr(reps) if c.n_rep else None, ld_R,
+          _ptr(src), _ptr(n_new), _ptr(weight_in), 1 if reset else 0, 1 if reset_live else 0)
+
+
+def gdn_decode8(q, k, v, beta, alpha, S_cur, At_cur, cache, gates_in=None, tau=1e-3, o=None, gates_out=None, ws=None):
+    """gdn_decode over an 8-bit cache: q, k [Bs, H, dk], v [Bs, H, dv]; S_cur and At_cur (float32,
+    updated in place); gates_in / gates_out [Bs, H, n_cap] by position in time.  The cache's
+    weight gains the gates.  Returns o [Bs, H, dv] float32."""
+    for t, name in ((beta, "beta"), (alpha, "alpha")):
+        _need_on(t, (cache.Bs, cache.H), torch.float32, cache.device, name)
+    return _decode8("hla_gdn_decode8", (beta, alpha), q, k, v, S_cur, At_cur, cache, gates_in, tau, o, gates_out, ws)
+
+
+def gdn2_decode8(q, k, v, a_decay, b_erase, w_write, S_cur, At_cur, cache, gates_in=None, tau=1e-3, o=None,
+                 gates_out=None, ws=None):
+    """gdn_decode8 under the Gated DeltaNet-2 recurrence (gates as for gdn2_decode)."""
+    for t, d, name in ((a_decay, cache.dk, "a_decay"), (b_erase, cache.dk, "b_erase"), (w_write, cache.dv, "w_write")):
+        _need_on(t, (cache.Bs, cache.H, d), torch.float32, cache.device, name)
+    return _decode8("hla_gdn2_decode8", (a_decay, b_erase, w_write), q, k, v, S_cur, At_cur, cache, gates_in, tau, o,
+                    gates_out, ws)
+
+
+def _decode8(fn, gates, q, k, v, S_cur, At_cur, c, gates_in, tau, o, gates_out, ws):
+    Bs, H, dk, dv, dev = c.Bs, c.H, c.dk, c.dv, c.device
+    dt = _dtype_code(k)
+    _need_on(q, (Bs, H, dk), k.dtype, dev, "q")
+    _need_on(k, (Bs, H, dk), k.dtype, dev, "k")
+    _need_on(v, (Bs, H, dv), k.dtype, dev, "v")
+    _need_on(S_cur, (Bs, H, dk, dv), torch.float32, dev, "S_cur")
+    _need_on(At_cur, (Bs, H, dk, dk), torch.float32, dev, "At_cur")
+    _need_on(gates_in, (Bs, H, c.n_cap), torch.float32, dev, "gates_in")
+    _need_on(gates_out, (Bs, H, c.n_cap), torch.float32, dev, "gates_out")
+    if o is None:
+        o = torch.empty((Bs, H, dv), dtype=torch.float32, device=dev)
+    _need_on(o, (Bs, H, dv), torch.float32, dev, "o")
+    if ws is None:
+        ws = _workspace(c._ws_bytes, dev)
+    elif ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    _call(fn, dev, c._ref, dt, _ptr(q), _ptr(k), _ptr(v), *(_ptr(g) for g in gates), _ptr(S_cur), _ptr(At_cur),
+          _ptr(gates_in), tau, _ptr(o), _ptr(gates_out), _ptr(ws), 0 if ws is None else ws.numel())
+    return o
+
+
+def gate_weights(gates, tau=1e-3, n_chunks=None, out=None):
+    """Weights that a prefill's gates [B, H, N, N] (as route_mix gives them) put on every chunk:
+    the sum over the later query chunks of the gates that reach tau.  n_chunks [B] int32: valid
+    chunks per batch row.  Returns [B, H, N] float32."""
+    B, H, N, _ = gates.shape
+    dev = gates.device
+    _need_on(gates, (B, H, N, N), torch.float32, dev, "gates")
+    _need_on(n_chunks, (B,), torch.int32, dev, "n_chunks")
+    if out is None:
+        out = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+    _need_on(out, (B, H, N), torch.float32, dev, "out")
+    _call("hla_gate_weights", dev, B, H, N, _ptr(gates), _ptr(n_chunks), tau, _ptr(out))
+    return out
+
+
+def evict_chunks(weight, count, budget, n_recent=0, order=None, out=None):
+    """Cut every row's chunks to `budget` by accumulated weight: of all but the n_recent newest
+    the lightest leave (of equal ones the older).  weight [Bs, H, n], count [Bs, H] int32, order
+    [Bs, H, n] int32 or None.  Returns (order, weight, count): the chunks that stay in time order,
+    then those that left; `out` may be the inputs."""
+    Bs, H, n = weight.shape
+    dev = weight.device
+    shapes = (((Bs, H, n), torch.int32, "order"), ((Bs, H, n), torch.float32, "weight"), ((Bs, H), torch.int32, "count"))
+    for t, (shape, dtype, name) in zip((order, weight, count), shapes):
+        _need_on(t, shape, dtype, dev, name)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=dtype, device=dev) for shape, dtype, _ in shapes)
+    for t, (shape, dtype, name) in zip(out, shapes):
+        _need_on(t, shape, dtype, dev, "out " + name)
+    _call("hla_evict_chunks", dev, Bs, H, n, _ptr(weight), _ptr(order), _ptr(count), budget, n_recent,
+          *(_ptr(t) for t in out))
+    return out
+
+
+def cache8_evict(cache, budget, n_recent=0):
+    """evict_chunks on the cache, in place: the freed slots are the next ones appended to."""
+    if cache.weight is None:
+        raise ValueError("the cache accumulates no weights")
+    evict_chunks(cache.weight, cache.count, budget, n_recent, order=cache.order,
+                 out=(cache.order, cache.weight, cache.count))
+
+
+def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
+    """What a decode needs after a routed prefill of T tokens (r: hla_prefill's result): the
+    complete chunks enter the cache, emptied first, and the rest of the prompt is the live chunk.
+    Where there are more than `budget` chunks (default and at most: the cache's capacity), those
+    stay that the prompt's own gates weigh most, and the n_recent newest.  Returns (S_cur,
+    At_cur), float32."""
+    At, Bc = r["At"], r["Bc"]
+    B, H, N, dk, _ = At.shape
+    dv, full = Bc.shape[-1], T // C
+    if N != math.ceil(T / C):
+        raise ValueError("T and C do not match the prefill's chunks")
+    keep = cache.n_cap if budget is None else min(budget, cache.n_cap)
+    weight = gate_weights(r["gates"], tau=tau)
+    count = torch.full((B, H), full, dtype=torch.int32, device=At.device)
+    order, weight, count = evict_chunks(weight, count, keep, min(n_recent, keep))
+    cache8_append(cache, At, Bc, r["reps"], src=order, n_new=count, weight_in=weight, reset=True, n=full)
+    if full < N:
+        return Bc[:, :, full].float().contiguous(), At[:, :, full].float().contiguous()
+    S = torch.zeros((B, H, dk, dv), dtype=torch.float32, device=At.device)
+    return S, torch.eye(dk, dtype=torch.float32, device=At.device).repeat(B, H, 1, 1)
 
 
 def timing_enable(on: bool = True) -> None:

@@ -334,6 +334,128 @@ hla_status_t hla_gdn2_decode(int64_t Bs, int64_t H, int32_t dk, int32_t dv, int3
                              hipStream_t stream);
 
 /*
+ * The chunk cache in 8 bits: what a decoding program keeps of the prefix, per (sequence,
+ * head), at about half the bytes of a bfloat16 cache, with a set of chunks of its own for
+ * every head.  [HLA] Methodology paragraphs 1 and 2 (each chunk's exact affine map, scored by
+ * its representatives).
+ *   maps   [Bs, H, n_cap, dk + dv, dk]  8 bits, math orientation: rows 0 .. dk-1 hold A - I,
+ *           rows dk .. dk+dv-1 hold B (S -> S A + B; A - I and not A, so that a chunk that
+ *           changes little costs little precision and a skipped one none).
+ *   reps   [Bs, H, n_cap, n_rep, dk]  8 bits: the representatives; NULL when n_rep is 0.
+ *   scale  [Bs, H, n_cap, 4]  float32: the factors of A - I, of B and of the
+ *           representatives, and 0.  The value of a stored number x is x * scale.
+ *   order  [Bs, H, n_cap]  int32: the slot of every position in time; a permutation of
+ *           0 .. n_cap-1, the positions from count on naming the free slots.  A slot out of
+ *           range is read as the last one.
+ *   count  [Bs, H]  int32: chunks held (positions 0 .. count-1), read as clamped to
+ *           0 .. n_cap.
+ *   weight [Bs, H, n_cap]  float32 by position: the sum of the gates that a chunk was read
+ *           with, each taken within [0, 1]; or NULL, then nothing is accumulated.
+ * Sizes: dk, dv in {64, 128}, 1 <= n_cap <= 1024, 0 <= n_rep <= 256.  maps, reps and scale are
+ * 16-byte aligned, the others 4-byte.  Slots that no position below count names may hold
+ * anything.  A call on a cache races with any other call that writes the same cache.
+ */
+typedef enum { HLA_CACHE_I8 = 0, HLA_CACHE_E4M3 = 1 } hla_cache8_format_t;
+typedef struct {
+  int64_t Bs, H;
+  int32_t dk, dv, n_cap, n_rep;
+  int32_t format; /* hla_cache8_format_t */
+  void* maps;
+  void* reps;
+  float* scale;
+  int32_t* order;
+  int32_t* count;
+  float* weight;
+} hla_cache8_t;
+
+/*
+ * hla_cache8_append -- quantise chunks and append them to the cache.
+ * Of each of X = A - I, X = B and X = the representatives of one chunk and head, with m the
+ * largest |X| and Q = 127 (int8) or 448 (e4m3): scale = m / Q, and X (Q / m) is rounded to the
+ * nearest stored value, ties to even; m < 2^-100 stores zeros with scale 0.  The inputs are
+ * finite.
+ *   At [Bs, H, ld_src, dk, dk], Bc [Bs, H, ld_src, dk, dv] (dtype): maps as
+ *           hla_chunk_transitions writes them, the first n_src of each row being complete
+ *           chunks (0 <= n_src <= ld_src; a partial last chunk is not appended); or with
+ *           n_src = ld_src = 1 the live chunk of a decode step (At_cur, S_cur).
+ *   reps    [Bs, ld_R, H, dk] (dtype): source chunk i's representatives are rows
+ *           [i n_rep, (i + 1) n_rep), ld_R >= n_src n_rep (hla_chunk_reps' output, or k with
+ *           n_rep = C); ignored when the cache holds none.
+ *   src     [Bs, H, ld_src] int32 or NULL: the source chunk of every appended one (clamped to
+ *           0 .. n_src-1; NULL: chunk i is source chunk i).
+ *   n_new   [Bs, H] int32 or NULL (n_src): chunks to append, clamped to 0 .. n_src and to the
+ *           room left; the chunks past the room are dropped.
+ *   weight_in [Bs, H, ld_src] float32 or NULL (zeros): the appended chunks' weights.
+ *   reset   : 1 = the cache is emptied first (count 0, slots in order, weights 0).
+ *   reset_live : 1 = the source maps of every chunk that was appended are set to A = I, B = 0
+ *           (a live chunk begins again); needs HLA_F32 and src = NULL, else HLA_ERR_UNSUPPORTED.
+ * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE, HLA_ERR_BAD_DTYPE (dtype, format),
+ *         HLA_ERR_ALIGN (At, Bc, reps 16 bytes), HLA_ERR_UNSUPPORTED, HLA_ERR_HIP.
+ */
+hla_status_t hla_cache8_append(const hla_cache8_t* c, int32_t dtype, int32_t n_src, int32_t ld_src,
+                               void* At, void* Bc, const void* reps, int64_t ld_R, const int32_t* src,
+                               const int32_t* n_new, const float* weight_in, int32_t reset,
+                               int32_t reset_live, hipStream_t stream);
+
+/*
+ * hla_gdn_decode8, hla_gdn2_decode8 -- hla_gdn_decode and hla_gdn2_decode over the 8-bit
+ * cache: the same live update, gates and composition, on the values the cache stands for
+ * (float32 accumulation; the stored numbers enter exactly).
+ *   q, k, v and the token gates, S_cur, At_cur (both required, updated in place), tau: as
+ *           there, with Bs, H, dk and dv of the cache and every head's own count and order.
+ *   gates_in  [Bs, H, n_cap] float32 by position or NULL (then n_rep >= 1).
+ *   gates_out [Bs, H, n_cap] float32 or NULL: every held position's gate, 0 behind them.
+ *   o         [Bs, H, dv] float32 out.
+ *   The cache is read; its weight (if any) gains every held position's gate after the
+ *   threshold.  A gate that is NaN is below every threshold.
+ *   ws, ws_bytes: workspace of at least hla_decode8_workspace_bytes() bytes, 16-byte aligned.
+ * Appending the live chunk is hla_cache8_append's (reset_live).
+ * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE, HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN,
+ *         HLA_ERR_WORKSPACE, HLA_ERR_HIP.
+ */
+hla_status_t hla_gdn_decode8(const hla_cache8_t* c, int32_t dtype, const void* q, const void* k,
+                             const void* v, const float* beta, const float* alpha, float* S_cur,
+                             float* At_cur, const float* gates_in, float tau, float* o,
+                             float* gates_out, void* ws, size_t ws_bytes, hipStream_t stream);
+hla_status_t hla_gdn2_decode8(const hla_cache8_t* c, int32_t dtype, const void* q, const void* k,
+                              const void* v, const float* a_decay, const float* b_erase,
+                              const float* w_write, float* S_cur, float* At_cur,
+                              const float* gates_in, float tau, float* o, float* gates_out, void* ws,
+                              size_t ws_bytes, hipStream_t stream);
+hla_status_t hla_decode8_workspace_bytes(const hla_cache8_t* c, size_t* out);
+
+/*
+ * hla_gate_weights -- the weight that a prefill's gates give every chunk: what a decode step's
+ * accumulation would have summed, over the prompt's own query chunks.
+ *     weight[b, h, j] = sum over j < i < n_b of g_ij [g_ij >= tau], g taken within [0, 1]
+ *   gates    [B, H, N, N] float32 as hla_route_mix writes them (entries j < i are read).
+ *   n_chunks [B] int32 or NULL (N): valid chunks n_b, clamped to 0 .. N.
+ *   weight   [B, H, N] float32 out (0 at and behind the last valid chunk).
+ * Sums are float32 in a fixed order.
+ * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE (sizes, NaN tau), HLA_ERR_ALIGN, HLA_ERR_HIP.
+ */
+hla_status_t hla_gate_weights(int64_t B, int64_t H, int32_t N, const float* gates, const int32_t* n_chunks,
+                              float tau, float* weight, hipStream_t stream);
+
+/*
+ * hla_evict_chunks -- cut every row's chunks to a budget by accumulated weight.
+ * With n_h = count (clamped to 0 .. n) and m = max(n_h - budget, 0): of the positions
+ * [0, n_h - n_recent) the m with the lowest weight leave (of equal weights the older first; NaN
+ * is below every number); the others keep their order in time.
+ *   weight [Bs, H, n], order [Bs, H, n] (NULL: position p is slot p), count [Bs, H]: as in the
+ *           cache, or of a prompt's chunks (hla_gate_weights), whose `order_out` is then the
+ *           src of hla_cache8_append.  1 <= n <= 16384; 0 <= n_recent <= budget.
+ *   order_out  : the slots that stay, in time order, then those that left, then (unmoved) the
+ *           positions from count on.   weight_out: likewise, 0 behind the chunks that stay.
+ *   count_out  : min(count, budget).
+ * Outputs may be the inputs of the same kind (in place); no other overlap.
+ * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE, HLA_ERR_ALIGN, HLA_ERR_HIP.
+ */
+hla_status_t hla_evict_chunks(int64_t Bs, int64_t H, int32_t n, const float* weight, const int32_t* order,
+                              const int32_t* count, int32_t budget, int32_t n_recent, int32_t* order_out,
+                              float* weight_out, int32_t* count_out, hipStream_t stream);
+
+/*
  * hla_compose_backward -- reverse of the gated composition of hla_route_mix.
  * [HLA] Methodology paragraphs 1, 3 and 4.  Query chunk i's routed state is the chain
  *     M_j = M_{j-1} + g_ij (At_j - I) M_{j-1} + g_ij Bc_j    over active j < i, M = S0 first,
