@@ -27,9 +27,10 @@ __device__ __forceinline__ int cache8_slot(const Cache8View& c, int64_t row, int
   return s < (unsigned)c.n_cap ? (int)s : c.n_cap - 1;
 }
 
-// The stored formats.  Quantising multiplies by top / max (rounded to nearest, ties to even)
-// so that the largest magnitude lands on `top`; a block whose largest magnitude is below
-// 2^-100 is stored as zeros with scale 0, since top / max would overflow.
+// The stored formats.  A block with largest magnitude m is multiplied by (1 / m) top and rounded
+// to the nearest stored value, ties to even, so that m lands on `top`; the scale is m (1 / top).
+// Each of the two factors is rounded twice, as written: what is stored depends on the last bit.
+// m < 2^-100 stores zeros with scale 0, since 1 / m would overflow.
 constexpr int kI8 = 0, kE4M3 = 1;
 constexpr float kCache8Tiny = 0x1p-100f;
 template <int FMT> struct Stored;
@@ -57,6 +58,13 @@ template <> struct Stored<kE4M3> {
     return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(cl(c), cl(d), w, true);
   }
 };
+
+template <int FMT> __device__ __forceinline__ float to_stored(float m) {
+  return m >= kCache8Tiny ? (1.f / m) * Stored<FMT>::top : 0.f;
+}
+template <int FMT> __device__ __forceinline__ float from_stored(float m) {
+  return m >= kCache8Tiny ? m * (1.f / Stored<FMT>::top) : 0.f;
+}
 
 struct Decode8Args {
   Cache8View c;

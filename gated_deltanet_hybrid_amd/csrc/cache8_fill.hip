@@ -115,8 +115,7 @@ __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
   rb.load(Bc);
   const float ma = block_max<NT>(ra.template largest<true>(), s_red);
   const float mb = block_max<NT>(rb.template largest<false>(), s_red);
-  constexpr float top = Stored<FMT>::top;
-  const float ia = ma >= kCache8Tiny ? top / ma : 0.f, ib = mb >= kCache8Tiny ? top / mb : 0.f;
+  const float ia = to_stored<FMT>(ma), ib = to_stored<FMT>(mb);
   ra.template store<true, FMT, LD>(s_img, ia);
   rb.template store<false, FMT, LD>(s_img + DK * LD, ib);
 
@@ -134,7 +133,7 @@ __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
       for (int e = 0; e < E; ++e) mr = fmaxf(mr, fabsf(f[e]));
     }
     mr = block_max<NT>(mr, s_red);
-    const float ir = mr >= kCache8Tiny ? top / mr : 0.f;
+    const float ir = to_stored<FMT>(mr);
     uint8_t* out = a.c.reps + slot * a.c.n_rep * DK;
     for (int u = tid; u < a.c.n_rep * CPR; u += NT) {
       const uint4 raw = *reinterpret_cast<const uint4*>(rep + (int64_t)(u / CPR) * a.H * DK + (u % CPR) * E);
@@ -153,8 +152,7 @@ __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
     maps[u] = make_uint4(p[0], p[1], p[2], p[3]);
   }
   if (tid == 0)
-    a.c.scale[slot] = make_float4(ma >= kCache8Tiny ? ma / top : 0.f, mb >= kCache8Tiny ? mb / top : 0.f,
-                                  mr >= kCache8Tiny ? mr / top : 0.f, 0.f);
+    a.c.scale[slot] = make_float4(from_stored<FMT>(ma), from_stored<FMT>(mb), from_stored<FMT>(mr), 0.f);
   if (a.reset_live) {
     reset_map<T, DK, NT>(At, DK, true);
     reset_map<T, DV, NT>(Bc, DK, false);

@@ -2,7 +2,7 @@
 
 The stored formats are stated by their value sets: int8 the integers -127 .. 127, e4m3 the
 numbers (-1)^s 2^(e-7) (1 + m/8) (e = 1 .. 15, without the NaN at e = 15, m = 7) and
-(-1)^s 2^-6 m/8.  A block is multiplied by top / max in float32 (the definition's own two
+(-1)^s 2^-6 m/8.  A block is multiplied by (1 / max) top in float32 (the definition's own
 roundings) and each product goes to the nearest value of the set, ties to the even code.
 """
 import numpy as np
@@ -24,15 +24,15 @@ def quantise(X, fmt):
     top = np.float32(TOP[fmt])
     if not m >= np.float32(2.0 ** -100):
         return np.zeros(X.shape), 0.0
-    y = (X * (top / m)).astype(np.float64)
+    y = (X * (np.float32(1) / m * top)).astype(np.float64)
     if fmt == "int8":
-        return np.clip(np.rint(y), -127, 127), float(m / top)
+        return np.clip(np.rint(y), -127, 127), float(m * (np.float32(1) / top))
     values = e4m3_values()
     mag = np.minimum(np.abs(y), values[-1])
     hi = np.clip(np.searchsorted(values, mag), 1, len(values) - 1)
     lo = hi - 1
     up = (mag - values[lo] > values[hi] - mag) | ((mag - values[lo] == values[hi] - mag) & (hi % 2 == 0))
-    return np.where(up, values[hi], values[lo]) * np.where(np.signbit(y), -1.0, 1.0), float(m / top)
+    return np.where(up, values[hi], values[lo]) * np.where(np.signbit(y), -1.0, 1.0), float(m * (np.float32(1) / top))
 
 
 def gate_weights(gates, tau, n):
