@@ -20,6 +20,22 @@ namespace {
 
 constexpr int kMaxCache = 1024;
 
+// Loads and stores of what a step touches once and the cache hierarchy cannot hold.
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ float4 load_once(const float* p) {
+  const f32x4v v = __builtin_nontemporal_load(reinterpret_cast<const f32x4v*>(p));
+  return make_float4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ void store_once(float* p, float4 x) {
+  const f32x4v v = {x.x, x.y, x.z, x.w};
+  __builtin_nontemporal_store(v, reinterpret_cast<f32x4v*>(p));
+}
+
 // One read + write pass over a live [DK][W] matrix: mat <- diag(a) mat - e u^T + k w^T with
 // u = (a o k)^T mat, and out = q^T mat (after) = (a o q)^T mat - (q . e) u + (q . k) w.
 // LDS rows: ka = a o k, qa = a o q, a, e, k; w null for the transition.
@@ -36,9 +52,10 @@ __device__ __forceinline__ void live_update(float* mat, const LiveRows& r, const
                                             float* s_u, float* out) {
   constexpr int CPR = W / 4, RPP = NT / CPR, NP = DK / RPP;
   const int tid = threadIdx.x, col = (tid % CPR) * 4, r0 = tid / CPR;
-  float4 m[NP], pu = make_float4(0.f, 0.f, 0.f, 0.f), pz = pu;
+  float4 m[NP];
 #pragma unroll
-  for (int p = 0; p < NP; ++p) m[p] = *reinterpret_cast<const float4*>(mat + (p * RPP + r0) * W + col);
+  for (int p = 0; p < NP; ++p) m[p] = load_once(mat + (p * RPP + r0) * W + col);
+  float4 pu = make_float4(0.f, 0.f, 0.f, 0.f), pz = pu;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const float kr = r.ka[p * RPP + r0], qr = r.qa[p * RPP + r0];
@@ -66,39 +83,181 @@ __device__ __forceinline__ void live_update(float* mat, const LiveRows& r, const
     n.y = ar * m[p].y - er * uu.y + kr * ww.y;
     n.z = ar * m[p].z - er * uu.z + kr * ww.z;
     n.w = ar * m[p].w - er * uu.w + kr * ww.w;
-    *reinterpret_cast<float4*>(mat + i * W + col) = n;
+    store_once(mat + i * W + col, n);
   }
   __syncthreads();
 }
 
-// Dot product of a stored row of DK bytes with DK floats in LDS.
-template <int FMT, int DK>
-__device__ __forceinline__ float row_dot(const uint8_t* row, const float* s_x) {
-  float acc = 0.f;
+// ---- products of stored rows with a float32 vector on the matrix cores
+//
+// The vector is written as four terms that stand in four columns of the B operand; a 16-row
+// product gives every column's sum, and the four sums are added at the end.  The vector units
+// would spend a conversion, a multiply-add and a share of a cross-lane sum on every stored
+// number; here they see only the sums.
+//   int8: the vector as 32-bit fixed point, x = F 2^(e-30) with |x| <= 2^e, and F's four signed
+//         bytes as terms.  The stored bytes enter the int8 product as they are, and its int32
+//         sums are exact; what is rounded is x, to 2^-30 of 2^e.
+//   e4m3: four bf16 terms, each the rounding of what the ones before left (three already hold a
+//         float32), stored numbers converted to bf16 exactly, float32 sums.
+// In the product's layout lane l holds row l % 16 and the 16 stored bytes from 64 p + 16 (l / 16)
+// on for each p; column l % 16 is term l % 4, and element i of the sums is row 4 (l / 16) + i.
+// Loaded like that, 16 neighbouring lanes would touch 16 cache lines (measured: 27 GB/s a CU).
+// So a wave loads its 16 rows as they lie, 1 KiB an instruction, and turns them in its own piece
+// of LDS, whose 16-byte pieces are swizzled by row so that neither side has bank conflicts.
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
+typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
+
+template <int FMT, int DK> struct Operand;
+template <int DK> struct Operand<kI8, DK> {
+  static constexpr bool kFixed = true;
+  uint8_t t[4][DK + 16];  // 16 bytes of padding: the four terms start in different banks
+  using Frag = i32x4;
+  // factor of the lane's term in the sums
+  __device__ __forceinline__ static float term_unit() {
+    return __builtin_bit_cast(float, (unsigned)(127 + 8 * (lane_id() & 3)) << 23);
+  }
+  // Rows row0 + 4 g .. of x, the same in all 16 lanes of group g; enc = 2^(30-e).
+  __device__ __forceinline__ void put(int row0, const float (&x)[4], float enc) {
+    unsigned f[4];
 #pragma unroll
-  for (int c = 0; c < DK / 16; ++c) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(row + 16 * c);
-    const unsigned w[4] = {raw.x, raw.y, raw.z, raw.w};
+    for (int i = 0; i < 4; ++i)  // F = sum of its bytes b_3 (signed), b_2 .. b_0 (less 128) 256^i
+      f[i] = ((unsigned)(int)(x[i] * enc) + 0x00808080u) ^ 0x00808080u;
+    const unsigned term = lane_id() & 3, sel = (4u + term) << 8 | term;  // byte `term` of two words
+    const unsigned lo = __builtin_amdgcn_perm(f[1], f[0], sel), hi = __builtin_amdgcn_perm(f[3], f[2], sel);
+    if ((lane_id() & 15) < 4)
+      *reinterpret_cast<unsigned*>(&t[term][row0 + (lane_id() >> 4) * 4]) = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+  }
+  __device__ __forceinline__ Frag get(int p) const {
+    return *reinterpret_cast<const i32x4*>(&t[lane_id() & 3][p * 64 + (lane_id() >> 4) * 16]);
+  }
+  using Acc = i32x4;
+  __device__ __forceinline__ static Acc step(const uint4& raw, const Frag& x, Acc acc) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, raw), x, acc, 0, 0, 0);
+  }
+};
+template <int DK> struct Operand<kE4M3, DK> {
+  static constexpr bool kFixed = false;
+  bf16 t[4][DK + 8];
+  struct Frag { bf16x8 lo, hi; };
+  __device__ __forceinline__ static float term_unit() { return 1.f; }
+  __device__ __forceinline__ void put(int row0, const float (&x)[4], float) {
+    const int term = lane_id() & 3;
+    bf16x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float f[4];
-      Stored<FMT>::unpack(w[i], f);
-      const float4 x = *reinterpret_cast<const float4*>(s_x + 16 * c + 4 * i);
-      acc += f[0] * x.x + f[1] * x.y + f[2] * x.z + f[3] * x.w;
+      float r = x[i];
+#pragma unroll
+      for (int s = 0; s < 3; ++s) r = s < term ? r - (float)(bf16)r : r;
+      v[i] = (bf16)r;
     }
+    if ((lane_id() & 15) < 4) *reinterpret_cast<bf16x4*>(&t[term][row0 + (lane_id() >> 4) * 4]) = v;
   }
-  return acc;
+  __device__ __forceinline__ Frag get(int p) const {
+    const bf16* at = &t[lane_id() & 3][p * 64 + (lane_id() >> 4) * 16];
+    return {*reinterpret_cast<const bf16x8*>(at), *reinterpret_cast<const bf16x8*>(at + 8)};
+  }
+  using Acc = f32x4;
+  __device__ __forceinline__ static Acc step(const uint4& raw, const Frag& x, Acc acc) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_frag(raw.x, raw.y), x.lo, acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_frag(raw.z, raw.w), x.hi, acc, 0, 0, 0);
+  }
+};
+
+// Sum of the four terms' shares a * unit.  The product is rounded on its own: fused into one of
+// the additions it would leave the four lanes with different last bits, and terms split from
+// different sums do not add up.
+__device__ __forceinline__ float terms_sum(float a, float unit) {
+#pragma clang fp contract(off)
+  const float x = a * unit;
+  return group_sum<4>(x);
 }
 
-template <int FMT, class T, int DK, int DV>
-__global__ __launch_bounds__(256) void decode8_kernel(Decode8Args a) {
-  constexpr int NT = 256, WMAX = DV > DK ? DV : DK;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t row = blockIdx.x;
-  __shared__ float s_q[DK], s_k[DK], s_a[DK], s_e[DK], s_ka[DK], s_qa[DK], s_w[DV];
-  __shared__ float s_u[WMAX], s_o[DV], s_z[DK], s_red[2][NT * 4];
-  __shared__ float s_dot[2], s_g[kMaxCache];
+template <int DK> struct Turn {
+  static constexpr int KP = DK / 64, PPR = DK / 16;  // 16-byte pieces to a row
+  uint4 t[16 * PPR];
+  __device__ __forceinline__ static int piece(int row, int c) { return row * PPR + (c ^ (KP == 2 ? row & 7 : row >> 1 & 3)); }
+  // raw[i]: piece l % PPR of row i 64 / PPR + l / PPR; frag[p] as the product takes it
+  __device__ __forceinline__ void turn(const uint4 (&raw)[KP], uint4 (&frag)[KP]) {
+    const int l = lane_id();
+#pragma unroll
+    for (int i = 0; i < KP; ++i) t[piece(i * (64 / PPR) + l / PPR, l % PPR)] = raw[i];
+    __builtin_amdgcn_wave_barrier();  // the LDS serves a wave's requests in order
+#pragma unroll
+    for (int p = 0; p < KP; ++p) frag[p] = t[piece(l & 15, 4 * p + (l >> 4))];
+    __builtin_amdgcn_wave_barrier();
+  }
+  // one k half (64 bytes) of 16 rows: raw is piece 4 half + l % 4 of row l / 4
+  __device__ __forceinline__ uint4 turn_half(const uint4& raw) {
+    const int l = lane_id();
+    t[(l >> 2) * 4 + ((l & 3) ^ (l >> 3 & 3))] = raw;
+    __builtin_amdgcn_wave_barrier();
+    const uint4 f = t[(l & 15) * 4 + ((l >> 4) ^ (l >> 1 & 3))];
+    __builtin_amdgcn_wave_barrier();
+    return f;
+  }
+};
 
+// 2^(30-e) for the least e in reach with bound < 2^e, and its counterpart 2^(e-30) = 1 / enc.
+struct Fixed { float enc, dec; };
+__device__ __forceinline__ Fixed fixed_for(float bound) {
+  int b = (int)(__builtin_bit_cast(unsigned, bound) >> 23) & 0xff;
+  b = b < 30 ? 30 : (b > 253 ? 253 : b);
+  return {__builtin_bit_cast(float, (unsigned)(283 - b) << 23), __builtin_bit_cast(float, (unsigned)(b - 29) << 23)};
+}
+// Magnitudes compare as their bits, and what is not finite is above every number.
+constexpr unsigned kInf = 0x7f800000u;
+__device__ __forceinline__ unsigned mag(float x) { return __builtin_bit_cast(unsigned, x) & 0x7fffffffu; }
+__device__ __forceinline__ unsigned max_u(unsigned a, unsigned b) { return a > b ? a : b; }
+// Largest over the lanes 16, 32 and 48 apart (the lanes of one 16-lane row hold the same value).
+__device__ __forceinline__ unsigned rows_max(unsigned x) {
+  auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = max_u(r[0], r[1]);
+  r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return max_u(r[0], r[1]);
+}
+
+// One workgroup per (sequence, head), a wave for every 16 rows of E: the live update, the gates
+// (16 representatives a product, their scores through LDS in blocks of whole chunks), then the
+// chain.  In the chain wave w owns z's rows 16 w .. and its share of o's; a chunk's new z becomes
+// terms in the other of two LDS buffers, so one barrier a chunk is enough, and the raw bytes of
+// the next P chunks are on their way to registers meanwhile.
+// int8 needs a bound of |z| before z is known to every wave.  The largest |z| is exchanged with
+// the terms, and the next z is at most (1 + |ghat sA| 128 dk) times that; where this factor is
+// over 2^7 (a term would then hold fewer than 23 bits of the largest |z|), the waves exchange the
+// new maximum first, at the price of a second barrier.
+template <int FMT, class T, int DK, int DV>
+__global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
+  using Op = Operand<FMT, DK>;
+  constexpr int NW = DK / 16, NT = NW * 64, WMAX = DV > DK ? DV : DK, P = 4, KP = DK / 64, PPR = DK / 16;
+  // o's tiles: OT of them to a wave, or where dv < dk one k half of a tile to a wave
+  constexpr bool kHalf = DV < DK;
+  constexpr int OT = kHalf ? 1 : DV / DK, OP = kHalf ? 1 : KP;
+  constexpr int kScores = 1024;  // scores held at a time (n_rep <= 256: at least four chunks)
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4;
+  const int64_t row = blockIdx.x;
+  __shared__ __align__(16) float s_q[DK], s_k[DK], s_a[DK], s_e[DK], s_ka[DK], s_qa[DK], s_w[DV];
+  __shared__ __align__(16) float s_u[WMAX], s_o[2][DV], s_z[DK];
+  constexpr int kRed = NT * 4;
+  __shared__ __align__(16) float s_red[2 * kRed > 3 * kMaxCache ? 2 * kRed : 3 * kMaxCache];
+  __shared__ __align__(16) unsigned s_max[2][8];
+  __shared__ __align__(16) Op s_x[2];
+  __shared__ __align__(16) float s_score[kScores];
+  __shared__ float s_dot[2];
+  // by position: slot, scale of A - I and B, and the scale of the representatives, then the gate
+  __shared__ int s_slot[kMaxCache];
+  __shared__ float s_sa[kMaxCache], s_sb[kMaxCache], s_g[kMaxCache];
+  __shared__ unsigned long long s_on[kMaxCache / 64];
+  __shared__ __align__(16) Turn<DK> s_turn[NW][kHalf ? 2 : 1 + OT];  // each wave's own
+
+  const int n = cache8_count(a.c, row), n_cap = a.c.n_cap, n_rep = a.c.n_rep;
+  for (int j = tid; j < n; j += NT) {
+    const int slot = cache8_slot(a.c, row, j);
+    const float4 sc = a.c.scale[row * n_cap + slot];
+    s_slot[j] = slot;
+    s_sa[j] = sc.x;
+    s_sb[j] = sc.y;
+    s_g[j] = sc.z;
+  }
   if (tid < DK) {
     const float qv = to_f<T>(reinterpret_cast<const T*>(a.q)[row * DK + tid]);
     const float kv = to_f<T>(reinterpret_cast<const T*>(a.k)[row * DK + tid]);
@@ -116,63 +275,246 @@ __global__ __launch_bounds__(256) void decode8_kernel(Decode8Args a) {
     const float* s = w ? s_e : s_k;
     float x = 0.f;
     for (int i = lane; i < DK; i += 64) x += s_q[i] * s[i];
-    x = wave_sum(x);
+    x = wave_sum_valu(x);
     if (lane == 0) s_dot[w] = x;
   }
+  // A vector that all waves can see becomes an operand; returns the factor of its sums (NaN where
+  // a value is not finite, which fixed point cannot hold).
+  auto encode = [&](Op& op, const float* src) {
+    float m = 0.f, bad = 0.f;
+    for (int i = lane; i < DK; i += 64) {
+      m = fmaxf(m, fabsf(src[i]));
+      bad += src[i] * 0.f;
+    }
+    const Fixed fx = fixed_for(wave_max_valu(m));
+    const float4 x = *reinterpret_cast<const float4*>(src + 16 * w + g * 4);
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    op.put(16 * w, v, fx.enc);
+    return (Op::kFixed ? fx.dec : 1.f) + wave_sum_valu(bad);
+  };
+  const float q_unit = encode(s_x[1], s_q) * Op::term_unit();
   __syncthreads();
   const LiveRows lr{s_ka, s_qa, s_a, s_e, s_k, s_dot[1], s_dot[0]};
-  live_update<DK, DV, NT>(a.S_cur + row * DK * DV, lr, s_w, s_red[0], s_red[1], s_u, s_o);
-  live_update<DK, DK, NT>(a.At_cur + row * DK * DK, lr, nullptr, s_red[0], s_red[1], s_u, s_z);
+  live_update<DK, DV, NT>(a.S_cur + row * DK * DV, lr, s_w, s_red, s_red + kRed, s_u, s_o[0]);
+  live_update<DK, DK, NT>(a.At_cur + row * DK * DK, lr, nullptr, s_red, s_red + kRed, s_u, s_z);
 
-  const int n = cache8_count(a.c, row), n_cap = a.c.n_cap, n_rep = a.c.n_rep;
-  for (int j = w; j < n; j += NT / 64) {
-    float g;
-    if (a.gates_in) {
-      g = a.gates_in[row * n_cap + j];
-    } else {
-      const int64_t slot = row * n_cap + cache8_slot(a.c, row, j);
-      const float sc = a.c.scale[slot].z / sqrtf((float)DK);
-      float m = -INFINITY, sum = 0.f;
-      for (int r = lane; r < n_rep; r += 64) {
-        const float s = row_dot<FMT, DK>(a.c.reps + (slot * n_rep + r) * DK, s_q) * sc;
-        const float mn = fmaxf(m, s);
-        sum = (m > -INFINITY ? sum * expf(m - mn) : 0.f) + expf(s - mn);
-        m = mn;
+  // ---- gates
+  auto take_gate = [&](int j, float x) {
+    const float gh = x >= a.tau ? x : 0.f;
+    s_g[j] = gh;
+    if (a.gates_out) a.gates_out[row * n_cap + j] = x;
+    if (a.c.weight) a.c.weight[row * n_cap + j] += gate_mass(gh);
+  };
+  if (a.gates_in) {
+    for (int j = tid; j < n; j += NT) take_gate(j, a.gates_in[row * n_cap + j]);
+  } else {
+    typename Op::Frag qf[KP];
+#pragma unroll
+    for (int p = 0; p < KP; ++p) qf[p] = s_x[1].get(p);
+    const int per = kScores / n_rep;  // chunks a block of scores holds
+    const unsigned inv = ((1u << 20) + n_rep - 1) / n_rep;  // r / n_rep = r inv >> 20 for r < 1024, n_rep <= 256
+    const float unit = 1.f / sqrtf((float)DK);
+    for (int j0 = 0; j0 < n; j0 += per) {
+      const int nj = n - j0 < per ? n - j0 : per, rows = nj * n_rep;
+      for (int r0 = w * 16; r0 < rows; r0 += NW * 16) {
+        uint4 raw[KP], frag[KP];
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+          const int r = r0 + i * 8 + lane / PPR < rows ? r0 + i * 8 + lane / PPR : rows - 1;
+          const int jj = (int)((unsigned)r * inv >> 20);
+          const int64_t slot = row * n_cap + s_slot[j0 + jj];
+          raw[i] = *reinterpret_cast<const uint4*>(a.c.reps + (slot * n_rep + (r - jj * n_rep)) * DK + lane % PPR * 16);
+        }
+        s_turn[w][0].turn(raw, frag);
+        typename Op::Acc acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < KP; ++p) acc = Op::step(frag[p], qf[p], acc);
+        float s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = terms_sum((float)acc[i], q_unit);
+        if ((lane & 15) == 0) *reinterpret_cast<float4*>(s_score + r0 + g * 4) = make_float4(s[0], s[1], s[2], s[3]);
       }
-      const float top = wave_max(m);
-      sum = wave_sum(m > -INFINITY ? sum * expf(m - top) : 0.f);
-      g = 1.f / (1.f + expf(-(top + logf(sum / (float)n_rep))));
-    }
-    if (lane == 0) {
-      const float gh = g >= a.tau ? g : 0.f;
-      s_g[j] = gh;
-      if (a.gates_out) a.gates_out[row * n_cap + j] = g;
-      if (a.c.weight) a.c.weight[row * n_cap + j] += gate_mass(gh);
+      __syncthreads();
+      // eight lanes a chunk: the largest score, then the mean of the exponentials
+      for (int jj = tid >> 3; jj < nj; jj += NT / 8) {
+        const float sc = s_g[j0 + jj] * unit;
+        const float* score = s_score + jj * n_rep;
+        float m = -INFINITY, sum = 0.f;
+        for (int r = tid & 7; r < n_rep; r += 8) m = fmaxf(m, score[r] * sc);
+        m = fmaxf(m, dpp_f<0xB1>(m));
+        m = fmaxf(m, dpp_f<0x4E>(m));
+        m = fmaxf(m, dpp_f<0x141>(m));
+        for (int r = tid & 7; r < n_rep; r += 8) sum += expf(score[r] * sc - m);
+        sum = group_sum<8>(sum);
+        if ((tid & 7) == 0) take_gate(j0 + jj, 1.f / (1.f + expf(-(m + logf(sum / (float)n_rep)))));
+      }
+      __syncthreads();
     }
   }
   if (a.gates_out)
     for (int j = n + tid; j < n_cap; j += NT) a.gates_out[row * n_cap + j] = 0.f;
   __syncthreads();
+  for (int i = w; i < kMaxCache / 64; i += NW) {
+    const int j = 64 * i + lane;
+    const unsigned long long on = __ballot(j < n && s_g[j] != 0.f);
+    if (lane == 0) s_on[i] = on;
+  }
+  float unit = encode(s_x[0], s_z);  // 2^(e-30) of the operand in use
+  float z[4], o[OT][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = s_z[16 * w + g * 4 + i];
+#pragma unroll
+  for (int t = 0; t < OT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+  auto share_max = [&](int buf) {
+    const unsigned m = rows_max(max_u(max_u(mag(z[0]), mag(z[1])), max_u(mag(z[2]), mag(z[3]))));
+    if (lane == 0) s_max[buf][w] = m;
+  };
+  auto read_max = [&](int buf) {
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < NW; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(&s_max[buf][i]);
+      m = max_u(max_u(m, max_u(x.x, x.y)), max_u(x.z, x.w));
+    }
+    return m;
+  };
+  if (Op::kFixed) share_max(0);
+  __syncthreads();
+  // the chunks in use, newest first: slot, ghat sA, ghat sB (in the live update's LDS)
+  int* l_slot = reinterpret_cast<int*>(s_red);
+  float *l_ca = s_red + kMaxCache, *l_cb = l_ca + kMaxCache;
+  int used = 0;
+  for (int i = 0; i < (n + 63) / 64; ++i) used += __builtin_popcountll(s_on[i]);
+  used = __builtin_amdgcn_readfirstlane(used);
+  for (int j = tid; j < n; j += NT) {
+    const unsigned long long on = s_on[j >> 6];
+    if (!(on >> (j & 63) & 1)) continue;
+    int at = __builtin_popcountll(on >> (j & 63)) - 1;
+    for (int i = (j >> 6) + 1; i < (n + 63) / 64; ++i) at += __builtin_popcountll(s_on[i]);
+    l_slot[at] = s_slot[j];
+    l_ca[at] = s_g[j] * s_sa[j];
+    l_cb[at] = s_g[j] * s_sb[j];
+  }
+  __syncthreads();
 
-  for (int j = n - 1; j >= 0; --j) {
-    const float g = s_g[j];
-    if (g == 0.f) continue;
-    const int64_t slot = row * n_cap + cache8_slot(a.c, row, j);
-    const float4 sc = a.c.scale[slot];
-    float d = 0.f;
-    if (tid < DK + DV) d = row_dot<FMT, DK>(a.c.maps + (slot * (DK + DV) + tid) * DK, s_z);
-    __syncthreads();
-    if (tid < DK) s_z[tid] += g * sc.x * d;
-    else if (tid < DK + DV) s_o[tid - DK] += g * sc.y * d;
+  // ---- chain
+  struct Raw { uint4 z[KP], o[OT][OP]; };
+  const uint8_t* base = a.c.maps + row * n_cap * (int64_t)((DK + DV) * DK);
+  const unsigned at_z = w * 16 * DK + lane * 16;
+  const unsigned at_o = DK * DK + (kHalf ? ((w >> 1) * 16 + lane / 4) * DK + (w & 1) * 64 + lane % 4 * 16
+                                         : OT * w * 16 * DK + lane * 16);
+  auto load = [&](Raw& r, int slot) {
+    const uint8_t* m = base + (int64_t)__builtin_amdgcn_readfirstlane(slot) * ((DK + DV) * DK);
+#pragma unroll
+    for (int p = 0; p < KP; ++p) r.z[p] = load_once(m + (at_z + p * 1024));
+#pragma unroll
+    for (int t = 0; t < OT; ++t)
+#pragma unroll
+      for (int p = 0; p < OP; ++p) r.o[t][p] = load_once(m + (at_o + t * 16 * DK + p * 1024));
+  };
+  const float tu = Op::term_unit();
+  Raw frag;  // the chunk in work, in the products' layout
+  auto turn = [&](const Raw& r) {
+    s_turn[w][0].turn(r.z, frag.z);
+    if constexpr (kHalf) {
+      frag.o[0][0] = s_turn[w][1].turn_half(r.o[0][0]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < OT; ++t) s_turn[w][1 + t].turn(r.o[t], frag.o[t]);
+    }
+  };
+  int buf = 0;
+  auto process = [&](int it) {
+    const float ca = l_ca[it], cb = l_cb[it];
+    typename Op::Frag x[KP], xo;
+#pragma unroll
+    for (int p = 0; p < KP; ++p) x[p] = s_x[buf].get(p);
+    if constexpr (kHalf) xo = s_x[buf].get(w & 1);
+    float us = unit * tu, bound = 0.f;
+    if constexpr (Op::kFixed) {
+      const unsigned m = read_max(buf);
+      us = m >= kInf ? __builtin_nanf("") : us;  // a z that is not finite makes NaN of all behind it
+      bound = __builtin_bit_cast(float, m);
+    }
+    buf ^= 1;
+    typename Op::Acc acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int p = 0; p < KP; ++p) acc = Op::step(frag.z[p], x[p], acc);
+    const float cz = ca * us;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] += terms_sum((float)acc[i], cz);
+    Fixed fx{1.f, 1.f};
+    if constexpr (Op::kFixed) {
+      const float factor = 1.f + fabsf(ca) * (128.f * DK);
+      share_max(buf);
+      if (factor <= 128.f) {
+        fx = fixed_for(bound * factor);
+      } else {
+        __syncthreads();
+        fx = fixed_for(__builtin_bit_cast(float, read_max(buf)));
+      }
+    }
+    s_x[buf].put(16 * w, z, fx.enc);
+    const float co = cb * us;
+#pragma unroll
+    for (int t = 0; t < OT; ++t) {  // each lane keeps its own term's share until the end
+      typename Op::Acc ao = {0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < OP; ++p) ao = Op::step(frag.o[t][p], kHalf ? xo : x[p], ao);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[t][i] += co * (float)ao[i];
+    }
+    if constexpr (Op::kFixed) unit = fx.dec;
+  };
+  if (used > 0) {
+    Raw ring[P];
+    load(frag, l_slot[0]);
+#pragma unroll
+    for (int i = 0; i < P; ++i) load(ring[i], l_slot[i + 1 < used ? i + 1 : used - 1]);
+    {
+      const Raw first = frag;
+      turn(first);
+    }
+    // The chunk behind the one in work is turned, and the one P behind that asked for, on the way:
+    // past the end the last one again, since a load under a condition would make every wait for a
+    // load one for all of them.
+    for (int it = 0; it < used; it += P)
+      static_for<0, P>([&](auto I) {
+        const int slot = l_slot[it + I + 1 + P < used ? it + I + 1 + P : used - 1];
+        if (it + I < used) process(it + I);
+        turn(ring[I]);
+        load(ring[I], slot);
+        __syncthreads();
+      });
+  }
+  // o: live part + the chain's, whose two k halves (dv < dk) meet in LDS
+  float sum[OT][4];
+#pragma unroll
+  for (int t = 0; t < OT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[t][i] = group_sum<4>(o[t][i]);
+  if constexpr (kHalf) {
+    if ((w & 1) && (lane & 15) == 0)
+      *reinterpret_cast<float4*>(&s_o[1][(w >> 1) * 16 + g * 4]) = make_float4(sum[0][0], sum[0][1], sum[0][2], sum[0][3]);
     __syncthreads();
   }
-  if (tid < DV) a.o[row * DV + tid] = s_o[tid];
+  if ((lane & 15) == 0 && !(kHalf && (w & 1))) {
+#pragma unroll
+    for (int t = 0; t < OT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = (kHalf ? w >> 1 : OT * w + t) * 16 + g * 4 + i;
+        a.o[row * DV + c] = s_o[0][c] + sum[t][i] + (kHalf ? s_o[1][c] : 0.f);
+      }
+  }
 }
 
 template <int FMT, class T, int DK, int DV>
 hipError_t run_decode8(const Decode8Args& a, hipStream_t s) {
   TimedLaunch tl(HLA_KERNEL_DECODE, s);
-  hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV>), dim3((unsigned)a.c.rows), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV>), dim3((unsigned)a.c.rows), dim3(DK * 4), 0, s, a);
   return hipGetLastError();
 }
 template <int FMT, class T>

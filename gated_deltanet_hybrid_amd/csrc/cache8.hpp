@@ -59,6 +59,15 @@ template <> struct Stored<kE4M3> {
   }
 };
 
+// Eight e4m3 numbers (two words) as bf16, exactly.
+__device__ __forceinline__ bf16x8 e4m3_frag(unsigned w0, unsigned w1) {
+  return __builtin_bit_cast(
+      bf16x8, make_uint4(__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, false)),
+                         __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, true)),
+                         __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, false)),
+                         __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, true))));
+}
+
 template <int FMT> __device__ __forceinline__ float to_stored(float m) {
   return m >= kCache8Tiny ? (1.f / m) * Stored<FMT>::top : 0.f;
 }
