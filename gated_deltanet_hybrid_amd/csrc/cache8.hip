@@ -120,12 +120,13 @@ template <int DK> struct Operand<kI8, DK> {
   __device__ __forceinline__ void put(int row0, const float (&x)[4], float enc) {
     unsigned f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // F = sum of its bytes b_3 (signed), b_2 .. b_0 (less 128) 256^i
-      f[i] = ((unsigned)(int)(x[i] * enc) + 0x00808080u) ^ 0x00808080u;
+    for (int i = 0; i < 4; ++i)  // F's bytes b_3 (signed) and b_2 .. b_0, less 128 each: F = sum b_i 256^i
+      f[i] = (unsigned)(int)(x[i] * enc) + 0x00808080u;
     const unsigned term = lane_id() & 3, sel = (4u + term) << 8 | term;  // byte `term` of two words
     const unsigned lo = __builtin_amdgcn_perm(f[1], f[0], sel), hi = __builtin_amdgcn_perm(f[3], f[2], sel);
-    if ((lane_id() & 15) < 4)
-      *reinterpret_cast<unsigned*>(&t[term][row0 + (lane_id() >> 4) * 4]) = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+    // four lanes of a group have the same term and write the same word
+    *reinterpret_cast<unsigned*>(&t[term][row0 + (lane_id() >> 4) * 4]) =
+        __builtin_amdgcn_perm(hi, lo, 0x05040100u) ^ (term == 3 ? 0u : 0x80808080u);
   }
   __device__ __forceinline__ Frag get(int p) const {
     return *reinterpret_cast<const i32x4*>(&t[lane_id() & 3][p * 64 + (lane_id() >> 4) * 16]);
@@ -150,7 +151,7 @@ template <int DK> struct Operand<kE4M3, DK> {
       for (int s = 0; s < 3; ++s) r = s < term ? r - (float)(bf16)r : r;
       v[i] = (bf16)r;
     }
-    if ((lane_id() & 15) < 4) *reinterpret_cast<bf16x4*>(&t[term][row0 + (lane_id() >> 4) * 4]) = v;
+    *reinterpret_cast<bf16x4*>(&t[term][row0 + (lane_id() >> 4) * 4]) = v;  // (the same from four lanes)
   }
   __device__ __forceinline__ Frag get(int p) const {
     const bf16* at = &t[lane_id() & 3][p * 64 + (lane_id() >> 4) * 16];
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
     for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
   auto share_max = [&](int buf) {
     const unsigned m = rows_max(max_u(max_u(mag(z[0]), mag(z[1])), max_u(mag(z[2]), mag(z[3]))));
-    if (lane == 0) s_max[buf][w] = m;
+    s_max[buf][w] = m;  // the same from every lane
   };
   auto read_max = [&](int buf) {
     unsigned m = 0;
@@ -426,8 +427,12 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
     }
   };
   int buf = 0;
-  auto process = [&](int it) {
-    const float ca = l_ca[it], cb = l_cb[it];
+  // Chunk `it`.  The products come first; then the chunk behind (`ring`) is turned and the one P
+  // behind that asked for, and the LDS and memory work on those while z is brought up to date.
+  auto process = [&](int it, Raw& ring) {
+    const bool live = it < used;
+    const float ca = live ? l_ca[it] : 0.f, cb = live ? l_cb[it] : 0.f;
+    const int slot = l_slot[it + 1 + P < used ? it + 1 + P : used - 1];
     typename Op::Frag x[KP], xo;
 #pragma unroll
     for (int p = 0; p < KP; ++p) x[p] = s_x[buf].get(p);
@@ -439,10 +444,18 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
       bound = __builtin_bit_cast(float, m);
     }
     buf ^= 1;
-    typename Op::Acc acc = {0, 0, 0, 0};
+    typename Op::Acc acc = {0, 0, 0, 0}, ao[OT];
 #pragma unroll
     for (int p = 0; p < KP; ++p) acc = Op::step(frag.z[p], x[p], acc);
-    const float cz = ca * us;
+#pragma unroll
+    for (int t = 0; t < OT; ++t) {
+      ao[t] = typename Op::Acc{0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < OP; ++p) ao[t] = Op::step(frag.o[t][p], kHalf ? xo : x[p], ao[t]);
+    }
+    turn(ring);
+    load(ring, slot);
+    const float cz = ca * us, co = cb * us;
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] += terms_sum((float)acc[i], cz);
     Fixed fx{1.f, 1.f};
@@ -455,18 +468,15 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
         __syncthreads();
         fx = fixed_for(__builtin_bit_cast(float, read_max(buf)));
       }
+      unit = fx.dec;
     }
     s_x[buf].put(16 * w, z, fx.enc);
-    const float co = cb * us;
+    if (live)
 #pragma unroll
-    for (int t = 0; t < OT; ++t) {  // each lane keeps its own term's share until the end
-      typename Op::Acc ao = {0, 0, 0, 0};
+      for (int t = 0; t < OT; ++t)  // each lane keeps its own term's share until the end
 #pragma unroll
-      for (int p = 0; p < OP; ++p) ao = Op::step(frag.o[t][p], kHalf ? xo : x[p], ao);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[t][i] += co * (float)ao[i];
-    }
-    if constexpr (Op::kFixed) unit = fx.dec;
+        for (int i = 0; i < 4; ++i) o[t][i] += co * (float)ao[t][i];
+    __syncthreads();
   };
   if (used > 0) {
     Raw ring[P];
@@ -477,17 +487,9 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
       const Raw first = frag;
       turn(first);
     }
-    // The chunk behind the one in work is turned, and the one P behind that asked for, on the way:
-    // past the end the last one again, since a load under a condition would make every wait for a
-    // load one for all of them.
-    for (int it = 0; it < used; it += P)
-      static_for<0, P>([&](auto I) {
-        const int slot = l_slot[it + I + 1 + P < used ? it + I + 1 + P : used - 1];
-        if (it + I < used) process(it + I);
-        turn(ring[I]);
-        load(ring[I], slot);
-        __syncthreads();
-      });
+    // Past the end the last chunk is loaded again, and composed with gate 0: a load under a
+    // condition would make every wait for a load one for all of them.
+    for (int it = 0; it < used; it += P) static_for<0, P>([&](auto I) { process(it + I, ring[I]); });
   }
   // o: live part + the chain's, whose two k halves (dv < dk) meet in LDS
   float sum[OT][4];
