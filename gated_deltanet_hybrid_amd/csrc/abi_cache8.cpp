@@ -45,17 +45,15 @@ hla::Cache8View view(const hla_cache8_t* c) {
 hla_status_t status(hipError_t e) { return e == hipSuccess ? HLA_OK : HLA_ERR_HIP; }
 
 // Checks shared by the two decode calls, and their common arguments.
-hla_status_t decode8(const hla_cache8_t* c, int32_t dtype, hla::Decode8Args& a, const void* ws, size_t ws_bytes,
+hla_status_t decode8(const hla_cache8_t* c, int32_t dtype, hla::Decode8Args& a, void* ws, size_t ws_bytes,
                      hipStream_t stream) {
   if (std::isnan(a.tau)) return HLA_ERR_BAD_SHAPE;
   if (!a.q || !a.k || !a.v || !a.S_cur || !a.At_cur || !a.o || (!a.gates_in && c->n_rep == 0)) return HLA_ERR_NULL_ARG;
   if (!aligned<16>(a.S_cur, a.At_cur, ws) || !aligned<4>(a.q, a.k, a.v, a.gates_in, a.o, a.gates_out))
     return HLA_ERR_ALIGN;
-  size_t need = 0;
-  const hla_status_t st = hla_decode8_workspace_bytes(c, &need);
-  if (st != HLA_OK) return st;
-  if (need && (!ws || ws_bytes < need)) return HLA_ERR_WORKSPACE;
   a.c = view(c);
+  const size_t need = (size_t)hla::plan_decode8(a, c->dk, c->dv, ws);
+  if (need && (!ws || ws_bytes < need)) return HLA_ERR_WORKSPACE;
   return status(hla::launch_decode8(a, c->format, dtype, c->dk, c->dv, stream));
 }
 
@@ -66,7 +64,12 @@ extern "C" {
 hla_status_t hla_decode8_workspace_bytes(const hla_cache8_t* c, size_t* out) {
   if (!out) return HLA_ERR_NULL_ARG;
   *out = 0;
-  return check_cache(c);
+  const hla_status_t st = check_cache(c);
+  if (st != HLA_OK) return st;
+  hla::Decode8Args a{};
+  a.c = view(c);
+  *out = (size_t)hla::plan_decode8(a, c->dk, c->dv, nullptr);
+  return HLA_OK;
 }
 
 hla_status_t hla_gdn_decode8(const hla_cache8_t* c, int32_t dtype, const void* q, const void* k, const void* v,

@@ -47,14 +47,15 @@ struct LiveRows {
   const float* k;
   float qe, qk;
 };
+// The columns go their own ways, so the matrix may be W columns of a wider one (rows ld apart).
 template <int DK, int W, int NT>
-__device__ __forceinline__ void live_update(float* mat, const LiveRows& r, const float* w, float* red0, float* red1,
-                                            float* s_u, float* out) {
+__device__ __forceinline__ void live_update(float* mat, int ld, const LiveRows& r, const float* w, float* red0,
+                                            float* red1, float* s_u, float* out) {
   constexpr int CPR = W / 4, RPP = NT / CPR, NP = DK / RPP;
   const int tid = threadIdx.x, col = (tid % CPR) * 4, r0 = tid / CPR;
   float4 m[NP];
 #pragma unroll
-  for (int p = 0; p < NP; ++p) m[p] = load_once(mat + (p * RPP + r0) * W + col);
+  for (int p = 0; p < NP; ++p) m[p] = load_once(mat + (p * RPP + r0) * ld + col);
   float4 pu = make_float4(0.f, 0.f, 0.f, 0.f), pz = pu;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
@@ -83,7 +84,7 @@ __device__ __forceinline__ void live_update(float* mat, const LiveRows& r, const
     n.y = ar * m[p].y - er * uu.y + kr * ww.y;
     n.z = ar * m[p].z - er * uu.z + kr * ww.z;
     n.w = ar * m[p].w - er * uu.w + kr * ww.w;
-    store_once(mat + i * W + col, n);
+    store_once(mat + i * ld + col, n);
   }
   __syncthreads();
 }
@@ -217,6 +218,119 @@ __device__ __forceinline__ unsigned rows_max(unsigned x) {
   return max_u(r[0], r[1]);
 }
 
+// A vector that all NW waves can see becomes an operand; returns the factor of its sums (NaN where
+// a value is not finite, which fixed point cannot hold).
+template <class Op, int DK, int NW> __device__ __forceinline__ float encode(Op& op, const float* src) {
+  const int lane = lane_id(), w = threadIdx.x >> 6;
+  float m = 0.f, bad = 0.f;
+  for (int i = lane; i < DK; i += 64) {
+    m = fmaxf(m, fabsf(src[i]));
+    bad += src[i] * 0.f;
+  }
+  const Fixed fx = fixed_for(wave_max_valu(m));
+  for (int r0 = 16 * w; r0 < DK; r0 += 16 * NW) {
+    const float4 x = *reinterpret_cast<const float4*>(src + r0 + (lane >> 4) * 4);
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    op.put(r0, v, fx.enc);
+  }
+  return (Op::kFixed ? fx.dec : 1.f) + wave_sum_valu(bad);
+}
+
+// The token as the live update takes it, in LDS.
+template <class T, int DK, int DV> struct Token {
+  float q[DK], k[DK], a[DK], e[DK], ka[DK], qa[DK], w[DV], dot[2];
+  template <int NT> __device__ __forceinline__ LiveRows load(const Decode8Args& in, int64_t row) {
+    const int tid = threadIdx.x;
+    for (int i = tid; i < DK; i += NT) {
+      const float qv = to_f<T>(reinterpret_cast<const T*>(in.q)[row * DK + i]);
+      const float kv = to_f<T>(reinterpret_cast<const T*>(in.k)[row * DK + i]);
+      const float dec = in.ga ? in.ga[row * DK + i] : in.alpha[row];
+      q[i] = qv;
+      k[i] = kv;
+      a[i] = dec;
+      ka[i] = dec * kv;
+      qa[i] = dec * qv;
+      e[i] = (in.ga ? in.gb[row * DK + i] : in.beta[row]) * kv;
+    }
+    for (int i = tid; i < DV; i += NT)
+      w[i] = (in.ga ? in.gw[row * DV + i] : in.beta[row]) * to_f<T>(reinterpret_cast<const T*>(in.v)[row * DV + i]);
+    __syncthreads();
+    if (tid < 128) {
+      const float* s = tid < 64 ? k : e;
+      float x = 0.f;
+      for (int i = lane_id(); i < DK; i += 64) x += q[i] * s[i];
+      x = wave_sum_valu(x);
+      if (lane_id() == 0) dot[tid >> 6] = x;
+    }
+    __syncthreads();
+    return {ka, qa, a, e, k, dot[1], dot[0]};
+  }
+};
+
+// A gate counts: skipped below tau, reported, added to its chunk's weight.
+__device__ __forceinline__ float take_gate(const Decode8Args& a, int64_t row, int j, float x) {
+  const float gh = x >= a.tau ? x : 0.f;
+  if (a.gates_out) a.gates_out[row * a.c.n_cap + j] = x;
+  if (a.c.weight) a.c.weight[row * a.c.n_cap + j] += gate_mass(gh);
+  return gh;
+}
+
+// Gates of the positions [lo, hi) whose slots and representatives' scales are slot[j - lo] and
+// g[j - lo], which becomes the gate.  The block works through them kScores scores at a time: 16
+// representatives a product, then eight lanes a chunk for the log-mean-exp.
+constexpr int kScores = 1024;  // n_rep <= 256: at least four chunks
+template <int FMT, int DK, int NW>
+__device__ __forceinline__ void chunk_gates(const Decode8Args& a, int64_t row, int lo, int hi, const int* slot, float* g,
+                                            const Operand<FMT, DK>& q, float q_unit, Turn<DK>& turn, float* s_score) {
+  using Op = Operand<FMT, DK>;
+  constexpr int KP = DK / 64, PPR = DK / 16, NT = NW * 64;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n_rep = a.c.n_rep;
+  typename Op::Frag qf[KP];
+#pragma unroll
+  for (int p = 0; p < KP; ++p) qf[p] = q.get(p);
+  const float qu = q_unit * Op::term_unit();
+  const int per = kScores / n_rep;  // chunks a block of scores holds
+  const unsigned inv = ((1u << 20) + n_rep - 1) / n_rep;  // r / n_rep = r inv >> 20 for r < 1024, n_rep <= 256
+  const float unit = 1.f / sqrtf((float)DK);
+  for (int j0 = 0; j0 < hi - lo; j0 += per) {
+    const int nj = hi - lo - j0 < per ? hi - lo - j0 : per, rows = nj * n_rep;
+    for (int r0 = w * 16; r0 < rows; r0 += NW * 16) {
+      uint4 raw[KP], frag[KP];
+#pragma unroll
+      for (int i = 0; i < KP; ++i) {
+        const int r = r0 + i * 8 + lane / PPR < rows ? r0 + i * 8 + lane / PPR : rows - 1;
+        const int jj = (int)((unsigned)r * inv >> 20);
+        const int64_t at = (row * a.c.n_cap + slot[j0 + jj]) * n_rep + (r - jj * n_rep);
+        raw[i] = *reinterpret_cast<const uint4*>(a.c.reps + at * DK + lane % PPR * 16);
+      }
+      turn.turn(raw, frag);
+      typename Op::Acc acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < KP; ++p) acc = Op::step(frag[p], qf[p], acc);
+      float s[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = terms_sum((float)acc[i], qu);
+      if ((lane & 15) == 0)
+        *reinterpret_cast<float4*>(s_score + r0 + (lane >> 4) * 4) = make_float4(s[0], s[1], s[2], s[3]);
+    }
+    __syncthreads();
+    for (int jj = tid >> 3; jj < nj; jj += NT / 8) {
+      const float sc = g[j0 + jj] * unit;
+      const float* score = s_score + jj * n_rep;
+      float m = -INFINITY, sum = 0.f;
+      for (int r = tid & 7; r < n_rep; r += 8) m = fmaxf(m, score[r] * sc);
+      m = fmaxf(m, dpp_f<0xB1>(m));
+      m = fmaxf(m, dpp_f<0x4E>(m));
+      m = fmaxf(m, dpp_f<0x141>(m));
+      for (int r = tid & 7; r < n_rep; r += 8) sum += expf(score[r] * sc - m);
+      sum = group_sum<8>(sum);
+      if ((tid & 7) == 0)
+        g[j0 + jj] = take_gate(a, row, lo + j0 + jj, 1.f / (1.f + expf(-(m + logf(sum / (float)n_rep)))));
+    }
+    __syncthreads();
+  }
+}
+
 // One workgroup per (sequence, head), a wave for every 16 rows of E: the live update, the gates
 // (16 representatives a product, their scores through LDS in blocks of whole chunks), then the
 // chain.  In the chain wave w owns z's rows 16 w .. and its share of o's; a chunk's new z becomes
@@ -226,141 +340,66 @@ __device__ __forceinline__ unsigned rows_max(unsigned x) {
 // the terms, and the next z is at most (1 + |ghat sA| 128 dk) times that; where this factor is
 // over 2^7 (a term would then hold fewer than 23 bits of the largest |z|), the waves exchange the
 // new maximum first, at the price of a second barrier.
-template <int FMT, class T, int DK, int DV>
+// PART: the chain over one segment of a row's positions for the split form below: gates, live part
+// and the z that enters come from the workspace, and o's share goes there.
+template <int FMT, class T, int DK, int DV, bool PART>
 __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
   using Op = Operand<FMT, DK>;
   constexpr int NW = DK / 16, NT = NW * 64, WMAX = DV > DK ? DV : DK, P = 4, KP = DK / 64, PPR = DK / 16;
   // o's tiles: OT of them to a wave, or where dv < dk one k half of a tile to a wave
   constexpr bool kHalf = DV < DK;
   constexpr int OT = kHalf ? 1 : DV / DK, OP = kHalf ? 1 : KP;
-  constexpr int kScores = 1024;  // scores held at a time (n_rep <= 256: at least four chunks)
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4;
-  const int64_t row = blockIdx.x;
-  __shared__ __align__(16) float s_q[DK], s_k[DK], s_a[DK], s_e[DK], s_ka[DK], s_qa[DK], s_w[DV];
-  __shared__ __align__(16) float s_u[WMAX], s_o[2][DV], s_z[DK];
+  const int64_t row = PART ? blockIdx.x / a.segs : blockIdx.x;
   constexpr int kRed = NT * 4;
+  __shared__ __align__(16) float s_u[WMAX], s_o[2][DV], s_z[DK];
   __shared__ __align__(16) float s_red[2 * kRed > 3 * kMaxCache ? 2 * kRed : 3 * kMaxCache];
   __shared__ __align__(16) unsigned s_max[2][8];
   __shared__ __align__(16) Op s_x[2];
-  __shared__ __align__(16) float s_score[kScores];
-  __shared__ float s_dot[2];
   // by position: slot, scale of A - I and B, and the scale of the representatives, then the gate
   __shared__ int s_slot[kMaxCache];
   __shared__ float s_sa[kMaxCache], s_sb[kMaxCache], s_g[kMaxCache];
   __shared__ unsigned long long s_on[kMaxCache / 64];
   __shared__ __align__(16) Turn<DK> s_turn[NW][kHalf ? 2 : 1 + OT];  // each wave's own
 
-  const int n = cache8_count(a.c, row), n_cap = a.c.n_cap, n_rep = a.c.n_rep;
+  const int held = cache8_count(a.c, row), n_cap = a.c.n_cap;
+  const int segs = PART ? split_segments(a, held) : 1, seg = PART ? (int)(blockIdx.x % a.segs) : 0;
+  if (seg >= segs) return;
+  const int lo = seg * a.seg_len, n = segs == 1 ? held : (held - lo < a.seg_len ? held - lo : a.seg_len);
   for (int j = tid; j < n; j += NT) {
-    const int slot = cache8_slot(a.c, row, j);
+    const int slot = cache8_slot(a.c, row, lo + j);
     const float4 sc = a.c.scale[row * n_cap + slot];
     s_slot[j] = slot;
     s_sa[j] = sc.x;
     s_sb[j] = sc.y;
-    s_g[j] = sc.z;
+    s_g[j] = PART ? a.ws.gate[row * n_cap + lo + j] : sc.z;
   }
-  if (tid < DK) {
-    const float qv = to_f<T>(reinterpret_cast<const T*>(a.q)[row * DK + tid]);
-    const float kv = to_f<T>(reinterpret_cast<const T*>(a.k)[row * DK + tid]);
-    const float dec = a.ga ? a.ga[row * DK + tid] : a.alpha[row];
-    s_q[tid] = qv;
-    s_k[tid] = kv;
-    s_a[tid] = dec;
-    s_ka[tid] = dec * kv;
-    s_qa[tid] = dec * qv;
-    s_e[tid] = (a.ga ? a.gb[row * DK + tid] : a.beta[row]) * kv;
-  }
-  if (tid < DV) s_w[tid] = (a.ga ? a.gw[row * DV + tid] : a.beta[row]) * to_f<T>(reinterpret_cast<const T*>(a.v)[row * DV + tid]);
-  __syncthreads();
-  if (w < 2) {
-    const float* s = w ? s_e : s_k;
-    float x = 0.f;
-    for (int i = lane; i < DK; i += 64) x += s_q[i] * s[i];
-    x = wave_sum_valu(x);
-    if (lane == 0) s_dot[w] = x;
-  }
-  // A vector that all waves can see becomes an operand; returns the factor of its sums (NaN where
-  // a value is not finite, which fixed point cannot hold).
-  auto encode = [&](Op& op, const float* src) {
-    float m = 0.f, bad = 0.f;
-    for (int i = lane; i < DK; i += 64) {
-      m = fmaxf(m, fabsf(src[i]));
-      bad += src[i] * 0.f;
-    }
-    const Fixed fx = fixed_for(wave_max_valu(m));
-    const float4 x = *reinterpret_cast<const float4*>(src + 16 * w + g * 4);
-    const float v[4] = {x.x, x.y, x.z, x.w};
-    op.put(16 * w, v, fx.enc);
-    return (Op::kFixed ? fx.dec : 1.f) + wave_sum_valu(bad);
-  };
-  const float q_unit = encode(s_x[1], s_q) * Op::term_unit();
-  __syncthreads();
-  const LiveRows lr{s_ka, s_qa, s_a, s_e, s_k, s_dot[1], s_dot[0]};
-  live_update<DK, DV, NT>(a.S_cur + row * DK * DV, lr, s_w, s_red, s_red + kRed, s_u, s_o[0]);
-  live_update<DK, DK, NT>(a.At_cur + row * DK * DK, lr, nullptr, s_red, s_red + kRed, s_u, s_z);
-
-  // ---- gates
-  auto take_gate = [&](int j, float x) {
-    const float gh = x >= a.tau ? x : 0.f;
-    s_g[j] = gh;
-    if (a.gates_out) a.gates_out[row * n_cap + j] = x;
-    if (a.c.weight) a.c.weight[row * n_cap + j] += gate_mass(gh);
-  };
-  if (a.gates_in) {
-    for (int j = tid; j < n; j += NT) take_gate(j, a.gates_in[row * n_cap + j]);
+  if constexpr (PART) {
+    const float* from = segs == 1 ? a.ws.y + row * DK : a.ws.z + (row * a.segs + seg) * DK;
+    if (tid < DK) s_z[tid] = from[tid];
+    if (tid < DV) s_o[0][tid] = segs == 1 ? a.ws.o[row * DV + tid] : 0.f;
   } else {
-    typename Op::Frag qf[KP];
-#pragma unroll
-    for (int p = 0; p < KP; ++p) qf[p] = s_x[1].get(p);
-    const int per = kScores / n_rep;  // chunks a block of scores holds
-    const unsigned inv = ((1u << 20) + n_rep - 1) / n_rep;  // r / n_rep = r inv >> 20 for r < 1024, n_rep <= 256
-    const float unit = 1.f / sqrtf((float)DK);
-    for (int j0 = 0; j0 < n; j0 += per) {
-      const int nj = n - j0 < per ? n - j0 : per, rows = nj * n_rep;
-      for (int r0 = w * 16; r0 < rows; r0 += NW * 16) {
-        uint4 raw[KP], frag[KP];
-#pragma unroll
-        for (int i = 0; i < KP; ++i) {
-          const int r = r0 + i * 8 + lane / PPR < rows ? r0 + i * 8 + lane / PPR : rows - 1;
-          const int jj = (int)((unsigned)r * inv >> 20);
-          const int64_t slot = row * n_cap + s_slot[j0 + jj];
-          raw[i] = *reinterpret_cast<const uint4*>(a.c.reps + (slot * n_rep + (r - jj * n_rep)) * DK + lane % PPR * 16);
-        }
-        s_turn[w][0].turn(raw, frag);
-        typename Op::Acc acc = {0, 0, 0, 0};
-#pragma unroll
-        for (int p = 0; p < KP; ++p) acc = Op::step(frag[p], qf[p], acc);
-        float s[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = terms_sum((float)acc[i], q_unit);
-        if ((lane & 15) == 0) *reinterpret_cast<float4*>(s_score + r0 + g * 4) = make_float4(s[0], s[1], s[2], s[3]);
-      }
-      __syncthreads();
-      // eight lanes a chunk: the largest score, then the mean of the exponentials
-      for (int jj = tid >> 3; jj < nj; jj += NT / 8) {
-        const float sc = s_g[j0 + jj] * unit;
-        const float* score = s_score + jj * n_rep;
-        float m = -INFINITY, sum = 0.f;
-        for (int r = tid & 7; r < n_rep; r += 8) m = fmaxf(m, score[r] * sc);
-        m = fmaxf(m, dpp_f<0xB1>(m));
-        m = fmaxf(m, dpp_f<0x4E>(m));
-        m = fmaxf(m, dpp_f<0x141>(m));
-        for (int r = tid & 7; r < n_rep; r += 8) sum += expf(score[r] * sc - m);
-        sum = group_sum<8>(sum);
-        if ((tid & 7) == 0) take_gate(j0 + jj, 1.f / (1.f + expf(-(m + logf(sum / (float)n_rep)))));
-      }
-      __syncthreads();
+    __shared__ __align__(16) Token<T, DK, DV> s_token;
+    __shared__ __align__(16) float s_score[kScores];
+    const LiveRows lr = s_token.template load<NT>(a, row);
+    const float q_unit = encode<Op, DK, NW>(s_x[1], s_token.q);
+    live_update<DK, DV, NT>(a.S_cur + row * DK * DV, DV, lr, s_token.w, s_red, s_red + kRed, s_u, s_o[0]);
+    live_update<DK, DK, NT>(a.At_cur + row * DK * DK, DK, lr, nullptr, s_red, s_red + kRed, s_u, s_z);
+    if (a.gates_in) {
+      for (int j = tid; j < n; j += NT) s_g[j] = take_gate(a, row, j, a.gates_in[row * n_cap + j]);
+    } else {
+      chunk_gates<FMT, DK, NW>(a, row, 0, n, s_slot, s_g, s_x[1], q_unit, s_turn[w][0], s_score);
     }
+    if (a.gates_out)
+      for (int j = n + tid; j < n_cap; j += NT) a.gates_out[row * n_cap + j] = 0.f;
   }
-  if (a.gates_out)
-    for (int j = n + tid; j < n_cap; j += NT) a.gates_out[row * n_cap + j] = 0.f;
   __syncthreads();
   for (int i = w; i < kMaxCache / 64; i += NW) {
     const int j = 64 * i + lane;
     const unsigned long long on = __ballot(j < n && s_g[j] != 0.f);
     if (lane == 0) s_on[i] = on;
   }
-  float unit = encode(s_x[0], s_z);  // 2^(e-30) of the operand in use
+  float unit = encode<Op, DK, NW>(s_x[0], s_z);  // 2^(e-30) of the operand in use
   float z[4], o[OT][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) z[i] = s_z[16 * w + g * 4 + i];
@@ -429,7 +468,7 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
   int buf = 0;
   // Chunk `it`.  The products come first; then the chunk behind (`ring`) is turned and the one P
   // behind that asked for, and the LDS and memory work on those while z is brought up to date.
-  auto process = [&](int it, Raw& ring) {
+  auto process = [&](int it, Raw& ring) __attribute__((always_inline)) {
     const bool live = it < used;
     const float ca = live ? l_ca[it] : 0.f, cb = live ? l_cb[it] : 0.f;
     const int slot = l_slot[it + 1 + P < used ? it + 1 + P : used - 1];
@@ -508,15 +547,266 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = (kHalf ? w >> 1 : OT * w + t) * 16 + g * 4 + i;
-        a.o[row * DV + c] = s_o[0][c] + sum[t][i] + (kHalf ? s_o[1][c] : 0.f);
+        float* out = segs == 1 ? a.o + row * DV : a.ws.part + (row * a.segs + seg) * DV;
+        out[c] = s_o[0][c] + sum[t][i] + (kHalf ? s_o[1][c] : 0.f);
       }
   }
+}
+
+// ---- the split form, for few rows
+//
+// A chain is a sequence of dependent products on one CU (about 0.6 us a chunk; the CU draws some 54
+// GB/s), so with few rows most of the card would wait.  The positions are cut into segments of
+// seg_len.  For every segment but the oldest all workgroups at once compose the linear parts,
+//   Phi_s = product over its chunks, newest first, of (I + ghat sA E),
+// a matrix product a chunk instead of a vector's; then one workgroup a row takes z through the
+// segments (z <- Phi_s z), and with every segment's z known all segments' chains run at once, their
+// shares of o added in a fixed order.
+//
+// First: the live update by 32-column slices, and the gates by blocks of positions.
+template <int FMT, class T, int DK, int DV>
+__global__ __launch_bounds__(256) void split_gates_kernel(Decode8Args a) {
+  using Op = Operand<FMT, DK>;
+  constexpr int NT = 256, LB = (DK + DV) / 32;
+  const int blocks = LB + a.gate_blocks, tid = threadIdx.x;
+  const int64_t row = blockIdx.x / blocks;
+  const int b = (int)(blockIdx.x % blocks);
+  __shared__ __align__(16) Token<T, DK, DV> s_token;
+  if (b < LB) {
+    __shared__ __align__(16) float s_red[2][NT * 4], s_u[32], s_out[32];
+    const LiveRows lr = s_token.template load<NT>(a, row);
+    const bool state = b < DV / 32;
+    const int c0 = (state ? b : b - DV / 32) * 32;
+    if (state)
+      live_update<DK, 32, NT>(a.S_cur + row * DK * DV + c0, DV, lr, s_token.w + c0, s_red[0], s_red[1], s_u, s_out);
+    else
+      live_update<DK, 32, NT>(a.At_cur + row * DK * DK + c0, DK, lr, nullptr, s_red[0], s_red[1], s_u, s_out);
+    if (tid < 32) (state ? a.ws.o + row * DV : a.ws.y + row * DK)[c0 + tid] = s_out[tid];
+    return;
+  }
+  const int n = cache8_count(a.c, row), n_cap = a.c.n_cap;
+  const int lo = (b - LB) * a.gate_len;
+  const int end = lo + a.gate_len < n_cap ? lo + a.gate_len : n_cap, hi = end < n ? end : n;
+  if (a.gates_out)
+    for (int j = (lo < n ? n : lo) + tid; j < end; j += NT) a.gates_out[row * n_cap + j] = 0.f;
+  if (lo >= hi) return;
+  if (a.gates_in) {
+    for (int j = lo + tid; j < hi; j += NT)
+      a.ws.gate[row * n_cap + j] = take_gate(a, row, j, a.gates_in[row * n_cap + j]);
+    return;
+  }
+  __shared__ __align__(16) Op s_x;
+  __shared__ __align__(16) Turn<DK> s_turn[NT / 64];
+  __shared__ __align__(16) float s_score[kScores];
+  __shared__ int s_slot[kMaxCache];
+  __shared__ float s_g[kMaxCache];
+  for (int j = lo + tid; j < hi; j += NT) {
+    const int slot = cache8_slot(a.c, row, j);
+    s_slot[j - lo] = slot;
+    s_g[j - lo] = a.c.scale[row * n_cap + slot].z;
+  }
+  for (int i = tid; i < DK; i += NT) s_token.q[i] = to_f<T>(reinterpret_cast<const T*>(a.q)[row * DK + i]);
+  __syncthreads();
+  const float q_unit = encode<Op, DK, NT / 64>(s_x, s_token.q);
+  __syncthreads();
+  chunk_gates<FMT, DK, NT / 64>(a, row, lo, hi, s_slot, s_g, s_x, q_unit, s_turn[tid >> 6], s_score);
+  for (int j = lo + tid; j < hi; j += NT) a.ws.gate[row * n_cap + j] = s_g[j - lo];
+}
+
+// Phi of one segment.  The matrix P (float32, in the accumulators of the 32 x 32 products) starts as
+// the identity; a chunk does P <- P + c E P, with E's stored numbers exact in bf16 and P as three
+// bf16 terms (24 bits: float32).  Wave w owns P's columns 32 w .., for which an accumulator tile
+// is, register for register, the next product's B operand; so P never leaves the wave, and the
+// waves share only E, which they bring to LDS as A fragments, a chunk ahead, in two buffers.
+// Bound by the products (3 x 2 dk^3 flops a chunk) and the splitting of P on the vector units.
+template <int FMT, int DK>
+__global__ __launch_bounds__(DK * 2, 2) void split_compose_kernel(Decode8Args a, int rec) {
+  constexpr int NT = DK * 2, RT = DK / 32, KS = DK / 16, PER = DK * DK / 16 / NT, FR = 1024 + 16;
+  __shared__ __align__(16) uint8_t s_e[2][RT * KS * FR];
+  __shared__ int l_slot[kMaxSegment];
+  __shared__ float l_ca[kMaxSegment];
+  __shared__ int s_used;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5;
+  const int64_t row = blockIdx.x / (a.segs - 1);
+  const int seg = (int)(blockIdx.x % (a.segs - 1)) + 1, n_cap = a.c.n_cap;
+  const int held = cache8_count(a.c, row), lo = seg * a.seg_len;
+  if (seg >= split_segments(a, held)) return;
+  const int n = held - lo < a.seg_len ? held - lo : a.seg_len;
+  if (w == 0) {  // chunks in use, newest first (n <= 64)
+    const int j = lo + n - 1 - lane;
+    const float gh = lane < n ? a.ws.gate[row * n_cap + j] : 0.f;
+    const unsigned long long on = __ballot(lane < n && gh != 0.f);
+    if (lane < n && gh != 0.f) {
+      const int at = __popcll(on & ((1ull << lane) - 1)), slot = cache8_slot(a.c, row, j);
+      l_slot[at] = slot;
+      l_ca[at] = gh * a.c.scale[row * n_cap + slot].x;
+    }
+    if (lane == 0) s_used = __popcll(on);
+  }
+  __syncthreads();
+  const int used = __builtin_amdgcn_readfirstlane(s_used);
+
+  f32x16 P[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) P[t][i] = 32 * t + acc_row(i, h) == 32 * w + (lane & 31) ? 1.f : 0.f;
+
+  const uint8_t* base = a.c.maps + row * n_cap * (int64_t)rec;
+  uint4 ring[PER];
+  auto load = [&](uint4 (&r)[PER], int it) __attribute__((always_inline)) {
+    const int slot = __builtin_amdgcn_readfirstlane(l_slot[it < used ? it : used - 1]);
+    const uint8_t* m = base + (int64_t)slot * rec;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) r[i] = load_once(m + (unsigned)(tid * 16 + i * NT * 16));
+  };
+  // 16 stored numbers of row r are two lanes' fragments: slot e of lane half h is
+  // k = 16 ks + 8 (e / 4) + 4 h + e % 4 (the order in which an accumulator tile holds its rows)
+  auto stage = [&](const uint4 (&r)[PER], int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int u = i * NT + tid, er = u / KS, ks = u % KS;
+      uint8_t* at = &s_e[buf][((er >> 5) * KS + ks) * FR + (er & 31) * 16];
+      *reinterpret_cast<bf16x8*>(at) = stored_frag<FMT>(r[i].x, r[i].z);
+      *reinterpret_cast<bf16x8*>(at + 512) = stored_frag<FMT>(r[i].y, r[i].w);
+    }
+  };
+  auto compose = [&](int it, int buf) __attribute__((always_inline)) {  // (P stays in registers)
+    const float ca = l_ca[it];
+    bf16x8 b[3][KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint4 pack[3];
+      unsigned* word[3] = {&pack[0].x, &pack[1].x, &pack[2].x};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // terms by cutting off, 8 bits of the significand each: and + subtract
+        float x[2] = {P[ks >> 1][(ks & 1) * 8 + 2 * e], P[ks >> 1][(ks & 1) * 8 + 2 * e + 1]};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const unsigned u0 = __builtin_bit_cast(unsigned, x[0]), u1 = __builtin_bit_cast(unsigned, x[1]);
+          word[i][e] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
+          x[0] -= __builtin_bit_cast(float, u0 & 0xffff0000u);
+          x[1] -= __builtin_bit_cast(float, u1 & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) b[i][ks] = __builtin_bit_cast(bf16x8, pack[i]);
+    }
+    constexpr int AHEAD = 4;  // fragments on their way from LDS
+    bf16x8 f[AHEAD];
+    auto get = [&](int i) __attribute__((always_inline)) {
+      return *reinterpret_cast<const bf16x8*>(&s_e[buf][i * FR + lane * 16]);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) f[i] = get(i);
+    f32x16 d;
+    static_for<0, RT * KS>([&](auto I) __attribute__((always_inline)) {
+      constexpr int i = I, t = i / KS, ks = i % KS;
+      if constexpr (ks == 0) d = zero16();
+#pragma unroll
+      for (int x = 0; x < 3; ++x) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD], b[x][ks], d, 0, 0, 0);
+      if constexpr (i + AHEAD < RT * KS) f[i % AHEAD] = get(i + AHEAD);
+      if constexpr (ks == KS - 1) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) P[t][e] += ca * d[e];
+      }
+    });
+  };
+  if (used > 0) {
+    load(ring, 0);
+    stage(ring, 0);
+    load(ring, 1);
+    __syncthreads();
+    for (int it = 0; it < used; it += 2)
+      static_for<0, 2>([&](auto I) __attribute__((always_inline)) {
+        if (it + I < used) compose(it + I, I);
+        stage(ring, I ^ 1);
+        load(ring, it + I + 2);
+        __syncthreads();
+      });
+  }
+  float* out = a.ws.phi + ((row * a.segs + seg) * DK + 32 * w + (lane & 31)) * DK + 4 * h;  // column by column
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(out + 32 * t + 8 * i) = make_float4(P[t][4 * i], P[t][4 * i + 1], P[t][4 * i + 2], P[t][4 * i + 3]);
+}
+
+// z through a row's segments, newest first: 16 groups of threads take DK / 16 columns of Phi each.
+template <int DK>
+__global__ __launch_bounds__(DK * 4) void split_join_kernel(Decode8Args a) {
+  constexpr int M4 = DK / 4, G = 16, PER = DK / G;
+  __shared__ __align__(16) float s_z[DK], s_red[G][DK];
+  const int tid = threadIdx.x, m = (tid % M4) * 4, grp = tid / M4;
+  const int64_t row = blockIdx.x;
+  const int segs = split_segments(a, cache8_count(a.c, row));
+  if (segs == 1) return;
+  float4 cur[PER], ahead[PER];
+  auto load = [&](float4 (&x)[PER], int seg) {
+    const float* phi = a.ws.phi + ((row * a.segs + seg) * DK + grp * PER) * DK + m;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) x[i] = *reinterpret_cast<const float4*>(phi + i * DK);
+  };
+  load(ahead, segs - 1);
+  if (tid < DK) s_z[tid] = a.ws.y[row * DK + tid];
+  __syncthreads();
+  for (int seg = segs - 1; seg > 0; --seg) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) cur[i] = ahead[i];
+    load(ahead, seg > 1 ? seg - 1 : 1);
+    if (tid < DK) a.ws.z[(row * a.segs + seg) * DK + tid] = s_z[tid];
+    float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float x = s_z[grp * PER + i];
+      p.x += x * cur[i].x; p.y += x * cur[i].y; p.z += x * cur[i].z; p.w += x * cur[i].w;
+    }
+    *reinterpret_cast<float4*>(&s_red[grp][m]) = p;
+    __syncthreads();
+    if (tid < DK) {
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < G; ++i) z += s_red[i][tid];
+      s_z[tid] = z;
+    }
+    __syncthreads();
+  }
+  if (tid < DK) a.ws.z[row * a.segs * DK + tid] = s_z[tid];
+}
+
+// o = the live part + every segment's share, newest first.
+__global__ __launch_bounds__(128) void split_sum_kernel(Decode8Args a, int dv) {
+  const int64_t row = blockIdx.x;
+  const int segs = split_segments(a, cache8_count(a.c, row)), c = threadIdx.x;
+  if (segs == 1 || c >= dv) return;
+  float o = a.ws.o[row * dv + c];
+#pragma unroll 8
+  for (int s = segs - 1; s >= 0; --s) o += a.ws.part[(row * a.segs + s) * dv + c];
+  a.o[row * dv + c] = o;
 }
 
 template <int FMT, class T, int DK, int DV>
 hipError_t run_decode8(const Decode8Args& a, hipStream_t s) {
   TimedLaunch tl(HLA_KERNEL_DECODE, s);
-  hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV>), dim3((unsigned)a.c.rows), dim3(DK * 4), 0, s, a);
+  const unsigned rows = (unsigned)a.c.rows;
+  if (a.segs == 0) {
+    hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV, false>), dim3(rows), dim3(DK * 4), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((split_gates_kernel<FMT, T, DK, DV>), dim3(rows * ((DK + DV) / 32 + a.gate_blocks)), dim3(256), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((split_compose_kernel<FMT, DK>), dim3(rows * (a.segs - 1)), dim3(DK * 2), 0, s, a, (DK + DV) * DK);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((split_join_kernel<DK>), dim3(rows), dim3(DK * 4), 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV, true>), dim3(rows * a.segs), dim3(DK * 4), 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(split_sum_kernel, dim3(rows), dim3(128), 0, s, a, DV);
   return hipGetLastError();
 }
 template <int FMT, class T>
@@ -526,6 +816,51 @@ hipError_t pick_decode8(const Decode8Args& a, int dk, int dv, hipStream_t s) {
 }
 
 }  // namespace
+
+// Which form a call takes, from its sizes alone.  In microseconds for n = n_cap chunks, as measured
+// (dk = 128 / 64): one workgroup a row composes a chunk in 0.63 / 0.5 and scores n_rep
+// representatives in 0.0075 n_rep (dk / 128), whatever the number of rows up to the CUs'; the split
+// form costs 60 / 30 for its launches and its walk over the segments, and for every row and chunk
+// 0.0187 / 0.0045 (the composition's matrix products at the rate a large library product reaches,
+// and the maps read a second time).  Measured on both sides: dk = 128, n_rep = 2, n = 1024, 16 rows
+// 356 split, 648 not, 64 rows 1039 and 711; n = 128, 4 rows 70 and 88, 32 rows 121 and 92; dk = 64,
+// n = 512, 64 rows 160 and 271, 256 rows 470 and 288; dk = 128, n_rep = 64, n = 64, 16 rows 69
+// and 75, 64 rows 119 and 85.
+static bool split_pays(int64_t rows, int n, int n_rep, int dk) {
+  const float whole = (dk == 128 ? 0.63f : 0.5f) + 0.0075f * n_rep * dk / 128.f;
+  const float fixed = dk == 128 ? 60.f : 30.f, each = dk == 128 ? 0.0187f : 0.0045f;
+  return n >= kSplitFrom && rows < 256 && fixed + each * rows * n < whole * n;
+}
+
+int64_t plan_decode8(Decode8Args& a, int dk, int dv, void* ws) {
+  const int64_t rows = a.c.rows;
+  const int n_cap = a.c.n_cap;
+  a.segs = 0;
+  if (!split_pays(rows, n_cap, a.c.n_rep, dk)) return 0;
+  // a segment's composition and its chain take turns with the walk over the segments, at about
+  // sqrt(n / 2) of each; and no more than four workgroups of the composition for each CU
+  int len = (int)(sqrtf(n_cap / 2.f) + 0.5f);
+  const int busy = (int)((rows * n_cap + 1023) / 1024);
+  if (len < busy) len = busy;
+  a.seg_len = len < 8 ? 8 : (len > kMaxSegment ? kMaxSegment : len);
+  a.segs = (n_cap + a.seg_len - 1) / a.seg_len;
+  a.gate_len = a.c.n_rep ? 512 / a.c.n_rep : 64;
+  a.gate_len = a.gate_len < 1 ? 1 : (a.gate_len > 64 ? 64 : a.gate_len);
+  a.gate_blocks = (n_cap + a.gate_len - 1) / a.gate_len;
+  int64_t used = 0;
+  auto take = [&](int64_t floats) {
+    float* p = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + used) : nullptr;
+    used += (floats * 4 + 255) / 256 * 256;
+    return p;
+  };
+  a.ws.gate = take(rows * n_cap);
+  a.ws.y = take(rows * dk);
+  a.ws.o = take(rows * dv);
+  a.ws.z = take(rows * a.segs * dk);
+  a.ws.part = take(rows * a.segs * dv);
+  a.ws.phi = take(rows * a.segs * dk * dk);
+  return used;
+}
 
 hipError_t launch_decode8(const Decode8Args& a, int fmt, int dtype, int dk, int dv, hipStream_t s) {
   if (fmt == kI8) return dtype == 1 ? pick_decode8<kI8, bf16>(a, dk, dv, s) : pick_decode8<kI8, float>(a, dk, dv, s);

@@ -59,13 +59,24 @@ template <> struct Stored<kE4M3> {
   }
 };
 
-// Eight e4m3 numbers (two words) as bf16, exactly.
+// Eight stored numbers (two words) as bf16, exactly.
 __device__ __forceinline__ bf16x8 e4m3_frag(unsigned w0, unsigned w1) {
   return __builtin_bit_cast(
       bf16x8, make_uint4(__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, false)),
                          __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, true)),
                          __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, false)),
                          __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, true))));
+}
+
+template <int FMT> __device__ __forceinline__ bf16x8 stored_frag(unsigned w0, unsigned w1) {
+  if constexpr (FMT == kE4M3) return e4m3_frag(w0, w1);
+  float a[4], b[4];
+  Stored<kI8>::unpack(w0, a);
+  Stored<kI8>::unpack(w1, b);
+  auto hi2 = [](float x, float y) {  // 8-bit integers: the low halves of their float32 images are zero
+    return __builtin_amdgcn_perm(__builtin_bit_cast(unsigned, y), __builtin_bit_cast(unsigned, x), 0x07060302u);
+  };
+  return __builtin_bit_cast(bf16x8, make_uint4(hi2(a[0], a[1]), hi2(a[2], a[3]), hi2(b[0], b[1]), hi2(b[2], b[3])));
 }
 
 template <int FMT> __device__ __forceinline__ float to_stored(float m) {
@@ -91,7 +102,26 @@ struct Decode8Args {
   float* o;               // [Bs,H,dv]
   float* gates_out;       // [Bs,H,n_cap] or null
   float tau;
+  // The split form (segs = 0: one workgroup a row does everything): at most `segs` segments of
+  // seg_len positions a row, the gates in gate_blocks blocks of gate_len.
+  int32_t segs, seg_len, gate_blocks, gate_len;
+  struct Work {
+    float* gate;  // [rows,n_cap]: gates after the threshold
+    float* y;     // [rows,dk]: At_cur^T q
+    float* o;     // [rows,dv]: the live part of o
+    float* z;     // [rows,segs,dk]: z as it enters each segment
+    float* part;  // [rows,segs,dv]: each segment's share of o
+    float* phi;   // [rows,segs,dk,dk]: column by column
+  } ws;
 };
+constexpr int kMaxSegment = 64;
+constexpr int kSplitFrom = 64;  // a row that holds fewer chunks is one segment
+__device__ __forceinline__ int split_segments(const Decode8Args& a, int held) {
+  return held < kSplitFrom ? 1 : (held + a.seg_len - 1) / a.seg_len;
+}
+// Sets the form of a call and its workspace (offsets from `ws`, which may be null); returns the
+// workspace's bytes.
+int64_t plan_decode8(Decode8Args& a, int dk, int dv, void* ws);
 hipError_t launch_decode8(const Decode8Args& a, int fmt, int dtype, int dk, int dv, hipStream_t s);
 
 struct Append8Args {
