@@ -125,7 +125,7 @@ hla_status_t hla_cache8_append(const hla_cache8_t* c, int32_t dtype, int32_t n_s
 hla_status_t hla_gate_weights(int64_t B, int64_t H, int32_t N, const float* gates, const int32_t* n_chunks,
                               float tau, float* weight, hipStream_t stream) {
   if (B < 1 || H < 1 || N < 1 || std::isnan(tau)) return HLA_ERR_BAD_SHAPE;
-  if ((double)B * (double)H * ((N + 63.0) / 64.0) > kMaxGrid || (double)B * (double)H * (double)N * (double)N > 4.0e18)
+  if ((double)B * (double)H * ((N + 31.0) / 32.0) > kMaxGrid || (double)B * (double)H * (double)N * (double)N > 4.0e18)
     return HLA_ERR_BAD_SHAPE;
   if (!gates || !weight) return HLA_ERR_NULL_ARG;
   if (!aligned<4>(gates, n_chunks, weight)) return HLA_ERR_ALIGN;

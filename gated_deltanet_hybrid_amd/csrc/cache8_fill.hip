@@ -89,6 +89,19 @@ __device__ __forceinline__ void reset_map(T* m, int rows, bool identity) {
   for (int i = threadIdx.x; i < rows * W; i += NT) m[i] = from_f<T>(identity && i / W == i % W ? 1.f : 0.f);
 }
 
+// A row's bookkeeping by one wave once its chunks are stored: count, and the new positions'
+// weights; a cache that starts empty also gets its order (position p in slot p).
+__device__ __forceinline__ void append_finish(const Append8Args& a, int64_t row, int held, int add) {
+  const int lane = threadIdx.x & 63, n_cap = a.c.n_cap;
+  const int p0 = a.reset ? 0 : held, p1 = a.reset ? n_cap : held + add;
+  for (int p = p0 + lane; p < p1; p += 64) {
+    if (a.reset) a.c.order[row * n_cap + p] = p;
+    const int i = p - held;
+    if (a.c.weight) a.c.weight[row * n_cap + p] = i < add && a.weight_in ? a.weight_in[row * a.ld_src + i] : 0.f;
+  }
+  if (lane == 0) a.c.count[row] = held + add;
+}
+
 // One workgroup per (row, appended chunk): the maps are read once into registers, their largest
 // magnitudes found, and the quantised transposes go through LDS to 16-byte stores.
 template <int FMT, class T, int DK, int DV, int NT>
@@ -98,8 +111,12 @@ __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
   __shared__ float s_red[NT / 64];
   const int64_t row = blockIdx.x / a.n_src;
   const int i = (int)(blockIdx.x % a.n_src), tid = threadIdx.x;
-  const int held = a.reset ? 0 : cache8_count(a.c, row);
-  if (i >= append_count(a, row, held)) return;
+  const int held = a.reset ? 0 : cache8_count(a.c, row), add = append_count(a, row, held);
+  if (a.n_src == 1) {  // the row's only workgroup does its bookkeeping too
+    __syncthreads();   // every thread has read the count
+    if (tid < 64) append_finish(a, row, held, add);
+  }
+  if (i >= add) return;
   int from = i;
   if (a.src) {
     from = a.src[row * a.ld_src + i];
@@ -159,21 +176,11 @@ __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
   }
 }
 
-// The rows' bookkeeping once every chunk is stored: count, and the new positions' weights; a
-// cache that starts empty also gets its order (position p in slot p).
 __global__ __launch_bounds__(256) void append8_finish_kernel(Append8Args a) {
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, n_cap = a.c.n_cap;
   if (row >= a.c.rows) return;
   const int held = a.reset ? 0 : cache8_count(a.c, row);
-  const int add = append_count(a, row, held);
-  for (int p = lane; p < n_cap; p += 64) {
-    if (a.reset) a.c.order[row * n_cap + p] = p;
-    const int i = p - held;
-    if (a.c.weight && (a.reset || (i >= 0 && i < add)))
-      a.c.weight[row * n_cap + p] = i >= 0 && i < add && a.weight_in ? a.weight_in[row * a.ld_src + i] : 0.f;
-  }
-  if (lane == 0) a.c.count[row] = held + add;
+  append_finish(a, row, held, append_count(a, row, held));
 }
 
 template <int FMT, class T, int DK, int DV>
@@ -182,7 +189,7 @@ hipError_t run_append8(const Append8Args& a, hipStream_t s) {
   if (a.n_src > 0) {
     hipLaunchKernelGGL((append8_kernel<FMT, T, DK, DV, NT>), dim3((unsigned)(a.c.rows * a.n_src)), dim3(NT), 0, s, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.n_src == 1) return e;
   }
   hipLaunchKernelGGL(append8_finish_kernel, dim3((unsigned)((a.c.rows + 3) / 4)), dim3(256), 0, s, a);
   return hipGetLastError();
@@ -195,27 +202,59 @@ hipError_t pick_append8(const Append8Args& a, int dk, int dv, hipStream_t s) {
 
 // ------------------------------------------------------------------------ gate weights
 // w_j = sum over query chunks i > j (below n_b) of the gates that reach tau.  One workgroup per
-// (row, 64 columns); wave w sums rows i = w mod 4, and the four sums are added in that order.
+// (row, 32 columns): V columns to a lane, 32 / V lanes to a row of the matrix, so that a wave's
+// load is whole 128-byte lines, eight loads on their way.  The lanes' sums are added across the
+// wave and then over the four waves, always in that order.  Reads n (n - 1) / 2 floats a head, and
+// the half lines on the diagonal.
+template <int V>
 __global__ __launch_bounds__(256) void gate_weights_kernel(GateWeightsArgs a) {
-  __shared__ float s_sum[4][64];
-  const int blocks = (a.N + 63) / 64, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  constexpr int LPR = 32 / V, RPP = 256 / LPR, U = 8;
+  __shared__ float s_sum[4][32];
+  const int blocks = (a.N + 31) / 32, tid = threadIdx.x;
   const int64_t row = blockIdx.x / blocks;
-  const int j0 = (int)(blockIdx.x % blocks) * 64, j = j0 + lane;
+  const int j0 = (int)(blockIdx.x % blocks) * 32, j = j0 + tid % LPR * V;
   int n = a.N;
   if (a.n_chunks) {
     n = a.n_chunks[row / a.H];
     n = n < 0 ? 0 : (n > a.N ? a.N : n);
   }
-  const float* g = a.gates + row * a.N * (int64_t)a.N;
-  float sum = 0.f;
-  for (int i = j0 + 1 + w; i < n; i += 4)
-    if (j < i) {
-      const float x = g[(int64_t)i * a.N + j];
-      sum += x >= a.tau ? gate_mass(x) : 0.f;
+  const float* g = a.gates + row * a.N * (int64_t)a.N + j;
+  float sum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum[v] = 0.f;
+  for (int i0 = j0 + 1; i0 < n; i0 += RPP * U) {
+    float x[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * RPP + tid / LPR;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[u][v] = 0.f;
+      if (i < n && j < i) {  // (j + V <= N: the vector form has N in whole vectors)
+        const float* p = g + (int64_t)i * a.N;
+        if constexpr (V == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(p);
+          x[u][0] = f.x; x[u][1] = f.y; x[u][2] = f.z; x[u][3] = f.w;
+        } else {
+          x[u][0] = *p;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[u][v] = j + v < i && x[u][v] >= a.tau ? gate_mass(x[u][v]) : 0.f;
+      }
     }
-  s_sum[w][lane] = sum;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum[v] += x[u][v];
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int off = LPR; off < 64; off *= 2) sum[v] += __shfl_xor(sum[v], off, 64);
+    if ((tid & 63) < LPR) s_sum[tid >> 6][(tid & 63) * V + v] = sum[v];
+  }
   __syncthreads();
-  if (w == 0 && j < a.N) a.weight[row * a.N + j] = s_sum[0][lane] + s_sum[1][lane] + s_sum[2][lane] + s_sum[3][lane];
+  if (tid < 32 && j0 + tid < a.N)
+    a.weight[row * a.N + j0 + tid] = s_sum[0][tid] + s_sum[1][tid] + s_sum[2][tid] + s_sum[3][tid];
 }
 
 // ------------------------------------------------------------------------------- evict
@@ -330,8 +369,12 @@ hipError_t launch_append8(const Append8Args& a, int fmt, int dtype, int dk, int 
 }
 
 hipError_t launch_gate_weights(const GateWeightsArgs& a, hipStream_t s) {
-  const int64_t blocks = a.B * a.H * ((a.N + 63) / 64);
-  hipLaunchKernelGGL(gate_weights_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a);
+  const dim3 grid((unsigned)(a.B * a.H * ((a.N + 31) / 32)));
+  // 16-byte loads where every row of the matrix is 16-byte aligned
+  if (a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.gates) & 15) == 0)
+    hipLaunchKernelGGL((gate_weights_kernel<4>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((gate_weights_kernel<1>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -339,8 +382,8 @@ hipError_t launch_evict(const EvictArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.rows + 3) / 4)), block(256), wide((unsigned)a.rows);
   if (a.n <= 64) hipLaunchKernelGGL((evict_kernel<1, 1>), grid, block, 0, s, a);
   else if (a.n <= 256) hipLaunchKernelGGL((evict_kernel<4, 1>), grid, block, 0, s, a);
-  else if (a.n <= 1024) hipLaunchKernelGGL((evict_kernel<16, 1>), grid, block, 0, s, a);
-  else if (a.n <= 4096) hipLaunchKernelGGL((evict_kernel<16, 4>), wide, dim3(256), 0, s, a);
+  else if (a.n <= 1024) hipLaunchKernelGGL((evict_kernel<4, 4>), wide, block, 0, s, a);
+  else if (a.n <= 4096) hipLaunchKernelGGL((evict_kernel<16, 4>), wide, block, 0, s, a);
   else hipLaunchKernelGGL((evict_kernel<16, 16>), wide, dim3(1024), 0, s, a);
   return hipGetLastError();
 }

@@ -715,6 +715,10 @@ def _need_on(t, shape, dtype, device, name):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _call(name, device, *args):
     """Library call on `device`'s current stream (whatever device is current)."""
     fn = getattr(library(), name)
@@ -813,8 +817,8 @@ def cache8_append(cache, At, Bc, reps=None, src=None, n_new=None, weight_in=None
     _need_on(src, (c.Bs, c.H, L), torch.int32, c.device, "src")
     _need_on(n_new, (c.Bs, c.H), torch.int32, c.device, "n_new")
     _need_on(weight_in, (c.Bs, c.H, L), torch.float32, c.device, "weight_in")
-    _call("hla_cache8_append", c.device, c._ref, dt, n, L, _ptr(At), _ptr(Bc), _ptr(reps) if c.n_rep else None, ld_R,
-          _ptr(src), _ptr(n_new), _ptr(weight_in), 1 if reset else 0, 1 if reset_live else 0)
+    _call("hla_cache8_append", c.device, c._ref, dt, n, L, _addr(At), _addr(Bc), _addr(reps) if c.n_rep else None, ld_R,
+          _addr(src), _addr(n_new), _addr(weight_in), 1 if reset else 0, 1 if reset_live else 0)
 
 
 def gdn_decode8(q, k, v, beta, alpha, S_cur, At_cur, cache, gates_in=None, tau=1e-3, o=None, gates_out=None, ws=None):
@@ -852,8 +856,8 @@ def _decode8(fn, gates, q, k, v, S_cur, At_cur, c, gates_in, tau, o, gates_out, 
         ws = _workspace(c._ws_bytes, dev)
     elif ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
-    _call(fn, dev, c._ref, dt, _ptr(q), _ptr(k), _ptr(v), *(_ptr(g) for g in gates), _ptr(S_cur), _ptr(At_cur),
-          _ptr(gates_in), tau, _ptr(o), _ptr(gates_out), _ptr(ws), 0 if ws is None else ws.numel())
+    _call(fn, dev, c._ref, dt, _addr(q), _addr(k), _addr(v), *(_addr(g) for g in gates), _addr(S_cur), _addr(At_cur),
+          _addr(gates_in), tau, _addr(o), _addr(gates_out), _addr(ws), 0 if ws is None else ws.numel())
     return o
 
 
@@ -868,7 +872,7 @@ def gate_weights(gates, tau=1e-3, n_chunks=None, out=None):
     if out is None:
         out = torch.empty((B, H, N), dtype=torch.float32, device=dev)
     _need_on(out, (B, H, N), torch.float32, dev, "out")
-    _call("hla_gate_weights", dev, B, H, N, _ptr(gates), _ptr(n_chunks), tau, _ptr(out))
+    _call("hla_gate_weights", dev, B, H, N, _addr(gates), _addr(n_chunks), tau, _addr(out))
     return out
 
 
@@ -886,8 +890,8 @@ def evict_chunks(weight, count, budget, n_recent=0, order=None, out=None):
         out = tuple(torch.empty(shape, dtype=dtype, device=dev) for shape, dtype, _ in shapes)
     for t, (shape, dtype, name) in zip(out, shapes):
         _need_on(t, shape, dtype, dev, "out " + name)
-    _call("hla_evict_chunks", dev, Bs, H, n, _ptr(weight), _ptr(order), _ptr(count), budget, n_recent,
-          *(_ptr(t) for t in out))
+    _call("hla_evict_chunks", dev, Bs, H, n, _addr(weight), _addr(order), _addr(count), budget, n_recent,
+          *(_addr(t) for t in out))
     return out
 
 
