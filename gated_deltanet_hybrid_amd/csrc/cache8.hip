@@ -48,14 +48,21 @@ struct LiveRows {
   float qe, qk;
 };
 // The columns go their own ways, so the matrix may be W columns of a wider one (rows ld apart).
+template <int DK, int W, int NT> struct LiveRegs {
+  static constexpr int CPR = W / 4, RPP = NT / CPR, NP = DK / RPP;
+  float4 m[NP];
+  __device__ __forceinline__ void load(const float* mat, int ld) {
+    const int col = (threadIdx.x % CPR) * 4, r0 = threadIdx.x / CPR;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) m[p] = load_once(mat + (p * RPP + r0) * ld + col);
+  }
+};
 template <int DK, int W, int NT>
-__device__ __forceinline__ void live_update(float* mat, int ld, const LiveRows& r, const float* w, float* red0,
-                                            float* red1, float* s_u, float* out) {
+__device__ __forceinline__ void live_update(float* mat, int ld, const LiveRegs<DK, W, NT>& in, const LiveRows& r,
+                                            const float* w, float* red0, float* red1, float* s_u, float* out) {
   constexpr int CPR = W / 4, RPP = NT / CPR, NP = DK / RPP;
   const int tid = threadIdx.x, col = (tid % CPR) * 4, r0 = tid / CPR;
-  float4 m[NP];
-#pragma unroll
-  for (int p = 0; p < NP; ++p) m[p] = load_once(mat + (p * RPP + r0) * ld + col);
+  const float4 (&m)[NP] = in.m;
   float4 pu = make_float4(0.f, 0.f, 0.f, 0.f), pz = pu;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
@@ -98,8 +105,8 @@ __device__ __forceinline__ void live_update(float* mat, int ld, const LiveRows& 
 //   int8: the vector as 32-bit fixed point, x = F 2^(e-30) with |x| <= 2^e, and F's four signed
 //         bytes as terms.  The stored bytes enter the int8 product as they are, and its int32
 //         sums are exact; what is rounded is x, to 2^-30 of 2^e.
-//   e4m3: four bf16 terms, each the rounding of what the ones before left (three already hold a
-//         float32), stored numbers converted to bf16 exactly, float32 sums.
+//   e4m3: three bf16 terms (and 0), each the leading eight bits of what the ones before left, which
+//         hold a float32 exactly; stored numbers converted to bf16 exactly, float32 sums.
 // In the product's layout lane l holds row l % 16 and the 16 stored bytes from 64 p + 16 (l / 16)
 // on for each p; column l % 16 is term l % 4, and element i of the sums is row 4 (l / 16) + i.
 // Loaded like that, 16 neighbouring lanes would touch 16 cache lines (measured: 27 GB/s a CU).
@@ -144,15 +151,17 @@ template <int DK> struct Operand<kE4M3, DK> {
   __device__ __forceinline__ static float term_unit() { return 1.f; }
   __device__ __forceinline__ void put(int row0, const float (&x)[4], float) {
     const int term = lane_id() & 3;
-    bf16x4 v;
+    unsigned v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float r = x[i];
-#pragma unroll
-      for (int s = 0; s < 3; ++s) r = s < term ? r - (float)(bf16)r : r;
-      v[i] = (bf16)r;
+      const float r1 = x[i] - cut(x[i]), r2 = r1 - cut(r1);  // (exact)
+      v[i] = __builtin_bit_cast(unsigned, term == 0 ? x[i] : term == 1 ? r1 : term == 2 ? r2 : 0.f);
     }
-    *reinterpret_cast<bf16x4*>(&t[term][row0 + (lane_id() >> 4) * 4]) = v;  // (the same from four lanes)
+    *reinterpret_cast<uint2*>(&t[term][row0 + (lane_id() >> 4) * 4]) =  // (the same from four lanes)
+        make_uint2(__builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u));
+  }
+  __device__ __forceinline__ static float cut(float x) {
+    return __builtin_bit_cast(float, __builtin_bit_cast(unsigned, x) & 0xffff0000u);
   }
   __device__ __forceinline__ Frag get(int p) const {
     const bf16* at = &t[lane_id() & 3][p * 64 + (lane_id() >> 4) * 16];
@@ -236,31 +245,41 @@ template <class Op, int DK, int NW> __device__ __forceinline__ float encode(Op& 
   return (Op::kFixed ? fx.dec : 1.f) + wave_sum_valu(bad);
 }
 
-// The token as the live update takes it, in LDS.
+// The token as the live update takes it, in LDS: thread i fetches element i of everything first
+// (no more elements than threads), so that other loads can be asked for before these are waited for.
 template <class T, int DK, int DV> struct Token {
   float q[DK], k[DK], a[DK], e[DK], ka[DK], qa[DK], w[DV], dot[2];
-  template <int NT> __device__ __forceinline__ LiveRows load(const Decode8Args& in, int64_t row) {
-    const int tid = threadIdx.x;
-    for (int i = tid; i < DK; i += NT) {
-      const float qv = to_f<T>(reinterpret_cast<const T*>(in.q)[row * DK + i]);
-      const float kv = to_f<T>(reinterpret_cast<const T*>(in.k)[row * DK + i]);
-      const float dec = in.ga ? in.ga[row * DK + i] : in.alpha[row];
-      q[i] = qv;
-      k[i] = kv;
-      a[i] = dec;
-      ka[i] = dec * kv;
-      qa[i] = dec * qv;
-      e[i] = (in.ga ? in.gb[row * DK + i] : in.beta[row]) * kv;
+  struct Regs { float q, k, dec, erase, w; };
+  __device__ __forceinline__ static Regs fetch(const Decode8Args& in, int64_t row) {
+    const int i = threadIdx.x;
+    Regs r{0.f, 0.f, 0.f, 0.f, 0.f};
+    if (i < DK) {
+      r.q = to_f<T>(reinterpret_cast<const T*>(in.q)[row * DK + i]);
+      r.k = to_f<T>(reinterpret_cast<const T*>(in.k)[row * DK + i]);
+      r.dec = in.ga ? in.ga[row * DK + i] : in.alpha[row];
+      r.erase = in.ga ? in.gb[row * DK + i] : in.beta[row];
     }
-    for (int i = tid; i < DV; i += NT)
-      w[i] = (in.ga ? in.gw[row * DV + i] : in.beta[row]) * to_f<T>(reinterpret_cast<const T*>(in.v)[row * DV + i]);
+    if (i < DV) r.w = (in.ga ? in.gw[row * DV + i] : in.beta[row]) * to_f<T>(reinterpret_cast<const T*>(in.v)[row * DV + i]);
+    return r;
+  }
+  __device__ __forceinline__ LiveRows store(const Regs& r) {
+    const int i = threadIdx.x;
+    if (i < DK) {
+      q[i] = r.q;
+      k[i] = r.k;
+      a[i] = r.dec;
+      ka[i] = r.dec * r.k;
+      qa[i] = r.dec * r.q;
+      e[i] = r.erase * r.k;
+    }
+    if (i < DV) w[i] = r.w;
     __syncthreads();
-    if (tid < 128) {
-      const float* s = tid < 64 ? k : e;
+    if (i < 128) {
+      const float* s = i < 64 ? k : e;
       float x = 0.f;
-      for (int i = lane_id(); i < DK; i += 64) x += q[i] * s[i];
+      for (int j = lane_id(); j < DK; j += 64) x += q[j] * s[j];
       x = wave_sum_valu(x);
-      if (lane_id() == 0) dot[tid >> 6] = x;
+      if (lane_id() == 0) dot[i >> 6] = x;
     }
     __syncthreads();
     return {ka, qa, a, e, k, dot[1], dot[0]};
@@ -362,6 +381,15 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
   __shared__ unsigned long long s_on[kMaxCache / 64];
   __shared__ __align__(16) Turn<DK> s_turn[NW][kHalf ? 2 : 1 + OT];  // each wave's own
 
+  // what depends on nothing is asked for first
+  typename Token<T, DK, DV>::Regs token{};
+  LiveRegs<DK, DV, NT> live_s;
+  LiveRegs<DK, DK, NT> live_a;
+  if constexpr (!PART) {
+    token = Token<T, DK, DV>::fetch(a, row);
+    live_s.load(a.S_cur + row * DK * DV, DV);
+    live_a.load(a.At_cur + row * DK * DK, DK);
+  }
   const int held = cache8_count(a.c, row), n_cap = a.c.n_cap;
   const int segs = PART ? split_segments(a, held) : 1, seg = PART ? (int)(blockIdx.x % a.segs) : 0;
   if (seg >= segs) return;
@@ -381,10 +409,10 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
   } else {
     __shared__ __align__(16) Token<T, DK, DV> s_token;
     __shared__ __align__(16) float s_score[kScores];
-    const LiveRows lr = s_token.template load<NT>(a, row);
+    const LiveRows lr = s_token.store(token);
     const float q_unit = encode<Op, DK, NW>(s_x[1], s_token.q);
-    live_update<DK, DV, NT>(a.S_cur + row * DK * DV, DV, lr, s_token.w, s_red, s_red + kRed, s_u, s_o[0]);
-    live_update<DK, DK, NT>(a.At_cur + row * DK * DK, DK, lr, nullptr, s_red, s_red + kRed, s_u, s_z);
+    live_update<DK, DV, NT>(a.S_cur + row * DK * DV, DV, live_s, lr, s_token.w, s_red, s_red + kRed, s_u, s_o[0]);
+    live_update<DK, DK, NT>(a.At_cur + row * DK * DK, DK, live_a, lr, nullptr, s_red, s_red + kRed, s_u, s_z);
     if (a.gates_in) {
       for (int j = tid; j < n; j += NT) s_g[j] = take_gate(a, row, j, a.gates_in[row * n_cap + j]);
     } else {
@@ -574,13 +602,14 @@ __global__ __launch_bounds__(256) void split_gates_kernel(Decode8Args a) {
   __shared__ __align__(16) Token<T, DK, DV> s_token;
   if (b < LB) {
     __shared__ __align__(16) float s_red[2][NT * 4], s_u[32], s_out[32];
-    const LiveRows lr = s_token.template load<NT>(a, row);
     const bool state = b < DV / 32;
-    const int c0 = (state ? b : b - DV / 32) * 32;
-    if (state)
-      live_update<DK, 32, NT>(a.S_cur + row * DK * DV + c0, DV, lr, s_token.w + c0, s_red[0], s_red[1], s_u, s_out);
-    else
-      live_update<DK, 32, NT>(a.At_cur + row * DK * DK + c0, DK, lr, nullptr, s_red[0], s_red[1], s_u, s_out);
+    const int c0 = (state ? b : b - DV / 32) * 32, ld = state ? DV : DK;
+    float* mat = (state ? a.S_cur + row * DK * DV : a.At_cur + row * DK * DK) + c0;
+    const typename Token<T, DK, DV>::Regs token = Token<T, DK, DV>::fetch(a, row);
+    LiveRegs<DK, 32, NT> live;
+    live.load(mat, ld);
+    const LiveRows lr = s_token.store(token);
+    live_update<DK, 32, NT>(mat, ld, live, lr, state ? s_token.w + c0 : nullptr, s_red[0], s_red[1], s_u, s_out);
     if (tid < 32) (state ? a.ws.o + row * DV : a.ws.y + row * DK)[c0 + tid] = s_out[tid];
     return;
   }
