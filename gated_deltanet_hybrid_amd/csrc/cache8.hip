@@ -38,63 +38,68 @@ __device__ __forceinline__ void store_once(float* p, float4 x) {
 
 // One read + write pass over a live [DK][W] matrix: mat <- diag(a) mat - e u^T + k w^T with
 // u = (a o k)^T mat, and out = q^T mat (after) = (a o q)^T mat - (q . e) u + (q . k) w.
-// LDS rows: ka = a o k, qa = a o q, a, e, k; w null for the transition.
+// LDS rows: ka = a o k, qa = a o q, a, e, k, and dot = (q . k, q . e); w null for the transition.
+// The columns go their own ways, so the matrix may be W columns of a wider one (rows ld apart).  A
+// thread holds four columns of every RPP-th row; the sums over rows go across the lanes of a wave,
+// then over the waves through LDS (`red`, NT / 64 x 2 W floats).
 struct LiveRows {
   const float* ka;
   const float* qa;
   const float* a;
   const float* e;
   const float* k;
-  float qe, qk;
+  const float* dot;
 };
-// The columns go their own ways, so the matrix may be W columns of a wider one (rows ld apart).
-template <int DK, int W, int NT> struct LiveRegs {
-  static constexpr int CPR = W / 4, RPP = NT / CPR, NP = DK / RPP;
+template <int DK, int W, int NT> struct Live {
+  static constexpr int CPR = W / 4, RPP = NT / CPR, NP = DK / RPP, NW = NT / 64;
   float4 m[NP];
+  __device__ __forceinline__ static int col() { return (threadIdx.x % CPR) * 4; }
+  __device__ __forceinline__ static int row0() { return threadIdx.x / CPR; }
   __device__ __forceinline__ void load(const float* mat, int ld) {
-    const int col = (threadIdx.x % CPR) * 4, r0 = threadIdx.x / CPR;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) m[p] = load_once(mat + (p * RPP + r0) * ld + col);
+    for (int p = 0; p < NP; ++p) m[p] = load_once(mat + (p * RPP + row0()) * ld + col());
+  }
+  __device__ __forceinline__ void sums(const LiveRows& r, float* red) const {
+    float u[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const float kr = r.ka[p * RPP + row0()], qr = r.qa[p * RPP + row0()];
+      const float x[4] = {m[p].x, m[p].y, m[p].z, m[p].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { u[i] += kr * x[i]; z[i] += qr * x[i]; }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { u[i] = stride_sum<CPR>(u[i]); z[i] = stride_sum<CPR>(z[i]); }
+    if (lane_id() < CPR) {
+      float* at = red + (threadIdx.x >> 6) * 2 * W + col();
+      *reinterpret_cast<float4*>(at) = make_float4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<float4*>(at + W) = make_float4(z[0], z[1], z[2], z[3]);
+    }
+  }
+  // column c by one thread: u into red's first row, out
+  __device__ __forceinline__ static float finish(const LiveRows& r, const float* w, float* red, int c) {
+    float u = 0.f, z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) { u += red[i * 2 * W + c]; z += red[i * 2 * W + W + c]; }
+    red[c] = u;
+    return z - r.dot[1] * u + (w ? r.dot[0] * w[c] : 0.f);
+  }
+  __device__ __forceinline__ void store(float* mat, int ld, const LiveRows& r, const float* w, const float* red) const {
+    const float4 uu = *reinterpret_cast<const float4*>(red + col());
+    const float4 ww = w ? *reinterpret_cast<const float4*>(w + col()) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int i = p * RPP + row0();
+      const float ar = r.a[i], er = r.e[i], kr = r.k[i];
+      float4 n;
+      n.x = ar * m[p].x - er * uu.x + kr * ww.x;
+      n.y = ar * m[p].y - er * uu.y + kr * ww.y;
+      n.z = ar * m[p].z - er * uu.z + kr * ww.z;
+      n.w = ar * m[p].w - er * uu.w + kr * ww.w;
+      store_once(mat + i * ld + col(), n);
+    }
   }
 };
-template <int DK, int W, int NT>
-__device__ __forceinline__ void live_update(float* mat, int ld, const LiveRegs<DK, W, NT>& in, const LiveRows& r,
-                                            const float* w, float* red0, float* red1, float* s_u, float* out) {
-  constexpr int CPR = W / 4, RPP = NT / CPR, NP = DK / RPP;
-  const int tid = threadIdx.x, col = (tid % CPR) * 4, r0 = tid / CPR;
-  const float4 (&m)[NP] = in.m;
-  float4 pu = make_float4(0.f, 0.f, 0.f, 0.f), pz = pu;
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const float kr = r.ka[p * RPP + r0], qr = r.qa[p * RPP + r0];
-    pu.x += kr * m[p].x; pu.y += kr * m[p].y; pu.z += kr * m[p].z; pu.w += kr * m[p].w;
-    pz.x += qr * m[p].x; pz.y += qr * m[p].y; pz.z += qr * m[p].z; pz.w += qr * m[p].w;
-  }
-  *reinterpret_cast<float4*>(red0 + r0 * W + col) = pu;
-  *reinterpret_cast<float4*>(red1 + r0 * W + col) = pz;
-  __syncthreads();
-  if (tid < W) {
-    float u = 0.f, z = 0.f;
-    for (int g = 0; g < RPP; ++g) { u += red0[g * W + tid]; z += red1[g * W + tid]; }
-    s_u[tid] = u;
-    out[tid] = z - r.qe * u + (w ? r.qk * w[tid] : 0.f);
-  }
-  __syncthreads();
-  const float4 uu = *reinterpret_cast<const float4*>(s_u + col);
-  const float4 ww = w ? *reinterpret_cast<const float4*>(w + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int i = p * RPP + r0;
-    const float ar = r.a[i], er = r.e[i], kr = r.k[i];
-    float4 n;
-    n.x = ar * m[p].x - er * uu.x + kr * ww.x;
-    n.y = ar * m[p].y - er * uu.y + kr * ww.y;
-    n.z = ar * m[p].z - er * uu.z + kr * ww.z;
-    n.w = ar * m[p].w - er * uu.w + kr * ww.w;
-    store_once(mat + i * ld + col, n);
-  }
-  __syncthreads();
-}
 
 // ---- products of stored rows with a float32 vector on the matrix cores
 //
@@ -262,6 +267,7 @@ template <class T, int DK, int DV> struct Token {
     if (i < DV) r.w = (in.ga ? in.gw[row * DV + i] : in.beta[row]) * to_f<T>(reinterpret_cast<const T*>(in.v)[row * DV + i]);
     return r;
   }
+  // (ends before the dots are written: the live update's barrier is theirs too)
   __device__ __forceinline__ LiveRows store(const Regs& r) {
     const int i = threadIdx.x;
     if (i < DK) {
@@ -281,8 +287,7 @@ template <class T, int DK, int DV> struct Token {
       x = wave_sum_valu(x);
       if (lane_id() == 0) dot[i >> 6] = x;
     }
-    __syncthreads();
-    return {ka, qa, a, e, k, dot[1], dot[0]};
+    return {ka, qa, a, e, k, dot};
   }
 };
 
@@ -364,15 +369,15 @@ __device__ __forceinline__ void chunk_gates(const Decode8Args& a, int64_t row, i
 template <int FMT, class T, int DK, int DV, bool PART>
 __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
   using Op = Operand<FMT, DK>;
-  constexpr int NW = DK / 16, NT = NW * 64, WMAX = DV > DK ? DV : DK, P = 4, KP = DK / 64, PPR = DK / 16;
+  constexpr int NW = DK / 16, NT = NW * 64, P = 4, KP = DK / 64;
   // o's tiles: OT of them to a wave, or where dv < dk one k half of a tile to a wave
   constexpr bool kHalf = DV < DK;
   constexpr int OT = kHalf ? 1 : DV / DK, OP = kHalf ? 1 : KP;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4;
   const int64_t row = PART ? blockIdx.x / a.segs : blockIdx.x;
-  constexpr int kRed = NT * 4;
-  __shared__ __align__(16) float s_u[WMAX], s_o[2][DV], s_z[DK];
-  __shared__ __align__(16) float s_red[2 * kRed > 3 * kMaxCache ? 2 * kRed : 3 * kMaxCache];
+  constexpr int kRed = 2 * NW * (DK + DV);  // the live update's sums, later the chain's lists
+  __shared__ __align__(16) float s_o[2][DV], s_z[DK];
+  __shared__ __align__(16) float s_red[kRed > 3 * kMaxCache ? kRed : 3 * kMaxCache];
   __shared__ __align__(16) unsigned s_max[2][8];
   __shared__ __align__(16) Op s_x[2];
   // by position: slot, scale of A - I and B, and the scale of the representatives, then the gate
@@ -383,8 +388,8 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
 
   // what depends on nothing is asked for first
   typename Token<T, DK, DV>::Regs token{};
-  LiveRegs<DK, DV, NT> live_s;
-  LiveRegs<DK, DK, NT> live_a;
+  Live<DK, DV, NT> live_s;
+  Live<DK, DK, NT> live_a;
   if constexpr (!PART) {
     token = Token<T, DK, DV>::fetch(a, row);
     live_s.load(a.S_cur + row * DK * DV, DV);
@@ -411,8 +416,17 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
     __shared__ __align__(16) float s_score[kScores];
     const LiveRows lr = s_token.store(token);
     const float q_unit = encode<Op, DK, NW>(s_x[1], s_token.q);
-    live_update<DK, DV, NT>(a.S_cur + row * DK * DV, DV, live_s, lr, s_token.w, s_red, s_red + kRed, s_u, s_o[0]);
-    live_update<DK, DK, NT>(a.At_cur + row * DK * DK, DK, live_a, lr, nullptr, s_red, s_red + kRed, s_u, s_z);
+    float *red_s = s_red, *red_a = s_red + 2 * NW * DV;
+    live_s.sums(lr, red_s);
+    live_a.sums(lr, red_a);
+    __syncthreads();
+    for (int c = tid; c < DV + DK; c += NT) {
+      if (c < DV) s_o[0][c] = live_s.finish(lr, s_token.w, red_s, c);
+      else s_z[c - DV] = live_a.finish(lr, nullptr, red_a, c - DV);
+    }
+    __syncthreads();
+    live_s.store(a.S_cur + row * DK * DV, DV, lr, s_token.w, red_s);
+    live_a.store(a.At_cur + row * DK * DK, DK, lr, nullptr, red_a);
     if (a.gates_in) {
       for (int j = tid; j < n; j += NT) s_g[j] = take_gate(a, row, j, a.gates_in[row * n_cap + j]);
     } else {
@@ -422,7 +436,7 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
       for (int j = n + tid; j < n_cap; j += NT) a.gates_out[row * n_cap + j] = 0.f;
   }
   __syncthreads();
-  for (int i = w; i < kMaxCache / 64; i += NW) {
+  for (int i = w; i < (n + 63) / 64; i += NW) {
     const int j = 64 * i + lane;
     const unsigned long long on = __ballot(j < n && s_g[j] != 0.f);
     if (lane == 0) s_on[i] = on;
@@ -601,16 +615,20 @@ __global__ __launch_bounds__(256) void split_gates_kernel(Decode8Args a) {
   const int b = (int)(blockIdx.x % blocks);
   __shared__ __align__(16) Token<T, DK, DV> s_token;
   if (b < LB) {
-    __shared__ __align__(16) float s_red[2][NT * 4], s_u[32], s_out[32];
+    __shared__ __align__(16) float s_red[NT / 64 * 64];
     const bool state = b < DV / 32;
     const int c0 = (state ? b : b - DV / 32) * 32, ld = state ? DV : DK;
     float* mat = (state ? a.S_cur + row * DK * DV : a.At_cur + row * DK * DK) + c0;
     const typename Token<T, DK, DV>::Regs token = Token<T, DK, DV>::fetch(a, row);
-    LiveRegs<DK, 32, NT> live;
+    Live<DK, 32, NT> live;
     live.load(mat, ld);
     const LiveRows lr = s_token.store(token);
-    live_update<DK, 32, NT>(mat, ld, live, lr, state ? s_token.w + c0 : nullptr, s_red[0], s_red[1], s_u, s_out);
-    if (tid < 32) (state ? a.ws.o + row * DV : a.ws.y + row * DK)[c0 + tid] = s_out[tid];
+    const float* w = state ? s_token.w + c0 : nullptr;
+    live.sums(lr, s_red);
+    __syncthreads();
+    if (tid < 32) (state ? a.ws.o + row * DV : a.ws.y + row * DK)[c0 + tid] = live.finish(lr, w, s_red, tid);
+    __syncthreads();
+    live.store(mat, ld, lr, w, s_red);
     return;
   }
   const int n = cache8_count(a.c, row), n_cap = a.c.n_cap;
