@@ -301,7 +301,8 @@ __device__ __forceinline__ float take_gate(const Decode8Args& a, int64_t row, in
 
 // Gates of the positions [lo, hi) whose slots and representatives' scales are slot[j - lo] and
 // g[j - lo], which becomes the gate.  The block works through them kScores scores at a time: 16
-// representatives a product, then eight lanes a chunk for the log-mean-exp.
+// representatives a product, then the log-mean-exp by eight lanes a chunk, or a wave where a chunk
+// has more than 32 representatives (64 of them by eight lanes took as long as their products).
 constexpr int kScores = 1024;  // n_rep <= 256: at least four chunks
 template <int FMT, int DK, int NW>
 __device__ __forceinline__ void chunk_gates(const Decode8Args& a, int64_t row, int lo, int hi, const int* slot, float* g,
@@ -338,19 +339,30 @@ __device__ __forceinline__ void chunk_gates(const Decode8Args& a, int64_t row, i
         *reinterpret_cast<float4*>(s_score + r0 + (lane >> 4) * 4) = make_float4(s[0], s[1], s[2], s[3]);
     }
     __syncthreads();
-    for (int jj = tid >> 3; jj < nj; jj += NT / 8) {
-      const float sc = g[j0 + jj] * unit;
-      const float* score = s_score + jj * n_rep;
-      float m = -INFINITY, sum = 0.f;
-      for (int r = tid & 7; r < n_rep; r += 8) m = fmaxf(m, score[r] * sc);
-      m = fmaxf(m, dpp_f<0xB1>(m));
-      m = fmaxf(m, dpp_f<0x4E>(m));
-      m = fmaxf(m, dpp_f<0x141>(m));
-      for (int r = tid & 7; r < n_rep; r += 8) sum += expf(score[r] * sc - m);
-      sum = group_sum<8>(sum);
-      if ((tid & 7) == 0)
-        g[j0 + jj] = take_gate(a, row, lo + j0 + jj, 1.f / (1.f + expf(-(m + logf(sum / (float)n_rep)))));
-    }
+    auto gates_of = [&](auto lanes) __attribute__((always_inline)) {  // that many lanes a chunk
+      constexpr int G = lanes;
+      for (int jj = tid / G; jj < nj; jj += NT / G) {
+        const float sc = g[j0 + jj] * unit;
+        const float* score = s_score + jj * n_rep;
+        float m = -INFINITY, sum = 0.f;
+        for (int r = tid % G; r < n_rep; r += G) m = fmaxf(m, score[r] * sc);
+        if constexpr (G == 64) {
+          m = wave_max_valu(m);
+        } else {
+          m = fmaxf(m, dpp_f<0xB1>(m));
+          m = fmaxf(m, dpp_f<0x4E>(m));
+          m = fmaxf(m, dpp_f<0x141>(m));
+        }
+        // (the fast exponential's error is that of the argument's product with log2 e, |x| 2^-24
+        // of e^x: for x <= 0 less than 2^-25 of the largest term)
+        for (int r = tid % G; r < n_rep; r += G) sum += __expf(score[r] * sc - m);
+        sum = lane_group_sum<G>(sum);
+        if (tid % G == 0)
+          g[j0 + jj] = take_gate(a, row, lo + j0 + jj, 1.f / (1.f + expf(-(m + logf(sum / (float)n_rep)))));
+      }
+    };
+    if (n_rep > 32) gates_of(std::integral_constant<int, 64>{});
+    else gates_of(std::integral_constant<int, 8>{});
     __syncthreads();
   }
 }
