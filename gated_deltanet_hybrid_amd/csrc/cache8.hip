@@ -27,6 +27,12 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
   const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
   return make_uint4(v.x, v.y, v.z, v.w);
 }
+// (The vector type matters for an ordinary load too: one of uint4's own components is copied, and so
+// waited for, where it is held across a loop.)
+__device__ __forceinline__ uint4 load_keep(const uint8_t* p) {
+  const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
 __device__ __forceinline__ float4 load_once(const float* p) {
   const f32x4v v = __builtin_nontemporal_load(reinterpret_cast<const f32x4v*>(p));
   return make_float4(v.x, v.y, v.z, v.w);
@@ -316,28 +322,43 @@ __device__ __forceinline__ void chunk_gates(const Decode8Args& a, int64_t row, i
   const float qu = q_unit * Op::term_unit();
   const int per = kScores / n_rep;  // chunks a block of scores holds
   const unsigned inv = ((1u << 20) + n_rep - 1) / n_rep;  // r / n_rep = r inv >> 20 for r < 1024, n_rep <= 256
+  const uint8_t* reps = a.c.reps + row * a.c.n_cap * (int64_t)n_rep * DK;
   const float unit = 1.f / sqrtf((float)DK);
   for (int j0 = 0; j0 < hi - lo; j0 += per) {
     const int nj = hi - lo - j0 < per ? hi - lo - j0 : per, rows = nj * n_rep;
-    for (int r0 = w * 16; r0 < rows; r0 += NW * 16) {
-      uint4 raw[KP], frag[KP];
+    // a piece is 16 rows; four of a wave's are on their way, past the end the last row again
+    constexpr int AHEAD = 4;
+    uint4 ring[AHEAD][KP];
+    auto ask = [&](uint4 (&t)[KP], int r0) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
-        const int r = r0 + i * 8 + lane / PPR < rows ? r0 + i * 8 + lane / PPR : rows - 1;
-        const int jj = (int)((unsigned)r * inv >> 20);
-        const int64_t at = (row * a.c.n_cap + slot[j0 + jj]) * n_rep + (r - jj * n_rep);
-        raw[i] = *reinterpret_cast<const uint4*>(a.c.reps + at * DK + lane % PPR * 16);
+        // (the row's representatives span at most 2^25 bytes; every factor fits 24 bits)
+        const int at = r0 + i * 8 + lane / PPR, r = at < rows ? at : rows - 1;
+        const int jj = (int)(__umul24(r, inv) >> 20);
+        t[i] = load_keep(reps + ((unsigned)(__mul24(slot[j0 + jj] - jj, n_rep) + r) * DK + lane % PPR * 16));
       }
-      turn.turn(raw, frag);
-      typename Op::Acc acc = {0, 0, 0, 0};
+    };
+    if (w * 16 < rows) {
 #pragma unroll
-      for (int p = 0; p < KP; ++p) acc = Op::step(frag[p], qf[p], acc);
-      float s[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = terms_sum((float)acc[i], qu);
-      if ((lane & 15) == 0)
-        *reinterpret_cast<float4*>(s_score + r0 + (lane >> 4) * 4) = make_float4(s[0], s[1], s[2], s[3]);
+      for (int i = 0; i < AHEAD; ++i) ask(ring[i], (w + i * NW) * 16);
     }
+    for (int base = w * 16; base < rows; base += NW * 16 * AHEAD)
+      static_for<0, AHEAD>([&](auto I) __attribute__((always_inline)) {
+        const int r0 = base + I * NW * 16;
+        uint4 frag[KP];
+        turn.turn(ring[I], frag);
+        ask(ring[I], r0 + NW * 16 * AHEAD);
+        if (r0 < rows) {
+          typename Op::Acc acc = {0, 0, 0, 0};
+#pragma unroll
+          for (int p = 0; p < KP; ++p) acc = Op::step(frag[p], qf[p], acc);
+          float s[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] = terms_sum((float)acc[i], qu);
+          if ((lane & 15) == 0)
+            *reinterpret_cast<float4*>(s_score + r0 + (lane >> 4) * 4) = make_float4(s[0], s[1], s[2], s[3]);
+        }
+      });
     __syncthreads();
     auto gates_of = [&](auto lanes) __attribute__((always_inline)) {  // that many lanes a chunk
       constexpr int G = lanes;

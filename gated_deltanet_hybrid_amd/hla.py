@@ -868,6 +868,8 @@ def gate_weights(gates, tau=1e-3, n_chunks=None, out=None):
     """Weights that a prefill's gates [B, H, N, N] (as route_mix gives them) put on every chunk:
     the sum over the later query chunks of the gates that reach tau.  n_chunks [B] int32: valid
     chunks per batch row.  Returns [B, H, N] float32."""
+    if gates.dim() != 4 or not gates.is_cuda:
+        raise ValueError("gates must be a CUDA tensor [B, H, N, N]")
     B, H, N, _ = gates.shape
     dev = gates.device
     _need_on(gates, (B, H, N, N), torch.float32, dev, "gates")
@@ -884,6 +886,8 @@ def evict_chunks(weight, count, budget, n_recent=0, order=None, out=None):
     the lightest leave (of equal ones the older).  weight [Bs, H, n], count [Bs, H] int32, order
     [Bs, H, n] int32 or None.  Returns (order, weight, count): the chunks that stay in time order,
     then those that left; `out` may be the inputs."""
+    if weight.dim() != 3 or not weight.is_cuda:
+        raise ValueError("weight must be a CUDA tensor [Bs, H, n]")
     Bs, H, n = weight.shape
     dev = weight.device
     shapes = (((Bs, H, n), torch.int32, "order"), ((Bs, H, n), torch.float32, "weight"), ((Bs, H), torch.int32, "count"))
@@ -917,6 +921,8 @@ def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
     dv, full = Bc.shape[-1], T // C
     if N != math.ceil(T / C):
         raise ValueError("T and C do not match the prefill's chunks")
+    if cache.n_rep and r["reps"].shape[1] != N * cache.n_rep and (r["reps"].shape[1], cache.n_rep) != (T, C):
+        raise ValueError("the cache's representatives per chunk are not the prefill's")
     keep = cache.n_cap if budget is None else min(budget, cache.n_cap)
     weight = gate_weights(r["gates"], tau=tau)
     count = torch.full((B, H), full, dtype=torch.int32, device=At.device)

@@ -145,3 +145,12 @@ def test_oracle_evict():
     assert o.tolist() == [4, 1, 2, 0, 3] and w.tolist() == [3, 0, 0, 0, 0] and c == 2  # the newest stays, of 1, 1 both go
     o, w, c = o8.evict(np.array([1, np.nan, 1, 2], np.float32), np.arange(4), 4, 2, 0)
     assert o.tolist() == [2, 3, 0, 1] and w.tolist() == [1, 2, 0, 0] and c == 2
+
+
+def test_python_refuses_host_arrays():
+    with pytest.raises(ValueError):
+        hla.gate_weights(torch.zeros(1, 1, 2, 2))
+    with pytest.raises(ValueError):
+        hla.evict_chunks(torch.zeros(1, 1, 2), torch.zeros(1, 1, dtype=torch.int32), 1)
+    with pytest.raises(KeyError):
+        hla.cache8_alloc(1, 1, 2, 64, 64, fmt="int4")
