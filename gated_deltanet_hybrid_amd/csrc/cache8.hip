@@ -208,15 +208,6 @@ template <int DK> struct Turn {
     for (int p = 0; p < KP; ++p) frag[p] = t[piece(l & 15, 4 * p + (l >> 4))];
     __builtin_amdgcn_wave_barrier();
   }
-  // one k half (64 bytes) of 16 rows: raw is piece 4 half + l % 4 of row l / 4
-  __device__ __forceinline__ uint4 turn_half(const uint4& raw) {
-    const int l = lane_id();
-    t[(l >> 2) * 4 + ((l & 3) ^ (l >> 3 & 3))] = raw;
-    __builtin_amdgcn_wave_barrier();
-    const uint4 f = t[(l & 15) * 4 + ((l >> 4) ^ (l >> 1 & 3))];
-    __builtin_amdgcn_wave_barrier();
-    return f;
-  }
 };
 
 // 2^(30-e) for the least e in reach with bound < 2^e, and its counterpart 2^(e-30) = 1 / enc.
@@ -388,11 +379,13 @@ __device__ __forceinline__ void chunk_gates(const Decode8Args& a, int64_t row, i
   }
 }
 
-// One workgroup per (sequence, head), a wave for every 16 rows of E: the live update, the gates
-// (16 representatives a product, their scores through LDS in blocks of whole chunks), then the
-// chain.  In the chain wave w owns z's rows 16 w .. and its share of o's; a chunk's new z becomes
-// terms in the other of two LDS buffers, so one barrier a chunk is enough, and the raw bytes of
-// the next P chunks are on their way to registers meanwhile.
+// One workgroup per (sequence, head), a wave for every 16 rows of a chunk's record: dk / 16 waves
+// own z with E's rows, dv / 16 own o with B's.  First the live update, the gates (16
+// representatives a product, their scores through LDS in blocks of whole chunks), then the chain:
+// every wave multiplies its 16 rows with z, and a chunk's new z becomes terms in the other of two
+// LDS buffers, so one barrier a chunk is enough.  The raw bytes of the next P chunks are on their
+// way to registers meanwhile.  Only z's waves are on the path from one chunk to the next (with both
+// parts in the same waves decode_skip took 40 us instead of 34; giving z's waves priority changed nothing).
 // int8 needs a bound of |z| before z is known to every wave.  The largest |z| is exchanged with
 // the terms, and the next z is at most (1 + |ghat sA| 128 dk) times that; where this factor is
 // over 2^7 (a term would then hold fewer than 23 bits of the largest |z|), the waves exchange the
@@ -400,33 +393,33 @@ __device__ __forceinline__ void chunk_gates(const Decode8Args& a, int64_t row, i
 // PART: the chain over one segment of a row's positions for the split form below: gates, live part
 // and the z that enters come from the workspace, and o's share goes there.
 template <int FMT, class T, int DK, int DV, bool PART>
-__global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
+__global__ __launch_bounds__((DK + DV) * 4) void decode8_kernel(Decode8Args a) {
   using Op = Operand<FMT, DK>;
-  constexpr int NW = DK / 16, NT = NW * 64, P = 4, KP = DK / 64;
-  // o's tiles: OT of them to a wave, or where dv < dk one k half of a tile to a wave
-  constexpr bool kHalf = DV < DK;
-  constexpr int OT = kHalf ? 1 : DV / DK, OP = kHalf ? 1 : KP;
+  constexpr int NZ = DK / 16, NW = NZ + DV / 16, NT = NW * 64, P = 4, KP = DK / 64;
+  constexpr int LT = 512;  // threads of the live update, at most NT
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4;
   const int64_t row = PART ? blockIdx.x / a.segs : blockIdx.x;
-  constexpr int kRed = 2 * NW * (DK + DV);  // the live update's sums, later the chain's lists
-  __shared__ __align__(16) float s_o[2][DV], s_z[DK];
+  constexpr int kRed = 2 * (LT / 64) * (DK + DV);  // the live update's sums, later the chain's lists
+  __shared__ __align__(16) float s_o[DV], s_z[DK];
   __shared__ __align__(16) float s_red[kRed > 3 * kMaxCache ? kRed : 3 * kMaxCache];
-  __shared__ __align__(16) unsigned s_max[2][8];
+  __shared__ __align__(16) unsigned s_max[2][NZ];
   __shared__ __align__(16) Op s_x[2];
   // by position: slot, scale of A - I and B, and the scale of the representatives, then the gate
   __shared__ int s_slot[kMaxCache];
   __shared__ float s_sa[kMaxCache], s_sb[kMaxCache], s_g[kMaxCache];
   __shared__ unsigned long long s_on[kMaxCache / 64];
-  __shared__ __align__(16) Turn<DK> s_turn[NW][kHalf ? 2 : 1 + OT];  // each wave's own
+  __shared__ __align__(16) Turn<DK> s_turn[NW];  // each wave's own
 
   // what depends on nothing is asked for first
   typename Token<T, DK, DV>::Regs token{};
-  Live<DK, DV, NT> live_s;
-  Live<DK, DK, NT> live_a;
+  Live<DK, DV, LT> live_s;
+  Live<DK, DK, LT> live_a;
   if constexpr (!PART) {
     token = Token<T, DK, DV>::fetch(a, row);
-    live_s.load(a.S_cur + row * DK * DV, DV);
-    live_a.load(a.At_cur + row * DK * DK, DK);
+    if (tid < LT) {
+      live_s.load(a.S_cur + row * DK * DV, DV);
+      live_a.load(a.At_cur + row * DK * DK, DK);
+    }
   }
   const int held = cache8_count(a.c, row), n_cap = a.c.n_cap;
   const int segs = PART ? split_segments(a, held) : 1, seg = PART ? (int)(blockIdx.x % a.segs) : 0;
@@ -443,27 +436,31 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
   if constexpr (PART) {
     const float* from = segs == 1 ? a.ws.y + row * DK : a.ws.z + (row * a.segs + seg) * DK;
     if (tid < DK) s_z[tid] = from[tid];
-    if (tid < DV) s_o[0][tid] = segs == 1 ? a.ws.o[row * DV + tid] : 0.f;
+    if (tid < DV) s_o[tid] = segs == 1 ? a.ws.o[row * DV + tid] : 0.f;
   } else {
     __shared__ __align__(16) Token<T, DK, DV> s_token;
     __shared__ __align__(16) float s_score[kScores];
     const LiveRows lr = s_token.store(token);
     const float q_unit = encode<Op, DK, NW>(s_x[1], s_token.q);
-    float *red_s = s_red, *red_a = s_red + 2 * NW * DV;
-    live_s.sums(lr, red_s);
-    live_a.sums(lr, red_a);
+    float *red_s = s_red, *red_a = s_red + 2 * (LT / 64) * DV;
+    if (tid < LT) {
+      live_s.sums(lr, red_s);
+      live_a.sums(lr, red_a);
+    }
     __syncthreads();
     for (int c = tid; c < DV + DK; c += NT) {
-      if (c < DV) s_o[0][c] = live_s.finish(lr, s_token.w, red_s, c);
+      if (c < DV) s_o[c] = live_s.finish(lr, s_token.w, red_s, c);
       else s_z[c - DV] = live_a.finish(lr, nullptr, red_a, c - DV);
     }
     __syncthreads();
-    live_s.store(a.S_cur + row * DK * DV, DV, lr, s_token.w, red_s);
-    live_a.store(a.At_cur + row * DK * DK, DK, lr, nullptr, red_a);
+    if (tid < LT) {
+      live_s.store(a.S_cur + row * DK * DV, DV, lr, s_token.w, red_s);
+      live_a.store(a.At_cur + row * DK * DK, DK, lr, nullptr, red_a);
+    }
     if (a.gates_in) {
       for (int j = tid; j < n; j += NT) s_g[j] = take_gate(a, row, j, a.gates_in[row * n_cap + j]);
     } else {
-      chunk_gates<FMT, DK, NW>(a, row, 0, n, s_slot, s_g, s_x[1], q_unit, s_turn[w][0], s_score);
+      chunk_gates<FMT, DK, NW>(a, row, 0, n, s_slot, s_g, s_x[1], q_unit, s_turn[w], s_score);
     }
     if (a.gates_out)
       for (int j = n + tid; j < n_cap; j += NT) a.gates_out[row * n_cap + j] = 0.f;
@@ -475,27 +472,23 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
     if (lane == 0) s_on[i] = on;
   }
   float unit = encode<Op, DK, NW>(s_x[0], s_z);  // 2^(e-30) of the operand in use
-  float z[4], o[OT][4];
+  float acc[4];  // the lane's rows of z, or its terms' shares of its rows of o
 #pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = s_z[16 * w + g * 4 + i];
-#pragma unroll
-  for (int t = 0; t < OT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+  for (int i = 0; i < 4; ++i) acc[i] = w < NZ ? s_z[16 * w + g * 4 + i] : 0.f;
   auto share_max = [&](int buf) {
-    const unsigned m = rows_max(max_u(max_u(mag(z[0]), mag(z[1])), max_u(mag(z[2]), mag(z[3]))));
+    const unsigned m = rows_max(max_u(max_u(mag(acc[0]), mag(acc[1])), max_u(mag(acc[2]), mag(acc[3]))));
     s_max[buf][w] = m;  // the same from every lane
   };
   auto read_max = [&](int buf) {
     unsigned m = 0;
 #pragma unroll
-    for (int i = 0; i < NW; i += 4) {
+    for (int i = 0; i < NZ; i += 4) {
       const uint4 x = *reinterpret_cast<const uint4*>(&s_max[buf][i]);
       m = max_u(max_u(m, max_u(x.x, x.y)), max_u(x.z, x.w));
     }
     return m;
   };
-  if (Op::kFixed) share_max(0);
+  if (Op::kFixed && w < NZ) share_max(0);
   __syncthreads();
   // the chunks in use, newest first: slot, ghat sA, ghat sB (in the live update's LDS)
   int* l_slot = reinterpret_cast<int*>(s_red);
@@ -515,81 +508,55 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
   __syncthreads();
 
   // ---- chain
-  struct Raw { uint4 z[KP], o[OT][OP]; };
+  struct Raw { uint4 t[KP]; };
   const uint8_t* base = a.c.maps + row * n_cap * (int64_t)((DK + DV) * DK);
-  const unsigned at_z = w * 16 * DK + lane * 16;
-  const unsigned at_o = DK * DK + (kHalf ? ((w >> 1) * 16 + lane / 4) * DK + (w & 1) * 64 + lane % 4 * 16
-                                         : OT * w * 16 * DK + lane * 16);
-  auto load = [&](Raw& r, int slot) {
+  const unsigned at = w * 16 * DK + lane * 16;
+  auto load = [&](Raw& r, int slot) __attribute__((always_inline)) {
     const uint8_t* m = base + (int64_t)__builtin_amdgcn_readfirstlane(slot) * ((DK + DV) * DK);
 #pragma unroll
-    for (int p = 0; p < KP; ++p) r.z[p] = load_once(m + (at_z + p * 1024));
-#pragma unroll
-    for (int t = 0; t < OT; ++t)
-#pragma unroll
-      for (int p = 0; p < OP; ++p) r.o[t][p] = load_once(m + (at_o + t * 16 * DK + p * 1024));
+    for (int p = 0; p < KP; ++p) r.t[p] = load_once(m + (at + p * 1024));
   };
   const float tu = Op::term_unit();
   Raw frag;  // the chunk in work, in the products' layout
-  auto turn = [&](const Raw& r) {
-    s_turn[w][0].turn(r.z, frag.z);
-    if constexpr (kHalf) {
-      frag.o[0][0] = s_turn[w][1].turn_half(r.o[0][0]);
-    } else {
-#pragma unroll
-      for (int t = 0; t < OT; ++t) s_turn[w][1 + t].turn(r.o[t], frag.o[t]);
-    }
-  };
   int buf = 0;
-  // Chunk `it`.  The products come first; then the chunk behind (`ring`) is turned and the one P
+  // Chunk `it`.  The product comes first; then the chunk behind (`ring`) is turned and the one P
   // behind that asked for, and the LDS and memory work on those while z is brought up to date.
   auto process = [&](int it, Raw& ring) __attribute__((always_inline)) {
     const bool live = it < used;
     const float ca = live ? l_ca[it] : 0.f, cb = live ? l_cb[it] : 0.f;
     const int slot = l_slot[it + 1 + P < used ? it + 1 + P : used - 1];
-    typename Op::Frag x[KP], xo;
+    typename Op::Acc sums = {0, 0, 0, 0};
 #pragma unroll
-    for (int p = 0; p < KP; ++p) x[p] = s_x[buf].get(p);
-    if constexpr (kHalf) xo = s_x[buf].get(w & 1);
-    float us = unit * tu, bound = 0.f;
+    for (int p = 0; p < KP; ++p) sums = Op::step(frag.t[p], s_x[buf].get(p), sums);
+    float us = unit * tu;
+    Fixed fx{1.f, 1.f};
+    bool measure = false;  // (the same in every thread)
     if constexpr (Op::kFixed) {
       const unsigned m = read_max(buf);
       us = m >= kInf ? __builtin_nanf("") : us;  // a z that is not finite makes NaN of all behind it
-      bound = __builtin_bit_cast(float, m);
+      const float factor = 1.f + fabsf(ca) * (128.f * DK);
+      measure = !(factor <= 128.f);
+      fx = fixed_for(__builtin_bit_cast(float, m) * factor);
     }
     buf ^= 1;
-    typename Op::Acc acc = {0, 0, 0, 0}, ao[OT];
-#pragma unroll
-    for (int p = 0; p < KP; ++p) acc = Op::step(frag.z[p], x[p], acc);
-#pragma unroll
-    for (int t = 0; t < OT; ++t) {
-      ao[t] = typename Op::Acc{0, 0, 0, 0};
-#pragma unroll
-      for (int p = 0; p < OP; ++p) ao[t] = Op::step(frag.o[t][p], kHalf ? xo : x[p], ao[t]);
-    }
-    turn(ring);
+    s_turn[w].turn(ring.t, frag.t);
     load(ring, slot);
-    const float cz = ca * us, co = cb * us;
+    if (w < NZ) {
+      const float cz = ca * us;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] += terms_sum((float)acc[i], cz);
-    Fixed fx{1.f, 1.f};
-    if constexpr (Op::kFixed) {
-      const float factor = 1.f + fabsf(ca) * (128.f * DK);
-      share_max(buf);
-      if (factor <= 128.f) {
-        fx = fixed_for(bound * factor);
-      } else {
-        __syncthreads();
-        fx = fixed_for(__builtin_bit_cast(float, read_max(buf)));
-      }
-      unit = fx.dec;
+      for (int i = 0; i < 4; ++i) acc[i] += terms_sum((float)sums[i], cz);
+      if (Op::kFixed) share_max(buf);
+    } else if (live) {  // each lane keeps its own term's share until the end
+      const float co = cb * us;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += co * (float)sums[i];
     }
-    s_x[buf].put(16 * w, z, fx.enc);
-    if (live)
-#pragma unroll
-      for (int t = 0; t < OT; ++t)  // each lane keeps its own term's share until the end
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[t][i] += co * (float)ao[t][i];
+    if (measure) {
+      __syncthreads();
+      fx = fixed_for(__builtin_bit_cast(float, read_max(buf)));
+    }
+    if (w < NZ) s_x[buf].put(16 * w, acc, fx.enc);
+    if constexpr (Op::kFixed) unit = fx.dec;
     __syncthreads();
   };
   if (used > 0) {
@@ -599,39 +566,27 @@ __global__ __launch_bounds__(DK * 4, 2) void decode8_kernel(Decode8Args a) {
     for (int i = 0; i < P; ++i) load(ring[i], l_slot[i + 1 < used ? i + 1 : used - 1]);
     {
       const Raw first = frag;
-      turn(first);
+      s_turn[w].turn(first.t, frag.t);
     }
     // Past the end the last chunk is loaded again, and composed with gate 0: a load under a
     // condition would make every wait for a load one for all of them.
     for (int it = 0; it < used; it += P) static_for<0, P>([&](auto I) { process(it + I, ring[I]); });
   }
-  // o: live part + the chain's, whose two k halves (dv < dk) meet in LDS
-  float sum[OT][4];
+  if (w >= NZ) {  // o: the live part and the chain's
+    const int c = (w - NZ) * 16 + g * 4;
+    float* out = (segs == 1 ? a.o + row * DV : a.ws.part + (row * a.segs + seg) * DV) + c;
 #pragma unroll
-  for (int t = 0; t < OT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[t][i] = group_sum<4>(o[t][i]);
-  if constexpr (kHalf) {
-    if ((w & 1) && (lane & 15) == 0)
-      *reinterpret_cast<float4*>(&s_o[1][(w >> 1) * 16 + g * 4]) = make_float4(sum[0][0], sum[0][1], sum[0][2], sum[0][3]);
-    __syncthreads();
-  }
-  if ((lane & 15) == 0 && !(kHalf && (w & 1))) {
-#pragma unroll
-    for (int t = 0; t < OT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = (kHalf ? w >> 1 : OT * w + t) * 16 + g * 4 + i;
-        float* out = segs == 1 ? a.o + row * DV : a.ws.part + (row * a.segs + seg) * DV;
-        out[c] = s_o[0][c] + sum[t][i] + (kHalf ? s_o[1][c] : 0.f);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float sum = group_sum<4>(acc[i]);
+      if ((lane & 15) == 0) out[i] = s_o[c + i] + sum;
+    }
   }
 }
 
 // ---- the split form, for few rows
 //
-// A chain is a sequence of dependent products on one CU (about 0.6 us a chunk; the CU draws some 54
-// GB/s), so with few rows most of the card would wait.  The positions are cut into segments of
+// A chain is a sequence of dependent products on one CU (0.65 us a chunk at dk = 128; the CU draws
+// some 50 GB/s), so with few rows most of the card would wait.  The positions are cut into segments of
 // seg_len.  For every segment but the oldest all workgroups at once compose the linear parts,
 //   Phi_s = product over its chunks, newest first, of (I + ghat sA E),
 // a matrix product a chunk instead of a vector's; then one workgroup a row takes z through the
@@ -698,7 +653,8 @@ __global__ __launch_bounds__(256) void split_gates_kernel(Decode8Args a) {
 // bf16 terms (24 bits: float32).  Wave w owns P's columns 32 w .., for which an accumulator tile
 // is, register for register, the next product's B operand; so P never leaves the wave, and the
 // waves share only E, which they bring to LDS as A fragments, a chunk ahead, in two buffers.
-// Bound by the products (3 x 2 dk^3 flops a chunk) and the splitting of P on the vector units.
+// Bound by the products, 3 x 2 dk^3 flops a chunk: 16 rows of 1024 chunks (dk = 128, 0.2 Tflop) take
+// 190 us, 1.06 Pflop/s, where a large library product of bf16 matrices reaches 1.21 on this card.
 template <int FMT, int DK>
 __global__ __launch_bounds__(DK * 2, 2) void split_compose_kernel(Decode8Args a, int rec) {
   constexpr int NT = DK * 2, RT = DK / 32, KS = DK / 16, PER = DK * DK / 16 / NT, FR = 1024 + 16;
@@ -871,7 +827,7 @@ hipError_t run_decode8(const Decode8Args& a, hipStream_t s) {
   TimedLaunch tl(HLA_KERNEL_DECODE, s);
   const unsigned rows = (unsigned)a.c.rows;
   if (a.segs == 0) {
-    hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV, false>), dim3(rows), dim3(DK * 4), 0, s, a);
+    hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV, false>), dim3(rows), dim3((DK + DV) * 4), 0, s, a);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((split_gates_kernel<FMT, T, DK, DV>), dim3(rows * ((DK + DV) / 32 + a.gate_blocks)), dim3(256), 0, s, a);
@@ -883,7 +839,7 @@ hipError_t run_decode8(const Decode8Args& a, hipStream_t s) {
   hipLaunchKernelGGL((split_join_kernel<DK>), dim3(rows), dim3(DK * 4), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV, true>), dim3(rows * a.segs), dim3(DK * 4), 0, s, a);
+  hipLaunchKernelGGL((decode8_kernel<FMT, T, DK, DV, true>), dim3(rows * a.segs), dim3((DK + DV) * 4), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(split_sum_kernel, dim3(rows), dim3(128), 0, s, a, DV);
@@ -897,18 +853,17 @@ hipError_t pick_decode8(const Decode8Args& a, int dk, int dv, hipStream_t s) {
 
 }  // namespace
 
-// Which form a call takes, from its sizes alone.  In microseconds for n = n_cap chunks, as measured
-// (dk = 128 / 64): one workgroup a row composes a chunk in 0.63 / 0.5 and scores n_rep
-// representatives in 0.0075 n_rep (dk / 128), whatever the number of rows up to the CUs'; the split
-// form costs 60 / 30 for its launches and its walk over the segments, and for every row and chunk
-// 0.0187 / 0.0045 (the composition's matrix products at the rate a large library product reaches,
-// and the maps read a second time).  Measured on both sides: dk = 128, n_rep = 2, n = 1024, 16 rows
-// 356 split, 648 not, 64 rows 1039 and 711; n = 128, 4 rows 70 and 88, 32 rows 121 and 92; dk = 64,
-// n = 512, 64 rows 160 and 271, 256 rows 470 and 288; dk = 128, n_rep = 64, n = 64, 16 rows 69
-// and 75, 64 rows 119 and 85.
+// Which form a call takes, from its sizes alone.  In microseconds, fitted to both forms' times
+// (dk = 128 / 64, n = n_cap chunks): one workgroup a row takes (0.65 + 0.0055 n_rep) n / (0.47 +
+// 0.0025 n_rep) n, whatever the number of rows up to the CUs'; the split form 42 + 0.1 n / 26 +
+// 0.06 n for its launches and the walk over the segments, and 0.0145 n / 0.0033 n for every row
+// (the composition's matrix products, and the maps read a second time).  Measured, split and not:
+// dk = 128, n_rep = 2: n = 1024: 1 row 136 and 665, 16 rows 346 and 675, 48 rows 808 and 683;
+// n = 128: 8 rows 67 and 94, 32 rows 115 and 97; n = 64: 8 rows 54 and 51.  n_rep = 64, n = 64, 16
+// rows: 62 and 71.  dk = 64: n = 512: 64 rows 147 and 265, 128 rows 270 and 267.
 static bool split_pays(int64_t rows, int n, int n_rep, int dk) {
-  const float whole = (dk == 128 ? 0.63f : 0.5f) + 0.0075f * n_rep * dk / 128.f;
-  const float fixed = dk == 128 ? 60.f : 30.f, each = dk == 128 ? 0.0187f : 0.0045f;
+  const float whole = dk == 128 ? 0.65f + 0.0055f * n_rep : 0.47f + 0.0025f * n_rep;
+  const float fixed = dk == 128 ? 42.f + 0.1f * n : 26.f + 0.06f * n, each = dk == 128 ? 0.0145f : 0.0033f;
   return n >= kSplitFrom && rows < 256 && fixed + each * rows * n < whole * n;
 }
 
