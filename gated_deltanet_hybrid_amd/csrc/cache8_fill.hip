@@ -103,7 +103,10 @@ __device__ __forceinline__ void append_finish(const Append8Args& a, int64_t row,
 }
 
 // One workgroup per (row, appended chunk): the maps are read once into registers, their largest
-// magnitudes found, and the quantised transposes go through LDS to 16-byte stores.
+// magnitudes found, and the quantised transposes go through LDS to 16-byte stores.  Bound by HBM:
+// 512 chunks of 16 heads (dk = dv = 128, bf16, 64 representatives, 1.01 GB read and written) take
+// 191 us, 5.3 TB/s, where a large copy moves 4.8; a batch's 1024 live chunks (float32, set back to
+// the identity, 303 MB) 40 us from the caches' reach and about 65 from HBM.
 template <int FMT, class T, int DK, int DV, int NT>
 __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
   constexpr int LD = DK + 4;  // image row: one word of padding spreads the transposed writes over the banks
@@ -205,7 +208,9 @@ hipError_t pick_append8(const Append8Args& a, int dk, int dv, hipStream_t s) {
 // (row, 32 columns): V columns to a lane, 32 / V lanes to a row of the matrix, so that a wave's
 // load is whole 128-byte lines, eight loads on their way.  The lanes' sums are added across the
 // wave and then over the four waves, always in that order.  Reads n (n - 1) / 2 floats a head, and
-// the half lines on the diagonal.
+// the half lines on the diagonal: 16 heads of 1024 chunks, 33.6 MB, in 7.4 us (4.5 TB/s; 13 us with
+// each load under its own condition, 83 us with one load at a time).
+typedef float f32x4v __attribute__((ext_vector_type(4)));
 template <int V>
 __global__ __launch_bounds__(256) void gate_weights_kernel(GateWeightsArgs a) {
   constexpr int LPR = 32 / V, RPP = 256 / LPR, U = 8;
@@ -218,7 +223,9 @@ __global__ __launch_bounds__(256) void gate_weights_kernel(GateWeightsArgs a) {
     n = a.n_chunks[row / a.H];
     n = n < 0 ? 0 : (n > a.N ? a.N : n);
   }
-  const float* g = a.gates + row * a.N * (int64_t)a.N + j;
+  // a lane past the last column, or a row past the last chunk, reads the last one and counts for nothing:
+  // a load under a condition would be waited for on its own
+  const float* g = a.gates + row * a.N * (int64_t)a.N + (j < a.N ? j : a.N - V);
   float sum[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) sum[v] = 0.f;
@@ -227,24 +234,20 @@ __global__ __launch_bounds__(256) void gate_weights_kernel(GateWeightsArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * RPP + tid / LPR;
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[u][v] = 0.f;
-      if (i < n && j < i) {  // (j + V <= N: the vector form has N in whole vectors)
-        const float* p = g + (int64_t)i * a.N;
-        if constexpr (V == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(p);
-          x[u][0] = f.x; x[u][1] = f.y; x[u][2] = f.z; x[u][3] = f.w;
-        } else {
-          x[u][0] = *p;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[u][v] = j + v < i && x[u][v] >= a.tau ? gate_mass(x[u][v]) : 0.f;
+      const float* p = g + (int64_t)(i < n ? i : n - 1) * a.N;
+      if constexpr (V == 4) {
+        const f32x4v f = *reinterpret_cast<const f32x4v*>(p);
+        x[u][0] = f.x; x[u][1] = f.y; x[u][2] = f.z; x[u][3] = f.w;
+      } else {
+        x[u][0] = *p;
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * RPP + tid / LPR;
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum[v] += x[u][v];
+      for (int v = 0; v < V; ++v) sum[v] += i < n && j + v < i && x[u][v] >= a.tau ? gate_mass(x[u][v]) : 0.f;
+    }
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -269,7 +272,9 @@ __device__ __forceinline__ unsigned order_key(float x) {
 // lane in register i).  The m lightest of the positions [0, n - n_recent) leave: the threshold
 // key (the m-th smallest) is found bit by bit from the top by counting ballots, every key below
 // it leaves, and of the equal ones the first in time.  All of a row is read before any of it is
-// written, so outputs may be the inputs.
+// written, so outputs may be the inputs.  Latency: 32 rounds of ballots, 9 us for 128 rows of 1024
+// by four waves a row (19 by one, whose 16 ballots a round follow one another), 4 us for 64
+// positions.  Up to 256 positions one wave needs at most four ballots a round and no barrier.
 template <int NI, int NW>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void evict_kernel(EvictArgs a) {
   constexpr int RPB = NW == 1 ? 4 : 1;  // rows per workgroup

@@ -408,7 +408,9 @@ hla_status_t hla_cache8_append(const hla_cache8_t* c, int32_t dtype, int32_t n_s
  *   o         [Bs, H, dv] float32 out.
  *   The cache is read; its weight (if any) gains every held position's gate after the
  *   threshold.  A gate that is NaN is below every threshold.
- *   ws, ws_bytes: workspace of at least hla_decode8_workspace_bytes() bytes, 16-byte aligned.
+ *   ws, ws_bytes: workspace of at least hla_decode8_workspace_bytes() bytes, 16-byte aligned
+ *           (0 but for few rows with a long cache, whose positions are cut into segments: then
+ *           mostly a float32 dk x dk matrix a segment).  It belongs to one call at a time.
  * Appending the live chunk is hla_cache8_append's (reset_live).
  * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE, HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN,
  *         HLA_ERR_WORKSPACE, HLA_ERR_HIP.
@@ -428,7 +430,7 @@ hla_status_t hla_decode8_workspace_bytes(const hla_cache8_t* c, size_t* out);
  * hla_gate_weights -- the weight that a prefill's gates give every chunk: what a decode step's
  * accumulation would have summed, over the prompt's own query chunks.
  *     weight[b, h, j] = sum over j < i < n_b of g_ij [g_ij >= tau], g taken within [0, 1]
- *   gates    [B, H, N, N] float32 as hla_route_mix writes them (entries j < i are read).
+ *   gates    [B, H, N, N] float32 as hla_route_mix writes them (entries j < i count).
  *   n_chunks [B] int32 or NULL (N): valid chunks n_b, clamped to 0 .. N.
  *   weight   [B, H, N] float32 out (0 at and behind the last valid chunk).
  * Sums are float32 in a fixed order.
