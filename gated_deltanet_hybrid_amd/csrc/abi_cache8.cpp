@@ -9,7 +9,8 @@
 
 namespace {
 
-constexpr double kMaxGrid = 2147483647.0;
+// A launch counts its workgroups in 31 bits and its threads in 32.
+bool launchable(double blocks, double threads) { return blocks <= 2147483647.0 && blocks * threads <= 4294967295.0; }
 constexpr int32_t kMaxSlots = 1024, kMaxRep = 256, kMaxEvict = 16384;
 
 template <int A, class... P>
@@ -22,7 +23,7 @@ hla_status_t check_cache(const hla_cache8_t* c) {
   if (c->format != HLA_CACHE_I8 && c->format != HLA_CACHE_E4M3) return HLA_ERR_BAD_DTYPE;
   if (c->Bs < 1 || c->H < 1 || (c->dk != 64 && c->dk != 128) || (c->dv != 64 && c->dv != 128)) return HLA_ERR_BAD_SHAPE;
   if (c->n_cap < 1 || c->n_cap > kMaxSlots || c->n_rep < 0 || c->n_rep > kMaxRep) return HLA_ERR_BAD_SHAPE;
-  if ((double)c->Bs * (double)c->H > kMaxGrid) return HLA_ERR_BAD_SHAPE;
+  if (!launchable((double)c->Bs * (double)c->H, (c->dk + c->dv) * 4.0)) return HLA_ERR_BAD_SHAPE;
   if (!c->maps || !c->scale || !c->order || !c->count || (c->n_rep && !c->reps)) return HLA_ERR_NULL_ARG;
   if (!aligned<16>(c->maps, c->reps, c->scale) || !aligned<4>(c->order, c->count, c->weight)) return HLA_ERR_ALIGN;
   return HLA_OK;
@@ -109,7 +110,7 @@ hla_status_t hla_cache8_append(const hla_cache8_t* c, int32_t dtype, int32_t n_s
   if (st != HLA_OK) return st;
   if (dtype != HLA_F32 && dtype != HLA_BF16) return HLA_ERR_BAD_DTYPE;
   if (n_src < 0 || ld_src < n_src || ld_src < 1 || (reset != 0 && reset != 1) || (reset_live != 0 && reset_live != 1)) return HLA_ERR_BAD_SHAPE;
-  if ((double)c->Bs * (double)c->H * (double)ld_src > kMaxGrid) return HLA_ERR_BAD_SHAPE;
+  if (!launchable((double)c->Bs * (double)c->H * (double)ld_src, 512.0)) return HLA_ERR_BAD_SHAPE;
   if (!At || !Bc || (c->n_rep && !reps)) return HLA_ERR_NULL_ARG;
   if (c->n_rep && ld_R < (int64_t)n_src * c->n_rep) return HLA_ERR_BAD_SHAPE;
   if (c->n_rep && (double)c->Bs * (double)ld_R * (double)c->H * c->dk > 4.0e18) return HLA_ERR_BAD_SHAPE;
@@ -125,7 +126,8 @@ hla_status_t hla_cache8_append(const hla_cache8_t* c, int32_t dtype, int32_t n_s
 hla_status_t hla_gate_weights(int64_t B, int64_t H, int32_t N, const float* gates, const int32_t* n_chunks,
                               float tau, float* weight, hipStream_t stream) {
   if (B < 1 || H < 1 || N < 1 || std::isnan(tau)) return HLA_ERR_BAD_SHAPE;
-  if ((double)B * (double)H * ((N + 31.0) / 32.0) > kMaxGrid || (double)B * (double)H * (double)N * (double)N > 4.0e18)
+  if (!launchable((double)B * (double)H * ((N + 31.0) / 32.0), 256.0) ||
+      (double)B * (double)H * (double)N * (double)N > 4.0e18)
     return HLA_ERR_BAD_SHAPE;
   if (!gates || !weight) return HLA_ERR_NULL_ARG;
   if (!aligned<4>(gates, n_chunks, weight)) return HLA_ERR_ALIGN;
@@ -136,7 +138,8 @@ hla_status_t hla_gate_weights(int64_t B, int64_t H, int32_t N, const float* gate
 hla_status_t hla_evict_chunks(int64_t Bs, int64_t H, int32_t n, const float* weight, const int32_t* order,
                               const int32_t* count, int32_t budget, int32_t n_recent, int32_t* order_out,
                               float* weight_out, int32_t* count_out, hipStream_t stream) {
-  if (Bs < 1 || H < 1 || n < 1 || n > kMaxEvict || (double)Bs * (double)H > kMaxGrid) return HLA_ERR_BAD_SHAPE;
+  if (Bs < 1 || H < 1 || n < 1 || n > kMaxEvict) return HLA_ERR_BAD_SHAPE;
+  if (!launchable((double)Bs * (double)H, n <= 256 ? 64.0 : n <= 4096 ? 256.0 : 1024.0)) return HLA_ERR_BAD_SHAPE;
   if (budget < 0 || n_recent < 0 || n_recent > budget) return HLA_ERR_BAD_SHAPE;
   if (!weight || !count || !order_out || !weight_out || !count_out) return HLA_ERR_NULL_ARG;
   if (!aligned<4>(weight, order, count, order_out, weight_out, count_out)) return HLA_ERR_ALIGN;

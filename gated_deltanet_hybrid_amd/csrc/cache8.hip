@@ -223,8 +223,9 @@ __device__ __forceinline__ Fixed fixed_for(float bound) {
   b = b < 30 ? 30 : (b > 253 ? 253 : b);
   return {__builtin_bit_cast(float, (unsigned)(283 - b) << 23), __builtin_bit_cast(float, (unsigned)(b - 29) << 23)};
 }
-// Magnitudes compare as their bits, and what is not finite is above every number.
-constexpr unsigned kInf = 0x7f800000u;
+// Magnitudes compare as their bits, and what is not finite is above every number.  Fixed point ends
+// at 2^127: from there on it makes NaN, as of what is not finite.
+constexpr unsigned kFixedEnd = 0x7f000000u;
 __device__ __forceinline__ unsigned mag(float x) { return __builtin_bit_cast(unsigned, x) & 0x7fffffffu; }
 __device__ __forceinline__ unsigned max_u(unsigned a, unsigned b) { return a > b ? a : b; }
 // Largest over the lanes 16, 32 and 48 apart (the lanes of one 16-lane row hold the same value).
@@ -236,13 +237,13 @@ __device__ __forceinline__ unsigned rows_max(unsigned x) {
 }
 
 // A vector that all NW waves can see becomes an operand; returns the factor of its sums (NaN where
-// a value is not finite, which fixed point cannot hold).
+// fixed point cannot hold a value).
 template <class Op, int DK, int NW> __device__ __forceinline__ float encode(Op& op, const float* src) {
   const int lane = lane_id(), w = threadIdx.x >> 6;
   float m = 0.f, bad = 0.f;
   for (int i = lane; i < DK; i += 64) {
     m = fmaxf(m, fabsf(src[i]));
-    bad += src[i] * 0.f;
+    bad += Op::kFixed && mag(src[i]) >= kFixedEnd ? __builtin_nanf("") : src[i] * 0.f;
   }
   const Fixed fx = fixed_for(wave_max_valu(m));
   for (int r0 = 16 * w; r0 < DK; r0 += 16 * NW) {
@@ -539,7 +540,7 @@ __global__ __launch_bounds__((DK + DV) * 4) void decode8_kernel(Decode8Args a) {
     bool measure = false;  // (the same in every thread)
     if constexpr (Op::kFixed) {
       const unsigned m = read_max(buf);
-      us = m >= kInf ? __builtin_nanf("") : us;  // a z that is not finite makes NaN of all behind it
+      us = m >= kFixedEnd ? __builtin_nanf("") : us;  // and of everything behind it
       const float factor = 1.f + fabsf(ca) * (128.f * DK);
       measure = !(factor <= 128.f);
       fx = fixed_for(__builtin_bit_cast(float, m) * factor);

@@ -36,10 +36,6 @@ constexpr float kCache8Tiny = 0x1p-100f;
 template <int FMT> struct Stored;
 template <> struct Stored<kI8> {
   static constexpr float top = 127.f;
-  // the four bytes of a word, exactly
-  __device__ __forceinline__ static void unpack(unsigned w, float (&f)[4]) {
-    f[0] = (float)(int8_t)w; f[1] = (float)(int8_t)(w >> 8); f[2] = (float)(int8_t)(w >> 16); f[3] = (float)(int8_t)(w >> 24);
-  }
   __device__ __forceinline__ static unsigned pack(float a, float b, float c, float d) {
     auto q = [](float x) { return (unsigned)(int)fminf(fmaxf(rintf(x), -127.f), 127.f) & 0xffu; };
     return q(a) | q(b) << 8 | q(c) << 16 | q(d) << 24;
@@ -47,10 +43,6 @@ template <> struct Stored<kI8> {
 };
 template <> struct Stored<kE4M3> {
   static constexpr float top = 448.f;
-  __device__ __forceinline__ static void unpack(unsigned w, float (&f)[4]) {
-    f[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0); f[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1);
-    f[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2); f[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3);
-  }
   __device__ __forceinline__ static unsigned pack(float a, float b, float c, float d) {
     // rounding may leave x (top / max) one step above top: clamped, it stores top
     auto cl = [](float x) { return fminf(fmaxf(x, -448.f), 448.f); };
@@ -70,13 +62,11 @@ __device__ __forceinline__ bf16x8 e4m3_frag(unsigned w0, unsigned w1) {
 
 template <int FMT> __device__ __forceinline__ bf16x8 stored_frag(unsigned w0, unsigned w1) {
   if constexpr (FMT == kE4M3) return e4m3_frag(w0, w1);
-  float a[4], b[4];
-  Stored<kI8>::unpack(w0, a);
-  Stored<kI8>::unpack(w1, b);
-  auto hi2 = [](float x, float y) {  // 8-bit integers: the low halves of their float32 images are zero
+  auto two = [](unsigned w, int at) {  // 8-bit integers: the low halves of their float32 images are zero
+    const float x = (float)(int8_t)(w >> at), y = (float)(int8_t)(w >> (at + 8));
     return __builtin_amdgcn_perm(__builtin_bit_cast(unsigned, y), __builtin_bit_cast(unsigned, x), 0x07060302u);
   };
-  return __builtin_bit_cast(bf16x8, make_uint4(hi2(a[0], a[1]), hi2(a[2], a[3]), hi2(b[0], b[1]), hi2(b[2], b[3])));
+  return __builtin_bit_cast(bf16x8, make_uint4(two(w0, 0), two(w0, 16), two(w1, 0), two(w1, 16)));
 }
 
 template <int FMT> __device__ __forceinline__ float to_stored(float m) {

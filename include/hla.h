@@ -407,7 +407,9 @@ hla_status_t hla_cache8_append(const hla_cache8_t* c, int32_t dtype, int32_t n_s
  *   gates_out [Bs, H, n_cap] float32 or NULL: every held position's gate, 0 behind them.
  *   o         [Bs, H, dv] float32 out.
  *   The cache is read; its weight (if any) gains every held position's gate after the
- *   threshold.  A gate that is NaN is below every threshold.
+ *   threshold.  A gate that is NaN is below every threshold.  The vectors that meet int8
+ *   chunks (q for the gates, At_cur^T q as the chunks pass it on) hold values below 2^127; a
+ *   larger one makes the gates, or o, NaN.
  *   ws, ws_bytes: workspace of at least hla_decode8_workspace_bytes() bytes, 16-byte aligned
  *           (0 but for few rows with a long cache, whose positions are cut into segments: then
  *           mostly a float32 dk x dk matrix a segment).  It belongs to one call at a time.

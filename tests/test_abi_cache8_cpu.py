@@ -117,6 +117,20 @@ def test_gate_weights_and_evict_validation(lib):
     assert put((4, P + 2)) == ALIGN
 
 
+def test_launches_are_counted_in_32_bits(lib):
+    """Refused where a grid's threads would pass 32 bits, whatever memory would hold."""
+    n = ctypes.c_size_t()
+    for dk, dv in itertools.product((64, 128), repeat=2):
+        rows = (1 << 32) // ((dk + dv) * 4)
+        ok, over = cache(Bs=rows - 1, H=1, dk=dk, dv=dv), cache(Bs=rows + 1, H=1, dk=dk, dv=dv)
+        assert lib.hla_decode8_workspace_bytes(ok, ctypes.byref(n)) == OK
+        assert lib.hla_decode8_workspace_bytes(over, ctypes.byref(n)) == BAD_SHAPE
+    assert lib.hla_cache8_append(cache(Bs=1 << 12, H=1 << 7), 1, 16, 16, P, P, P, 32, None, None, None, 0, 0, None) == BAD_SHAPE
+    assert lib.hla_gate_weights(1 << 24, 1, 1, P, None, 0.0, P, None) == BAD_SHAPE
+    for rows, n_pos in ((1 << 26, 1), (1 << 26, 256), (1 << 24, 257), (1 << 24, 4096), (1 << 22, 4097)):
+        assert lib.hla_evict_chunks(rows, 1, n_pos, P, None, P, 1, 1, P, P, P, None) == BAD_SHAPE
+
+
 def test_python_refuses_host_tensors():
     z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt)  # noqa: E731
     with pytest.raises(ValueError):

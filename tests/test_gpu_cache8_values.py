@@ -123,6 +123,31 @@ def test_both_forms_on_the_same_rows(fmt, dk, dv):
         assert np.max(np.abs(a - b)) <= tol * max(1.0, np.max(np.abs(a)))
 
 
+@pytest.mark.parametrize("n_cap", [20, 200])
+def test_z_at_the_end_of_its_range(n_cap):
+    """int8 chunks hold z below 2^127: just below, o is right; from there on it is NaN, not wrong."""
+    note(f"cache8 largest z {n_cap}")
+    h = hla()
+    for zmax, fits in ((1.5 * 2.0 ** 126, True), (1.5 * 2.0 ** 127, False)):
+        c = make_cache(h, 1, 1, n_cap, 64, 64, 0, "int8", 231)
+        c.count.fill_(n_cap)
+        c.scale[..., 0] = 0.0  # A = I: z stays as it enters
+        c.scale[..., 1] = 2.0 ** -20
+        zero, one = torch.zeros(1, 1, 64, device="cuda"), torch.ones(1, 1, device="cuda")
+        q = zero.clone()
+        q[..., 3] = 1.0
+        S, A = torch.zeros(1, 1, 64, 64, device="cuda"), torch.zeros(1, 1, 64, 64, device="cuda")
+        A[0, 0, 3, 5] = zmax  # z = zmax e_5
+        gi = torch.full((1, 1, n_cap), 0.0, device="cuda")
+        gi[..., n_cap // 2] = 1.0
+        o = host(h.gdn_decode8(q, zero, zero, 0 * one, one, S, A, c, gates_in=gi, tau=0.5))[0, 0]
+        if fits:
+            ref = row_cache(c, 0, 0)[1][n_cap // 2][:, 5] * zmax
+            assert np.all(np.abs(o - ref) <= 4 * EPS * np.abs(ref))
+        else:
+            assert np.isnan(o).all()
+
+
 @pytest.mark.parametrize("n_cap", [30, 300])
 def test_same_bits_every_time(n_cap):
     """Two equal calls give equal bits (fixed orders of summation in both forms)."""
