@@ -915,7 +915,7 @@ def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
     complete chunks enter the cache, emptied first, and the rest of the prompt is the live chunk.
     Where there are more than `budget` chunks (default and at most: the cache's capacity), those
     stay that the prompt's own gates weigh most, and the n_recent newest.  Returns (S_cur,
-    At_cur), float32."""
+    At_cur), float32 tensors of their own."""
     At, Bc = r["At"], r["Bc"]
     B, H, N, dk, _ = At.shape
     dv, full = Bc.shape[-1], T // C
@@ -928,8 +928,9 @@ def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
     count = torch.full((B, H), full, dtype=torch.int32, device=At.device)
     order, weight, count = evict_chunks(weight, count, keep, min(n_recent, keep))
     cache8_append(cache, At, Bc, r["reps"], src=order, n_new=count, weight_in=weight, reset=True, n=full)
-    if full < N:
-        return Bc[:, :, full].float().contiguous(), At[:, :, full].float().contiguous()
+    if full < N:  # copies, also where the maps are float32 and lie contiguous: decode updates them in place
+        return tuple(t[:, :, full].to(torch.float32, copy=True, memory_format=torch.contiguous_format)
+                     for t in (Bc, At))
     S = torch.zeros((B, H, dk, dv), dtype=torch.float32, device=At.device)
     return S, torch.eye(dk, dtype=torch.float32, device=At.device).repeat(B, H, 1, 1)
 

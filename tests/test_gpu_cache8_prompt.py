@@ -1,0 +1,50 @@
+"""From a prompt to the 8-bit chunk cache on the GPU: both recurrences, what the call returns and
+leaves alone, the units of the weights it hands to the decode steps, and the prefills it refuses."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache8 as o8
+from gated_deltanet_hybrid_amd import inputs
+from gpu_util import f32, note, token_tensors
+from test_gpu_cache8 import EPS, check_decode, check_slot, f32s, hla, token
+
+pytestmark = pytest.mark.gpu
+C = 64
+
+
+def prompt(h, B, T, H, dk, dv, dtype="f32", gdn2=False, seed=301, chunk=C, **kw):
+    x = inputs.gen_tokens(B, T, H, dk, dv, dtype=dtype, seed=seed, alpha_mode="slow")
+    q, k, v, beta, alpha = token_tensors(x)
+    if not gdn2:
+        return k, h.hla_prefill(q, k, v, beta, alpha, C=chunk, **kw)
+    g = inputs.gen_gdn2_gates(B, T, H, dk, dv, seed=seed, alpha_mode="slow")
+    return k, h.gdn2_hla_prefill(q, k, v, *(f32(g[n]) for n in ("a", "b", "w")), C=chunk, **kw)
+
+
+def check_cache(c, r, k, n, chunk=C):
+    """Every held position's stored values are those of the source chunk `kept[p]`."""
+    for b in range(c.Bs):
+        for hh in range(c.H):
+            for p, src in enumerate(n[b][hh]):
+                slot = int(c.order[b, hh, p])
+                reps = None if not c.n_rep else f32s(k)[b, src * chunk:(src + 1) * chunk, hh]
+                check_slot(c, b, hh, slot, f32s(r["At"])[b, hh, src], f32s(r["Bc"])[b, hh, src], reps,
+                           "int8" if c.maps.dtype == torch.int8 else "e4m3")
+
+
+@pytest.mark.parametrize("T", [40, 150])
+def test_the_live_chunk_is_not_the_prefills(T):
+    """One row: the last chunk's maps are contiguous as they lie in the prefill's tensors.  A decode
+    step, which updates the live chunk in place, leaves the prefill's result as it was."""
+    note(f"cache8 live chunk of its own T={T}")
+    h = hla()
+    k, r = prompt(h, 1, T, 1, 64, 64)
+    At, Bc = r["At"].clone(), r["Bc"].clone()
+    c = h.cache8_alloc(1, 1, 4, 64, 64, C, "int8")
+    S, A = h.prefill_to_cache8(c, r, T)
+    tok, gates, _, _ = token(1, 1, 64, 64, "f32", False, 321)
+    h.gdn_decode8(*tok, *gates, S, A, c)
+    assert torch.equal(r["At"], At) and torch.equal(r["Bc"], Bc)
+    S2, A2 = h.prefill_to_cache8(c, r, T)  # and the same prompt enters again
+    assert torch.equal(A2, At[:, :, -1]) and torch.equal(S2, Bc[:, :, -1])
