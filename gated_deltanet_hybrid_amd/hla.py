@@ -329,11 +329,12 @@ def gdn2_prefill(q, k, v, a_decay, b_erase, w_write, S0=None, chunk_init=None, w
 
 def gdn2_hla_prefill(q, k, v, a_decay, b_erase, w_write, tau=1e-3, gates_in=None, S0=None, C=CHUNK):
     """The routed prefill under the Gated DeltaNet-2 recurrence: GDN-2 chunk maps, the HLA
-    router and composition unchanged, GDN-2 chunk outputs from the routed states."""
+    router and composition unchanged, GDN-2 chunk outputs from the routed states.
+    Representatives are each chunk's raw keys."""
     At, Bc = gdn2_chunk_transitions(k, v, a_decay, b_erase, w_write, C=C)
     r = route_mix(q, k, At, Bc, n_rep=C, tau=tau, S0=S0, gates_in=gates_in, C=C)
     o, _ = gdn2_prefill(q, k, v, a_decay, b_erase, w_write, chunk_init=r["S_routed"], want_state=False, C=C)
-    r.update(At=At, Bc=Bc, o=o)
+    r.update(At=At, Bc=Bc, o=o, reps=k)
     return r
 
 
@@ -911,11 +912,11 @@ def cache8_evict(cache, budget, n_recent=0):
 
 
 def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
-    """What a decode needs after a routed prefill of T tokens (r: hla_prefill's result): the
-    complete chunks enter the cache, emptied first, and the rest of the prompt is the live chunk.
-    Where there are more than `budget` chunks (default and at most: the cache's capacity), those
-    stay that the prompt's own gates weigh most, and the n_recent newest.  Returns (S_cur,
-    At_cur), float32 tensors of their own."""
+    """What a decode needs after a routed prefill of T tokens (r: the result of hla_prefill or
+    gdn2_hla_prefill): the complete chunks enter the cache, emptied first, and the rest of the
+    prompt is the live chunk.  Where there are more than `budget` chunks (default and at most: the
+    cache's capacity), those stay that the prompt's own gates weigh most, and the n_recent newest.
+    Returns (S_cur, At_cur), float32 tensors of their own."""
     At, Bc = r["At"], r["Bc"]
     B, H, N, dk, _ = At.shape
     dv, full = Bc.shape[-1], T // C
@@ -927,7 +928,7 @@ def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
     weight = gate_weights(r["gates"], tau=tau)
     count = torch.full((B, H), full, dtype=torch.int32, device=At.device)
     order, weight, count = evict_chunks(weight, count, keep, min(n_recent, keep))
-    cache8_append(cache, At, Bc, r["reps"], src=order, n_new=count, weight_in=weight, reset=True, n=full)
+    cache8_append(cache, At, Bc, r["reps"] if cache.n_rep else None, src=order, n_new=count, weight_in=weight, reset=True, n=full)
     if full < N:  # copies, also where the maps are float32 and lie contiguous: decode updates them in place
         return tuple(t[:, :, full].to(torch.float32, copy=True, memory_format=torch.contiguous_format)
                      for t in (Bc, At))

@@ -33,6 +33,26 @@ def check_cache(c, r, k, n, chunk=C):
                            "int8" if c.maps.dtype == torch.int8 else "e4m3")
 
 
+@pytest.mark.parametrize("fmt,dtype,dk,dv,n_rep", [("int8", "bf16", 128, 64, C), ("e4m3", "f32", 64, 128, C),
+                                                   ("int8", "f32", 64, 64, 0)], ids=str)
+def test_gdn2_prompt_to_decode(fmt, dtype, dk, dv, n_rep):
+    """Gated DeltaNet-2: 200 tokens leave three chunks and a live one of 8; scored by the chunks'
+    own keys, or by the caller's gates over a cache that holds none."""
+    note(f"cache8 gdn2 prompt {fmt} {dtype} {dk} {dv} {n_rep}")
+    h = hla()
+    B, H, T = 2, 2, 200
+    k, r = prompt(h, B, T, H, dk, dv, dtype, gdn2=True)
+    c = h.cache8_alloc(B, H, 5, dk, dv, n_rep, fmt)
+    S, A = h.prefill_to_cache8(c, r, T)
+    assert c.count.tolist() == [[3, 3]] * B
+    check_cache(c, r, k, [[[0, 1, 2]] * H] * B)
+    assert torch.equal(A, r["At"][:, :, 3].float()) and torch.equal(S, r["Bc"][:, :, 3].float())
+    for s in range(3):
+        tok, gates, _, _ = token(B, H, dk, dv, dtype, True, 310 + s)
+        gi = None if n_rep else torch.full((B, H, 5), 0.25, device="cuda")
+        check_decode(h, c, tok, gates, S, A, gates_in=gi)
+
+
 @pytest.mark.parametrize("T", [40, 150])
 def test_the_live_chunk_is_not_the_prefills(T):
     """One row: the last chunk's maps are contiguous as they lie in the prefill's tensors.  A decode
