@@ -334,7 +334,7 @@ def gdn2_hla_prefill(q, k, v, a_decay, b_erase, w_write, tau=1e-3, gates_in=None
     At, Bc = gdn2_chunk_transitions(k, v, a_decay, b_erase, w_write, C=C)
     r = route_mix(q, k, At, Bc, n_rep=C, tau=tau, S0=S0, gates_in=gates_in, C=C)
     o, _ = gdn2_prefill(q, k, v, a_decay, b_erase, w_write, chunk_init=r["S_routed"], want_state=False, C=C)
-    r.update(At=At, Bc=Bc, o=o, reps=k)
+    r.update(At=At, Bc=Bc, o=o, reps=k, n_rep=C, C=C)
     return r
 
 
@@ -646,7 +646,7 @@ def hla_prefill(q, k, v, beta, alpha, tau=1e-3, gates_in=None, S0=None, C=CHUNK,
         reps, n_rep = chunk_reps(k, pooler, window=window, C=C), C // window
     r = route_mix(q, reps, At, Bc, n_rep=n_rep, tau=tau, S0=S0, gates_in=gates_in, C=C)
     o, _ = gdn_prefill(q, k, v, beta, alpha, chunk_init=r["S_routed"], want_state=False, C=C, wu=wu)
-    r.update(At=At, Bc=Bc, o=o, reps=reps)
+    r.update(At=At, Bc=Bc, o=o, reps=reps, n_rep=n_rep, C=C)
     return r
 
 
@@ -920,15 +920,16 @@ def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
     At, Bc = r["At"], r["Bc"]
     B, H, N, dk, _ = At.shape
     dv, full = Bc.shape[-1], T // C
-    if N != math.ceil(T / C):
-        raise ValueError("T and C do not match the prefill's chunks")
-    if cache.n_rep and r["reps"].shape[1] != N * cache.n_rep and (r["reps"].shape[1], cache.n_rep) != (T, C):
+    if (T, C) != (r["o"].shape[1], r["C"]):
+        raise ValueError("T and C are not the prefill's")
+    if cache.n_rep not in (0, r["n_rep"]):
         raise ValueError("the cache's representatives per chunk are not the prefill's")
     keep = cache.n_cap if budget is None else min(budget, cache.n_cap)
     weight = gate_weights(r["gates"], tau=tau)
     count = torch.full((B, H), full, dtype=torch.int32, device=At.device)
     order, weight, count = evict_chunks(weight, count, keep, min(n_recent, keep))
-    cache8_append(cache, At, Bc, r["reps"] if cache.n_rep else None, src=order, n_new=count, weight_in=weight, reset=True, n=full)
+    cache8_append(cache, At, Bc, r["reps"] if cache.n_rep else None, src=order, n_new=count, weight_in=weight,
+                  reset=True, n=full)
     if full < N:  # copies, also where the maps are float32 and lie contiguous: decode updates them in place
         return tuple(t[:, :, full].to(torch.float32, copy=True, memory_format=torch.contiguous_format)
                      for t in (Bc, At))

@@ -68,3 +68,20 @@ def test_the_live_chunk_is_not_the_prefills(T):
     assert torch.equal(r["At"], At) and torch.equal(r["Bc"], Bc)
     S2, A2 = h.prefill_to_cache8(c, r, T)  # and the same prompt enters again
     assert torch.equal(A2, At[:, :, -1]) and torch.equal(S2, Bc[:, :, -1])
+
+
+def test_prefills_that_do_not_fit_are_refused():
+    """The same refusals as on the host, of results that a prefill gave."""
+    note("cache8 prompt refusals")
+    h = hla()
+    k, r = prompt(h, 1, 96, 2, 64, 64)
+    assert r["reps"].shape[1] == 2 * 48
+    with pytest.raises(ValueError):
+        h.prefill_to_cache8(h.cache8_alloc(1, 2, 4, 64, 64, 48, "int8"), r, 96)
+    c = h.cache8_alloc(1, 2, 4, 64, 64, C, "int8")
+    for T, chunk in ((127, 64), (65, 64), (96, 48)):
+        with pytest.raises(ValueError):
+            h.prefill_to_cache8(c, r, T, C=chunk)
+    assert not c.count.any()
+    h.prefill_to_cache8(c, r, 96)
+    assert c.count.tolist() == [[1, 1]]
