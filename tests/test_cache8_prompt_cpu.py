@@ -53,3 +53,8 @@ def test_a_single_chunk_of_another_size_is_refused():
     """64 tokens are one whole chunk of 64, and one unfinished chunk of 128."""
     with pytest.raises(ValueError, match="T and C"):
         hla.prefill_to_cache8(cache(0), result(64, C=128), 64)
+
+
+def test_an_initial_state_is_refused():
+    with pytest.raises(ValueError, match="S0"):
+        hla.prefill_to_cache8(cache(64), result(96, S0=torch.zeros(1, 2, 64, 64)), 96)

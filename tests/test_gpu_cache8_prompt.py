@@ -82,6 +82,11 @@ def test_prefills_that_do_not_fit_are_refused():
     for T, chunk in ((127, 64), (65, 64), (96, 48)):
         with pytest.raises(ValueError):
             h.prefill_to_cache8(c, r, T, C=chunk)
+    _, r0 = prompt(h, 1, 96, 2, 64, 64, S0=torch.ones(1, 2, 64, 64, device="cuda"))
+    _, r2 = prompt(h, 1, 96, 2, 64, 64, gdn2=True, S0=torch.ones(1, 2, 64, 64, device="cuda"))
+    for bad in (r0, r2):
+        with pytest.raises(ValueError, match="S0"):
+            h.prefill_to_cache8(c, bad, 96)
     assert not c.count.any()
     h.prefill_to_cache8(c, r, 96)
     assert c.count.tolist() == [[1, 1]]
