@@ -334,7 +334,7 @@ def gdn2_hla_prefill(q, k, v, a_decay, b_erase, w_write, tau=1e-3, gates_in=None
     At, Bc = gdn2_chunk_transitions(k, v, a_decay, b_erase, w_write, C=C)
     r = route_mix(q, k, At, Bc, n_rep=C, tau=tau, S0=S0, gates_in=gates_in, C=C)
     o, _ = gdn2_prefill(q, k, v, a_decay, b_erase, w_write, chunk_init=r["S_routed"], want_state=False, C=C)
-    r.update(At=At, Bc=Bc, o=o, reps=k, n_rep=C, C=C, S0=S0)
+    r.update(At=At, Bc=Bc, o=o, reps=k, n_rep=C, C=C, S0=S0, tau=tau)
     return r
 
 
@@ -646,7 +646,7 @@ def hla_prefill(q, k, v, beta, alpha, tau=1e-3, gates_in=None, S0=None, C=CHUNK,
         reps, n_rep = chunk_reps(k, pooler, window=window, C=C), C // window
     r = route_mix(q, reps, At, Bc, n_rep=n_rep, tau=tau, S0=S0, gates_in=gates_in, C=C)
     o, _ = gdn_prefill(q, k, v, beta, alpha, chunk_init=r["S_routed"], want_state=False, C=C, wu=wu)
-    r.update(At=At, Bc=Bc, o=o, reps=reps, n_rep=n_rep, C=C, S0=S0)
+    r.update(At=At, Bc=Bc, o=o, reps=reps, n_rep=n_rep, C=C, S0=S0, tau=tau)
     return r
 
 
@@ -911,11 +911,12 @@ def cache8_evict(cache, budget, n_recent=0):
                  out=(cache.order, cache.weight, cache.count))
 
 
-def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
+def prefill_to_cache8(cache, r, T, C=CHUNK, tau=None, budget=None, n_recent=1):
     """What a decode needs after a routed prefill of T tokens (r: the result of hla_prefill or
     gdn2_hla_prefill): the complete chunks enter the cache, emptied first, and the rest of the
     prompt is the live chunk.  Where there are more than `budget` chunks (default and at most: the
-    cache's capacity), those stay that the prompt's own gates weigh most, and the n_recent newest.
+    cache's capacity), those stay that the prompt's own gates weigh most (the gates that reach tau,
+    by default the prefill's), and the n_recent newest.
     A prefill from a state S0 is refused: a decode composes the cached chunks from zero.
     Returns (S_cur, At_cur), float32 tensors of their own."""
     At, Bc = r["At"], r["Bc"]
@@ -928,7 +929,7 @@ def prefill_to_cache8(cache, r, T, C=CHUNK, tau=1e-3, budget=None, n_recent=1):
     if cache.n_rep not in (0, r["n_rep"]):
         raise ValueError("the cache's representatives per chunk are not the prefill's")
     keep = cache.n_cap if budget is None else min(budget, cache.n_cap)
-    weight = gate_weights(r["gates"], tau=tau)
+    weight = gate_weights(r["gates"], tau=r["tau"] if tau is None else tau)
     count = torch.full((B, H), full, dtype=torch.int32, device=At.device)
     order, weight, count = evict_chunks(weight, count, keep, min(n_recent, keep))
     cache8_append(cache, At, Bc, r["reps"] if cache.n_rep else None, src=order, n_new=count, weight_in=weight,

@@ -70,6 +70,23 @@ def test_the_live_chunk_is_not_the_prefills(T):
     assert torch.equal(A2, At[:, :, -1]) and torch.equal(S2, Bc[:, :, -1])
 
 
+@pytest.mark.parametrize("tau", [1e-3, 0.4, 0.5, 2.0])
+def test_weights_are_of_the_gates_that_the_prefill_kept(tau):
+    """Without a tau of its own the call weighs by the prefill's: chunks that it skipped weigh nothing."""
+    note(f"cache8 weights by the prefill's tau={tau}")
+    h = hla()
+    k, r = prompt(h, 1, 300, 2, 64, 64, tau=tau)
+    weights = []
+    for kw in ({}, dict(tau=tau)):
+        c = h.cache8_alloc(1, 2, 6, 64, 64, 0, "int8")
+        h.prefill_to_cache8(c, r, 300, **kw)
+        weights.append(c.weight)
+        for hh in range(2):
+            kept = o8.gate_weights(f32s(r["gates"])[0, hh], tau, 5)[:4]
+            assert np.array_equal(c.weight[0, hh, :4].cpu().numpy() > 0, kept > 0)
+    assert torch.equal(*weights)
+
+
 def test_prefills_that_do_not_fit_are_refused():
     """The same refusals as on the host, of results that a prefill gave."""
     note("cache8 prompt refusals")
