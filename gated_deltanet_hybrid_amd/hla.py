@@ -867,7 +867,8 @@ def _decode8(fn, gates, q, k, v, S_cur, At_cur, c, gates_in, tau, o, gates_out, 
 
 def gate_weights(gates, tau=1e-3, n_chunks=None, out=None):
     """Weights that a prefill's gates [B, H, N, N] (as route_mix gives them) put on every chunk:
-    the sum over the later query chunks of the gates that reach tau.  n_chunks [B] int32: valid
+    the sum over the later query chunks of the gates that reach tau, one gate for all of a query
+    chunk's tokens (times C they count as a decode step's gates do, one for each token).  n_chunks [B] int32: valid
     chunks per batch row.  Returns [B, H, N] float32."""
     if gates.dim() != 4 or not gates.is_cuda:
         raise ValueError("gates must be a CUDA tensor [B, H, N, N]")
@@ -911,12 +912,14 @@ def cache8_evict(cache, budget, n_recent=0):
                  out=(cache.order, cache.weight, cache.count))
 
 
-def prefill_to_cache8(cache, r, T, C=CHUNK, tau=None, budget=None, n_recent=1):
+def prefill_to_cache8(cache, r, T, C=CHUNK, tau=None, budget=None, n_recent=1, gate_tokens=None):
     """What a decode needs after a routed prefill of T tokens (r: the result of hla_prefill or
     gdn2_hla_prefill): the complete chunks enter the cache, emptied first, and the rest of the
     prompt is the live chunk.  Where there are more than `budget` chunks (default and at most: the
     cache's capacity), those stay that the prompt's own gates weigh most (the gates that reach tau,
-    by default the prefill's), and the n_recent newest.
+    by default the prefill's), and the n_recent newest.  A decode step adds one gate for its token to
+    a chunk's weight; a prompt has one gate for a query chunk, which enters the weight gate_tokens
+    times (default C: once for each of a chunk's tokens).
     A prefill from a state S0 is refused: a decode composes the cached chunks from zero.
     Returns (S_cur, At_cur), float32 tensors of their own."""
     At, Bc = r["At"], r["Bc"]
@@ -932,6 +935,7 @@ def prefill_to_cache8(cache, r, T, C=CHUNK, tau=None, budget=None, n_recent=1):
     weight = gate_weights(r["gates"], tau=r["tau"] if tau is None else tau)
     count = torch.full((B, H), full, dtype=torch.int32, device=At.device)
     order, weight, count = evict_chunks(weight, count, keep, min(n_recent, keep))
+    weight.mul_(C if gate_tokens is None else gate_tokens)
     cache8_append(cache, At, Bc, r["reps"] if cache.n_rep else None, src=order, n_new=count, weight_in=weight,
                   reset=True, n=full)
     if full < N:  # copies, also where the maps are float32 and lie contiguous: decode updates them in place

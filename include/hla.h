@@ -429,8 +429,9 @@ hla_status_t hla_gdn2_decode8(const hla_cache8_t* c, int32_t dtype, const void* 
 hla_status_t hla_decode8_workspace_bytes(const hla_cache8_t* c, size_t* out);
 
 /*
- * hla_gate_weights -- the weight that a prefill's gates give every chunk: what a decode step's
- * accumulation would have summed, over the prompt's own query chunks.
+ * hla_gate_weights -- the weight that a prefill's gates give every chunk: the sum of the gates
+ * that the prompt's own later query chunks read it with, one for each query chunk (a decode step
+ * adds one for each token: times C the two are in one unit).
  *     weight[b, h, j] = sum over j < i < n_b of g_ij [g_ij >= tau], g taken within [0, 1]
  *   gates    [B, H, N, N] float32 as hla_route_mix writes them (entries j < i count).
  *   n_chunks [B] int32 or NULL (N): valid chunks n_b, clamped to 0 .. N.

@@ -87,6 +87,30 @@ def test_weights_are_of_the_gates_that_the_prefill_kept(tau):
     assert torch.equal(*weights)
 
 
+@pytest.mark.parametrize("chunk", [64, 128])
+@pytest.mark.parametrize("tau", [1e-3, 0.4])
+def test_weights_count_tokens(chunk, tau):
+    """A prompt's gate is one query chunk's, a decode step's one token's: the prompt's weights count
+    each gate once for every token of a chunk, of the gates that the prefill itself kept."""
+    note(f"cache8 weights by token C={chunk} tau={tau}")
+    h = hla()
+    B, H, T = 1, 2, 5 * chunk + 10
+    k, r = prompt(h, B, T, H, 128, 64, "bf16", chunk=chunk, tau=tau)
+    for gate_tokens in (None, 1):
+        c = h.cache8_alloc(B, H, 8, 128, 64, 0, "e4m3")
+        S, A = h.prefill_to_cache8(c, r, T, C=chunk, **({} if gate_tokens is None else dict(gate_tokens=gate_tokens)))
+        for hh in range(H):
+            want = o8.gate_weights(f32s(r["gates"])[0, hh], tau, 6)[:5] * (chunk if gate_tokens is None else 1)
+            got = c.weight[0, hh].tolist()
+            assert np.all(np.abs(np.array(got[:5]) - want) <= 8 * EPS * max(1.0, want.max()))
+            assert got[5:] == [0.0] * 3
+    gi = torch.full((B, H, 8), 0.5, device="cuda")
+    before = c.weight.clone()
+    tok, gates, _, _ = token(B, H, 128, 64, "bf16", False, 331)
+    h.gdn_decode8(*tok, *gates, S, A, c, gates_in=gi)
+    assert torch.equal(c.weight[..., :5], before[..., :5] + 0.5)  # one token's gate
+
+
 def test_prefills_that_do_not_fit_are_refused():
     """The same refusals as on the host, of results that a prefill gave."""
     note("cache8 prompt refusals")
