@@ -226,8 +226,6 @@ __device__ __forceinline__ Fixed fixed_for(float bound) {
 // Magnitudes compare as their bits, and what is not finite is above every number.  Fixed point ends
 // at 2^127: from there on it makes NaN, as of what is not finite.
 constexpr unsigned kFixedEnd = 0x7f000000u;
-__device__ __forceinline__ unsigned mag(float x) { return __builtin_bit_cast(unsigned, x) & 0x7fffffffu; }
-__device__ __forceinline__ unsigned max_u(unsigned a, unsigned b) { return a > b ? a : b; }
 // Largest over the lanes 16, 32 and 48 apart (the lanes of one 16-lane row hold the same value).
 __device__ __forceinline__ unsigned rows_max(unsigned x) {
   auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);

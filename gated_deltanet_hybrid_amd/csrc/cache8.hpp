@@ -30,9 +30,14 @@ __device__ __forceinline__ int cache8_slot(const Cache8View& c, int64_t row, int
 // The stored formats.  A block with largest magnitude m is multiplied by (1 / m) top and rounded
 // to the nearest stored value, ties to even, so that m lands on `top`; the scale is m (1 / top).
 // Each of the two factors is rounded twice, as written: what is stored depends on the last bit.
-// m < 2^-100 stores zeros with scale 0, since 1 / m would overflow.
+// m < 2^-100 stores zeros with scale 0, since 1 / m would overflow.  A block with a number that is
+// not finite stores zeros with scale NaN, so that every decode that reads it shows it.
+// m is held as its bits: magnitudes compare as those, and what is not finite is above every number
+// (fmaxf would drop a NaN).
 constexpr int kI8 = 0, kE4M3 = 1;
-constexpr float kCache8Tiny = 0x1p-100f;
+constexpr unsigned kCache8Tiny = (127u - 100u) << 23, kNotFinite = 0x7f800000u;
+__device__ __forceinline__ unsigned mag(float x) { return __builtin_bit_cast(unsigned, x) & 0x7fffffffu; }
+__device__ __forceinline__ unsigned max_u(unsigned a, unsigned b) { return a > b ? a : b; }
 template <int FMT> struct Stored;
 template <> struct Stored<kI8> {
   static constexpr float top = 127.f;
@@ -69,12 +74,15 @@ template <int FMT> __device__ __forceinline__ bf16x8 stored_frag(unsigned w0, un
   return __builtin_bit_cast(bf16x8, make_uint4(two(w0, 0), two(w0, 16), two(w1, 0), two(w1, 16)));
 }
 
-template <int FMT> __device__ __forceinline__ float to_stored(float m) {
-  return m >= kCache8Tiny ? (1.f / m) * Stored<FMT>::top : 0.f;
+template <int FMT> __device__ __forceinline__ float to_stored(unsigned m) {
+  return m >= kCache8Tiny && m < kNotFinite ? (1.f / __builtin_bit_cast(float, m)) * Stored<FMT>::top : 0.f;
 }
-template <int FMT> __device__ __forceinline__ float from_stored(float m) {
-  return m >= kCache8Tiny ? m * (1.f / Stored<FMT>::top) : 0.f;
+template <int FMT> __device__ __forceinline__ float from_stored(unsigned m) {
+  if (m >= kNotFinite) return __builtin_nanf("");
+  return m >= kCache8Tiny ? __builtin_bit_cast(float, m) * (1.f / Stored<FMT>::top) : 0.f;
 }
+// the packed words of a block are taken through this: none of one that is not finite
+__device__ __forceinline__ unsigned stored_mask(unsigned m) { return m < kNotFinite ? ~0u : 0u; }
 
 struct Decode8Args {
   Cache8View c;

@@ -22,16 +22,17 @@ template <class T> __device__ __forceinline__ void unpack16(const uint4& raw, fl
   for (int i = 0; i < (int)(16 / sizeof(T)); ++i) f[i] = to_f<T>(e[i]);
 }
 
-// Largest magnitude over the block, on every thread.
+// Largest magnitude (as bits) over the block, on every thread.
 template <int NT>
-__device__ __forceinline__ float block_max(float x, float* red) {
-  x = wave_max(x);
+__device__ __forceinline__ unsigned block_max(unsigned x, unsigned* red) {
+#pragma unroll
+  for (int off = 32; off > 0; off /= 2) x = max_u(x, __shfl_xor(x, off, 64));
   __syncthreads();  // red may still be read from the call before
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
   __syncthreads();
-  float m = red[0];
+  unsigned m = red[0];
 #pragma unroll
-  for (int i = 1; i < NT / 64; ++i) m = fmaxf(m, red[i]);
+  for (int i = 1; i < NT / 64; ++i) m = max_u(m, red[i]);
   return m;
 }
 
@@ -58,19 +59,21 @@ template <class T, int DK, int W, int NT> struct MapRegs {
     unpack16<T>(raw[p][i], f);
     return f[e] - (SUB && (u / CPR) * 4 + i == (u % CPR) * E + e ? 1.f : 0.f);
   }
-  template <bool SUB> __device__ __forceinline__ float largest() const {
-    float m = 0.f;
+  template <bool SUB> __device__ __forceinline__ unsigned largest() const {
+    unsigned m = 0;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
       if (UNITS % NT != 0 && p * NT + (int)threadIdx.x >= UNITS) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(value<SUB>(p, i, e)));
+        for (int e = 0; e < E; ++e) m = max_u(m, mag(value<SUB>(p, i, e)));
     }
     return m;
   }
-  template <bool SUB, int FMT, int LD> __device__ __forceinline__ void store(uint8_t* img, float inv) const {
+  template <bool SUB, int FMT, int LD> __device__ __forceinline__ void store(uint8_t* img, unsigned m) const {
+    const float inv = to_stored<FMT>(m);
+    const unsigned mask = stored_mask(m);
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
       const int u = p * NT + threadIdx.x;
@@ -79,7 +82,7 @@ template <class T, int DK, int W, int NT> struct MapRegs {
       for (int e = 0; e < E; ++e)
         *reinterpret_cast<unsigned*>(img + ((u % CPR) * E + e) * LD + (u / CPR) * 4) =
             Stored<FMT>::pack(value<SUB>(p, 0, e) * inv, value<SUB>(p, 1, e) * inv, value<SUB>(p, 2, e) * inv,
-                              value<SUB>(p, 3, e) * inv);
+                              value<SUB>(p, 3, e) * inv) & mask;
     }
   }
 };
@@ -111,7 +114,7 @@ template <int FMT, class T, int DK, int DV, int NT>
 __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
   constexpr int LD = DK + 4;  // image row: one word of padding spreads the transposed writes over the banks
   __shared__ __align__(16) uint8_t s_img[(DK + DV) * LD];
-  __shared__ float s_red[NT / 64];
+  __shared__ unsigned s_red[NT / 64];
   const int64_t row = blockIdx.x / a.n_src;
   const int i = (int)(blockIdx.x % a.n_src), tid = threadIdx.x;
   const int held = a.reset ? 0 : cache8_count(a.c, row), add = append_count(a, row, held);
@@ -133,14 +136,13 @@ __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
   MapRegs<T, DK, DV, NT> rb;
   ra.load(At);
   rb.load(Bc);
-  const float ma = block_max<NT>(ra.template largest<true>(), s_red);
-  const float mb = block_max<NT>(rb.template largest<false>(), s_red);
-  const float ia = to_stored<FMT>(ma), ib = to_stored<FMT>(mb);
-  ra.template store<true, FMT, LD>(s_img, ia);
-  rb.template store<false, FMT, LD>(s_img + DK * LD, ib);
+  const unsigned ma = block_max<NT>(ra.template largest<true>(), s_red);
+  const unsigned mb = block_max<NT>(rb.template largest<false>(), s_red);
+  ra.template store<true, FMT, LD>(s_img, ma);
+  rb.template store<false, FMT, LD>(s_img + DK * LD, mb);
 
   // representatives: rows of one head, H dk elements apart
-  float mr = 0.f;
+  unsigned mr = 0;
   constexpr int E = 16 / sizeof(T), CPR = DK / E;
   if (a.c.n_rep) {
     const T* rep = reinterpret_cast<const T*>(a.reps) +
@@ -150,10 +152,11 @@ __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
       float f[E];
       unpack16<T>(raw, f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) mr = fmaxf(mr, fabsf(f[e]));
+      for (int e = 0; e < E; ++e) mr = max_u(mr, mag(f[e]));
     }
     mr = block_max<NT>(mr, s_red);
     const float ir = to_stored<FMT>(mr);
+    const unsigned mask = stored_mask(mr);
     uint8_t* out = a.c.reps + slot * a.c.n_rep * DK;
     for (int u = tid; u < a.c.n_rep * CPR; u += NT) {
       const uint4 raw = *reinterpret_cast<const uint4*>(rep + (int64_t)(u / CPR) * a.H * DK + (u % CPR) * E);
@@ -162,7 +165,7 @@ __global__ __launch_bounds__(NT) void append8_kernel(Append8Args a) {
 #pragma unroll
       for (int e = 0; e < E; e += 4)
         *reinterpret_cast<unsigned*>(out + u * E + e) =
-            Stored<FMT>::pack(f[e] * ir, f[e + 1] * ir, f[e + 2] * ir, f[e + 3] * ir);
+            Stored<FMT>::pack(f[e] * ir, f[e + 1] * ir, f[e + 2] * ir, f[e + 3] * ir) & mask;
     }
   }
   __syncthreads();

@@ -802,7 +802,8 @@ def cache8_append(cache, At, Bc, reps=None, src=None, n_new=None, weight_in=None
     chunk i's rows [i n_rep, (i + 1) n_rep).  src [Bs, H, L] int32 names the source chunk of
     every appended one, n_new [Bs, H] int32 how many to append, weight_in [Bs, H, L] their
     weights.  reset empties the cache first; reset_live sets the source maps to A = I, B = 0
-    where they were appended.  Chunks past the cache's room are dropped."""
+    where they were appended.  Chunks past the cache's room are dropped.  A map with a NaN or an
+    infinity makes every decode that reads it NaN."""
     c = cache
     if At.dim() == 4:
         At, Bc = At.unsqueeze(2), Bc.unsqueeze(2)

@@ -373,7 +373,8 @@ typedef struct {
  * Of each of X = A - I, X = B and X = the representatives of one chunk and head, with m the
  * largest |X| and Q = 127 (int8) or 448 (e4m3): scale = m (1 / Q), and X ((1 / m) Q) is rounded
  * to the nearest stored value, ties to even, every operation in float32; m < 2^-100 stores
- * zeros with scale 0.  The inputs are finite.
+ * zeros with scale 0.  An X with a NaN or an infinity stores zeros with scale NaN: a decode that
+ * reads the chunk gives NaN (of representatives its gate is NaN, which is below every threshold).
  *   At [Bs, H, ld_src, dk, dk], Bc [Bs, H, ld_src, dk, dv] (dtype): maps as
  *           hla_chunk_transitions writes them, the first n_src of each row being complete
  *           chunks (0 <= n_src <= ld_src; a partial last chunk is not appended); or with

@@ -22,6 +22,8 @@ def quantise(X, fmt):
     X = np.asarray(X, np.float32)
     m = np.float32(np.max(np.abs(X))) if X.size else np.float32(0)
     top = np.float32(TOP[fmt])
+    if not np.all(np.isfinite(X)):
+        return np.zeros(X.shape), float("nan")
     if not m >= np.float32(2.0 ** -100):
         return np.zeros(X.shape), 0.0
     y = (X * (np.float32(1) / m * top)).astype(np.float64)
