@@ -858,14 +858,16 @@ hipError_t pick_decode8(const Decode8Args& a, int dk, int dv, hipStream_t s) {
 
 }  // namespace
 
-// Which form a call takes, from its sizes alone.  In microseconds, fitted to both forms' times
-// (dk = 128 / 64, n = n_cap chunks): one workgroup a row takes (0.65 + 0.0055 n_rep) n / (0.47 +
-// 0.0025 n_rep) n, whatever the number of rows up to the CUs'; the split form 42 + 0.1 n / 26 +
-// 0.06 n for its launches and the walk over the segments, and 0.0145 n / 0.0033 n for every row
-// (the composition's matrix products, and the maps read a second time).  Measured, split and not:
-// dk = 128, n_rep = 2: n = 1024: 1 row 136 and 665, 16 rows 346 and 675, 48 rows 808 and 683;
-// n = 128: 8 rows 67 and 94, 32 rows 115 and 97; n = 64: 8 rows 54 and 51.  n_rep = 64, n = 64, 16
-// rows: 62 and 71.  dk = 64: n = 512: 64 rows 147 and 265, 128 rows 270 and 267.
+// Which form a call takes, from its sizes and whether it scores representatives (n_rep = 0 here where
+// the gates are given).  In microseconds, fitted to both forms' times (dk = 128 / 64, n = n_cap
+// chunks): one workgroup a row takes (0.65 + 0.0055 n_rep) n / (0.47 + 0.0025 n_rep) n, whatever the
+// number of rows up to the CUs'; the split form 42 + 0.1 n / 26 + 0.06 n for its launches and the walk
+// over the segments, and 0.0145 n / 0.0033 n for every row (the composition's matrix products, and the
+// maps read a second time).  Measured, split and not: dk = 128, n_rep = 2: n = 1024: 1 row 136 and 665,
+// 16 rows 346 and 675, 48 rows 808 and 683; n = 128: 8 rows 67 and 94, 32 rows 115 and 97; n = 64: 8
+// rows 54 and 51.  n_rep = 64, n = 64, 16 rows: 62 and 71.  dk = 64: n = 512: 64 rows 147 and 265, 128
+// rows 270 and 267.  With the gates given: dk = 128, n = 1024: 50 rows 809 and 670, 100 rows 1523 and
+// 697; n = 64, 16 rows: 58 and 52; dk = 64, n = 512, 160 rows: 279 and 242.
 static bool split_pays(int64_t rows, int n, int n_rep, int dk) {
   const float whole = dk == 128 ? 0.65f + 0.0055f * n_rep : 0.47f + 0.0025f * n_rep;
   const float fixed = dk == 128 ? 42.f + 0.1f * n : 26.f + 0.06f * n, each = dk == 128 ? 0.0145f : 0.0033f;
@@ -876,7 +878,7 @@ int64_t plan_decode8(Decode8Args& a, int dk, int dv, void* ws) {
   const int64_t rows = a.c.rows;
   const int n_cap = a.c.n_cap;
   a.segs = 0;
-  if (!split_pays(rows, n_cap, a.c.n_rep, dk)) return 0;
+  if (!split_pays(rows, n_cap, a.gates_in ? 0 : a.c.n_rep, dk)) return 0;
   // a segment's composition and its chain take turns with the walk over the segments, at about
   // sqrt(n / 2) of each; and no more than four workgroups of the composition for each CU
   int len = (int)(sqrtf(n_cap / 2.f) + 0.5f);

@@ -118,7 +118,7 @@ __device__ __forceinline__ int split_segments(const Decode8Args& a, int held) {
   return held < kSplitFrom ? 1 : (held + a.seg_len - 1) / a.seg_len;
 }
 // Sets the form of a call and its workspace (offsets from `ws`, which may be null); returns the
-// workspace's bytes.
+// workspace's bytes.  Without gates_in it is the most that a call on the cache takes.
 int64_t plan_decode8(Decode8Args& a, int dk, int dv, void* ws);
 hipError_t launch_decode8(const Decode8Args& a, int fmt, int dtype, int dk, int dv, hipStream_t s);
 
