@@ -408,9 +408,13 @@ hla_status_t hla_cache8_append(const hla_cache8_t* c, int32_t dtype, int32_t n_s
  *   gates_out [Bs, H, n_cap] float32 or NULL: every held position's gate, 0 behind them.
  *   o         [Bs, H, dv] float32 out.
  *   The cache is read; its weight (if any) gains every held position's gate after the
- *   threshold.  A gate that is NaN is below every threshold.  The vectors that meet int8
- *   chunks (q for the gates, At_cur^T q as the chunks pass it on) hold values below 2^127; a
- *   larger one makes the gates, or o, NaN.
+ *   threshold.  A gate that is NaN is below every threshold.
+ *   The vectors that meet the chunks are q (for the gates) and At_cur^T q as the chunks pass it
+ *   on.  Over int8 chunks they enter as fixed point, to 2^-22 of the vector's largest magnitude (of
+ *   the one before the last chunk, where that chunk shrank it), so that a row of a map that reads
+ *   only the smallest elements sees them coarsely; they hold values below 2^127, and a larger one
+ *   makes the gates, or o, NaN.  Over e4m3 chunks they enter as float32; a sum over values of 2^112
+ *   and above may pass float32's range and is then not finite.
  *   ws, ws_bytes: workspace of at least hla_decode8_workspace_bytes() bytes, 16-byte aligned
  *           (0 but for few rows with a long cache, whose positions are cut into segments: then
  *           mostly a float32 dk x dk matrix a segment; a call with gates_in may leave it

@@ -7,7 +7,7 @@ import torch
 
 from gpu_util import host, note
 from test_cache8_bounds_cpu import SCALES
-from test_gpu_cache8 import hla, make_cache, rnd, token
+from test_gpu_cache8 import EPS, hla, make_cache, rnd, row_cache, token
 from test_gpu_cache8_precision import check_close
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +108,29 @@ def test_a_scale_that_is_not_finite_is_not_hidden(n_cap, part):
         assert not np.isfinite(o[0, 1]).any()
         gi[0, 1, n_cap // 2 + 1] = 0.0  # and a skipped one is not read
         assert np.isfinite(host(h.gdn_decode8(*tok, *gates, S, A, c, gates_in=gi))).all()
+
+
+@pytest.mark.parametrize("n_cap", [20, 200])
+def test_e4m3_z_up_to_the_end_of_its_sums(n_cap):
+    """The sums over e4m3 chunks are float32 sums of the stored numbers times z: z below 2^112 is
+    exact, a larger one is right or not finite."""
+    note(f"cache8 e4m3 largest z {n_cap}")
+    h = hla()
+    for zmax in (1.5 * 2.0 ** 111, 1.5 * 2.0 ** 127):
+        c = make_cache(h, 1, 1, n_cap, 64, 64, 0, "e4m3", 541)
+        c.count.fill_(n_cap)
+        c.scale[..., 0] = 0.0  # A = I
+        c.scale[..., 1] = 2.0 ** -20
+        zero, one = torch.zeros(1, 1, 64, device="cuda"), torch.ones(1, 1, device="cuda")
+        q = zero.clone()
+        q[..., 3] = 1.0
+        S, A = torch.zeros(1, 1, 64, 64, device="cuda"), torch.zeros(1, 1, 64, 64, device="cuda")
+        A[0, 0, 3, 5] = zmax
+        gi = torch.zeros(1, 1, n_cap, device="cuda")
+        gi[..., n_cap // 2] = 1.0
+        o = host(h.gdn_decode8(q, zero, zero, 0 * one, one, S, A, c, gates_in=gi, tau=0.5))[0, 0]
+        ref = row_cache(c, 0, 0)[1][n_cap // 2][:, 5] * zmax
+        right = np.abs(o - ref) <= 4 * EPS * np.abs(ref)
+        assert np.all(right | ~np.isfinite(o))
+        if zmax < 2.0 ** 112:
+            assert np.all(right)
