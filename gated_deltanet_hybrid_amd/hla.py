@@ -777,7 +777,8 @@ class Cache8:
 
 
 def cache8_alloc(Bs, H, n_cap, dk, dv, n_rep=0, fmt="int8", weights=True, device="cuda"):
-    """An empty 8-bit chunk cache (fmt "int8" or "e4m3")."""
+    """An empty 8-bit chunk cache (fmt "int8" or "e4m3").  Of a decode's output int8 changes about
+    1 % and e4m3 about 2.5 % where most of it comes from the cache (bfloat16 maps: 0.2 %)."""
     dtype = CACHE_FORMATS[fmt][1]
     e = lambda *s, dt: torch.zeros(s, dtype=dt, device=device)  # noqa: E731
     return Cache8(maps=e(Bs, H, n_cap, dk + dv, dk, dt=torch.uint8).view(dtype),

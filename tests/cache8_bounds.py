@@ -109,3 +109,33 @@ def gate(q, R8, scale, fmt):
     var = (share ** 2 * vs).sum() + EPS ** 2 * (len(s) / 2 + 32 + 8 * logit ** 2)
     g = 1.0 / (1.0 + np.exp(-logit))
     return g, SIGMAS * np.sqrt((g * (1 - g)) ** 2 * var + EPS ** 2 * 16 * g ** 2)
+
+
+def step_variance(X, fmt):
+    """Variance of each number of a block that is stored in 8 bits: a rounding error spread evenly over
+    a step of the stored value, in the block's own unit."""
+    top = {"int8": 127.0, "e4m3": 448.0}[fmt]
+    m = np.max(np.abs(X))
+    if m == 0.0:
+        return np.zeros(X.shape)
+    y = np.abs(X) / m * top
+    step = np.ones(X.shape) if fmt == "int8" else 2.0 ** (np.floor(np.log2(np.maximum(y, 2.0 ** -6))) - 3)
+    return (step * m / top) ** 2 / 12
+
+
+def unquantised(q, k, v, gates, S, A, cA, cB, ghat, fmt):
+    """(o over the maps cA [n, dk, dk] and cB [n, dv, dk] as they were before they were stored in 8
+    bits, what storing them may change o by: six standard deviations of the stored numbers' roundings,
+    carried along the chain)."""
+    a, e, w = token_rows(q, k, v, gates)
+    o, _ = live(S, q, k, a, e, w)
+    z, _ = live(A, q, k, a, e, None)
+    vo, vz = np.zeros(len(o)), np.zeros(len(z))
+    for j in reversed(range(len(ghat))):
+        g, E = ghat[j], cA[j] - np.eye(len(q))
+        o = o + g * (cB[j] @ z)
+        vo = vo + g ** 2 * (cB[j] ** 2 @ vz + step_variance(cB[j], fmt) @ (z ** 2 + vz))
+        vz = (1 + g * np.diagonal(E)) ** 2 * vz - (g * np.diagonal(E)) ** 2 * vz + g ** 2 * (
+            E ** 2 @ vz + step_variance(E, fmt) @ (z ** 2 + vz))
+        z = z + g * (E @ z)
+    return o, SIGMAS * np.sqrt(vo)

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import cache8_bounds as cb
-from gpu_util import host, note
+from gated_deltanet_hybrid_amd import inputs
+from gpu_util import host, note, token_tensors
 from test_gpu_cache8 import hla, make_cache, rnd, token, values
 
 pytestmark = pytest.mark.gpu
@@ -142,3 +143,33 @@ def test_both_forms_to_rounding(fmt):
     St, At = part(S), part(A)
     check_close(h, big, tok, gates, S, A, rows=rows)
     check_close(h, small, [part(t) for t in tok], [part(t) for t in gates], St, At)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("alpha_mode", ["slow", "config"])
+@pytest.mark.parametrize("n,dk,dv", [(1, 128, 128), (20, 64, 128), (100, 128, 64)], ids=str)
+def test_what_eight_bits_cost(fmt, alpha_mode, n, dk, dv):
+    """A prompt's chunks in the cache against the same decode over their unquantised maps: within what
+    the stored numbers' roundings explain (the float32 arithmetic is three orders below)."""
+    note(f"cache8 cost {fmt} {alpha_mode} {n} {dk} {dv}")
+    h = hla()
+    H = 2
+    x = inputs.gen_tokens(1, 64 * n, H, dk, dv, dtype="f32", seed=441, alpha_mode=alpha_mode)
+    _, k, v, beta, alpha = token_tensors(x)
+    At, Bc = h.chunk_transitions(k, v, beta, alpha)
+    c = h.cache8_alloc(1, H, n, dk, dv, 0, fmt)
+    h.cache8_append(c, At, Bc)
+    tok, gates, _, _ = token(1, H, dk, dv, "f32", False, 442)
+    S, A = torch.zeros(1, H, dk, dv, device="cuda"), torch.eye(dk, device="cuda").repeat(1, H, 1, 1)
+    S0, A0 = host(S), host(A)
+    gi = 0.1 + 0.8 * rnd(443)[1](1, H, n)
+    o = host(h.gdn_decode8(*tok, *gates, S, A, c, gates_in=gi))
+    for hh in range(H):
+        maps = [host(t)[0, hh].transpose(0, 2, 1) for t in (At, Bc)]
+        tk, gt = [host(t)[0, hh] for t in tok], [host(t)[0, hh] for t in gates]
+        ref, tol = cb.unquantised(*tk, gt, S0[0, hh], A0[0, hh], *maps, host(gi)[0, hh], fmt)
+        past = ref - cb.live(S0[0, hh], tk[0], tk[1], *cb.token_rows(*tk, gt))[0]
+        off = o[0, hh] - ref
+        assert np.all(np.abs(off) <= tol + 1e-5 * np.max(np.abs(ref))), float(np.max(np.abs(off) / tol))
+        share = np.linalg.norm(off) / np.linalg.norm(past)
+        note(f"  {share:.4f} of the past's share, {float(np.max(np.abs(off) / tol)):.2f} of the bound")
