@@ -10,9 +10,9 @@
 //       o += ghat_j sB_j (B_j x),   z = x + ghat_j sA_j (E_j x),   weight_j += ghat_j
 // Chunks with ghat_j = 0 are not read.  (The composition of states, [dv, dk] a chunk, is never
 // formed: read backwards, only the vector z passes from chunk to chunk.)
-// Many rows: bound by HBM.  256 x 16 rows of 64 chunks (dk = dv = 128, int8, 64 representatives,
-// 11.8 GB) take 1.83 - 1.93 ms, 6.1 - 6.45 TB/s; 2.15 GB of it are the live matrices, read and
-// written.  Few rows: bound by the chain's latency, 0.65 us a chunk at dk = 128 and 0.5 at 64 (LDS
+// Many rows: bound by HBM.  256 x 16 rows of 64 chunks (dk = dv = 128, int8, 64 representatives)
+// take 1.92 ms: 8.59 GB of maps, 2.15 of representatives and 1.07 of live matrices, read and
+// written, are 11.8 GB at 6.2 TB/s (counters: 11.56 GB fetched, 0.54 written).  Few rows: bound by the chain's latency, 0.65 us a chunk at dk = 128 and 0.5 at 64 (LDS
 // reads, the product, the sums, the new terms and a barrier, one after the other).
 #include <hip/hip_runtime.h>
 
@@ -880,7 +880,8 @@ int64_t plan_decode8(Decode8Args& a, int dk, int dv, void* ws) {
   a.segs = 0;
   if (!split_pays(rows, n_cap, a.gates_in ? 0 : a.c.n_rep, dk)) return 0;
   // a segment's composition and its chain take turns with the walk over the segments, at about
-  // sqrt(n / 2) of each; and no more than four workgroups of the composition for each CU
+  // sqrt(n / 2) of each; and, as far as the longest segment allows, no more than four workgroups of
+  // the composition for each CU (up to 64 rows of 1024 chunks; above that they take turns)
   int len = (int)(sqrtf(n_cap / 2.f) + 0.5f);
   const int busy = (int)((rows * n_cap + 1023) / 1024);
   if (len < busy) len = busy;

@@ -277,7 +277,8 @@ __device__ __forceinline__ unsigned order_key(float x) {
 // it leaves, and of the equal ones the first in time.  All of a row is read before any of it is
 // written, so outputs may be the inputs.  Latency: 32 rounds of ballots, 9 us for 128 rows of 1024
 // by four waves a row (19 by one, whose 16 ballots a round follow one another), 4 us for 64
-// positions.  Up to 256 positions one wave needs at most four ballots a round and no barrier.
+// positions, 25 us for 512 rows of 4096 and 43 us for 128 rows of 16384 (16 positions a lane).
+// Up to 256 positions one wave needs at most four ballots a round and no barrier.
 template <int NI, int NW>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void evict_kernel(EvictArgs a) {
   constexpr int RPB = NW == 1 ? 4 : 1;  // rows per workgroup

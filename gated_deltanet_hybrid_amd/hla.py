@@ -706,7 +706,6 @@ def _decode(fn, gates, q, k, v, S_cur, At_cur, At_cache, Bc_cache, reps_cache, n
 
 # ------------------------------------------------------------------ the 8-bit chunk cache
 CACHE_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
-MAX_CACHE_REPS = 256
 
 
 def _need_on(t, shape, dtype, device, name):
