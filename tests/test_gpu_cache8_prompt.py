@@ -131,3 +131,30 @@ def test_prefills_that_do_not_fit_are_refused():
     assert not c.count.any()
     h.prefill_to_cache8(c, r, 96)
     assert c.count.tolist() == [[1, 1]]
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_gdn2_live_chunk_enters_the_cache(fmt):
+    """Gated DeltaNet-2 as it is served: 250 tokens, then steps until the live chunk is complete, the full
+    cache drops its lightest chunk and takes it, and steps over the new set."""
+    note(f"cache8 gdn2 serve {fmt}")
+    h = hla()
+    B, H, T, dk, dv = 1, 2, 250, 64, 128
+    k, r = prompt(h, B, T, H, dk, dv, "bf16", gdn2=True)
+    c = h.cache8_alloc(B, H, 3, dk, dv, C, fmt)
+    S, A = h.prefill_to_cache8(c, r, T)
+    live = [k[:, T // C * C:]]
+    for s in range(9):
+        tok, gates, _, _ = token(B, H, dk, dv, "bf16", True, 350 + s)
+        check_decode(h, c, tok, gates, S, A)
+        live.append(tok[1].unsqueeze(1))
+        if (T + s + 1) % C == 0:
+            keys, S0, A0 = torch.cat(live, 1).float().contiguous(), f32s(S), f32s(A)
+            assert keys.shape[1] == C
+            weights = c.weight.clone()
+            h.cache8_evict(c, 2, 1)
+            h.cache8_append(c, A, S, keys, reset_live=True)
+            for hh in range(H):
+                assert c.weight[0, hh, 2] == 0 and c.weight[0, hh, 1] == weights[0, hh, 2]  # the newest stayed
+                check_slot(c, 0, hh, int(c.order[0, hh, 2]), A0[0, hh], S0[0, hh], f32s(keys)[0, :, hh], fmt)
+    assert c.count.tolist() == [[3, 3]] and s > 6
