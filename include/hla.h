@@ -417,8 +417,9 @@ hla_status_t hla_cache8_append(const hla_cache8_t* c, int32_t dtype, int32_t n_s
  *   and above may pass float32's range and is then not finite.
  *   ws, ws_bytes: workspace of at least hla_decode8_workspace_bytes() bytes, 16-byte aligned
  *           (0 but for few rows with a long cache, whose positions are cut into segments: then
- *           mostly a float32 dk x dk matrix a segment; a call with gates_in may leave it
- *           unused).  It belongs to one call at a time.
+ *           mostly a float32 dk x dk matrix a segment, the product of up to 64 neighbouring
+ *           chunks' gated maps, which has to lie in float32's range; a call with gates_in may
+ *           leave it unused).  It belongs to one call at a time.
  * Appending the live chunk is hla_cache8_append's (reset_live).
  * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE, HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN,
  *         HLA_ERR_WORKSPACE, HLA_ERR_HIP.
