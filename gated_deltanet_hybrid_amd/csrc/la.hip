@@ -1,0 +1,674 @@
+// Linear attention with a decay for each head: M_t = exp(g_t) M_{t-1} + k_t v_t^T, o_t = M_t^T q_t.
+//
+// A piece of P tokens from state M_0, with lg the inclusive sums of g over it (float64, in units of
+// log 2) and D_ij = 2^(lg_i - lg_j) for j <= i:
+//     o_i = 2^lg_i M_0^T q_i + sum_{j<=i} D_ij (q_i . k_j) v_j
+//     M_P = 2^lg_P M_0 + sum_j 2^(lg_P - lg_j) k_j v_j^T
+// so a piece is four matrix products: scores K Q^T, Q M, (D o scores) V and K^T (decayed V).
+// The gradients are the same recurrence with the roles changed.  With G_t = dL/dM_t (o_t included),
+// G_t = exp(g_{t+1}) G_{t+1} + q_t do_t^T, and
+//     dq_t = M_t do_t       roles (do, v, k), state M^T, forward
+//     dv_t = G_t^T k_t      roles (k, q, do), state G, reversed
+//     dk_t = G_t v_t        roles (v, do, q), state G^T, reversed
+//     exp(g_t) dL/d(exp g_t) = exp(g_t) <G_t, M_{t-1}>, see la_decay_kernel.
+//
+// The state lives in the accumulators of the matrix cores: wave w owns columns [32 w, 32 w + 32) and
+// all dk rows, and an accumulator tile is the B operand of the next product without leaving its lane.
+// float32 tensors run on the float32 matrix instructions.  bf16 tensors enter exactly; what is float32
+// enters as bf16 terms, each of which takes 8 bits.  Three of them (24 bits) where the result comes out
+// as float32: the decayed values, which enter the states, and the state where the decays' gradient is
+// formed from it.  Two (2^-16 at most) for the state that outputs read, and one (2^-8) for the decayed
+// scores: these reach bf16 outputs only, which round to 2^-8 themselves.
+#include "la.hpp"
+#include "kernels.hpp"
+#include "timing.hpp"
+
+namespace hla {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr double kLog2e = 1.4426950408889634;
+constexpr float kLgFloor = -1.0e4f;  // stands for -inf: 2^-14427 is zero in every type used here
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+// exp(g) by way of log 2 in float64; a NaN stays
+__device__ __forceinline__ float decay_of(float g) {
+  return exp2_((float)((double)(g < kLgFloor ? kLgFloor : g) * kLog2e));
+}
+
+// The operands of a product over K: `Frag` is what a lane holds of KG consecutive k.
+// bf16: one 32x32x16 instruction, 8 values a lane.  float32: four 32x32x2, slot e of the group is
+// k = 4 h + e, which is also the order in which an accumulator holds its rows.
+template <class T> struct La;
+
+template <> struct La<bf16> {
+  static constexpr int P = 64, KG = 16, TERMS = 3;
+  using Frag = bf16x8;
+  // An LDS tile of W columns: rows of 16-byte chunks, permuted by the row so that the row reads (16
+  // rows, one chunk) and the transposing reads (4 rows, 4 chunks) both meet every bank once.
+  template <int W> __device__ __forceinline__ static int at(int row, int col) {
+    const int s = W == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    return row * W + (((col >> 3) ^ s) << 3) + (col & 7);
+  }
+  template <int W> static constexpr int size() { return P * W; }
+  static constexpr int PS = P + 8;  // row stride of the decayed scores
+  __device__ __forceinline__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  // k = 16 g + 8 h + e of one row
+  __device__ __forceinline__ static Frag plain(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
+  template <int W> __device__ __forceinline__ static Frag row(const bf16* t, int r, int g, int h) {
+    return plain(t + at<W>(r, g * 16 + h * 8));
+  }
+  // k = 16 g + 8 (e / 4) + 4 h + e % 4: the accumulators' order
+  template <int W> __device__ __forceinline__ static Frag rowc(const bf16* t, int r, int g, int h) {
+    const bf16x4 lo = *reinterpret_cast<const bf16x4*>(t + at<W>(r, g * 16 + h * 4));
+    const bf16x4 hi = *reinterpret_cast<const bf16x4*>(t + at<W>(r, g * 16 + 8 + h * 4));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  // column n0 + lane % 32, rows k = 16 g + 8 h + e: the transposing LDS read hands lane i of 16 the
+  // i-th column of the four rows that its 16 lanes address (4 lanes a row, 4 columns each)
+  template <int W> __device__ __forceinline__ static Frag col(const bf16* t, int n0, int g, int lane) {
+    const int k = g * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3), c = n0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + at<W>(k, c)));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + at<W>(k + 4, c)));
+    return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  __device__ __forceinline__ static int col_k(int g, int h) { return g * 16 + h * 8; }  // first of 8 k
+  // the first N bf16 terms of 8 float32 values
+  template <int N> __device__ __forceinline__ static void split(const float (&x)[8], Frag (&f)[N]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float r = x[e];
+#pragma unroll
+      for (int t = 0; t < N; ++t) {
+        f[t][e] = (bf16)r;
+        r -= (float)f[t][e];
+      }
+    }
+  }
+  static constexpr int FN = 8;
+};
+
+template <> struct La<float> {
+  static constexpr int P = 32, KG = 8, TERMS = 1;
+  using Frag = f32x4;
+  template <int W> __device__ __forceinline__ static int at(int row, int col) { return row * (W + 8) + col; }
+  template <int W> static constexpr int size() { return P * (W + 8); }
+  static constexpr int PS = P + 8;
+  __device__ __forceinline__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+  __device__ __forceinline__ static Frag plain(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+  template <int W> __device__ __forceinline__ static Frag row(const float* t, int r, int g, int h) {
+    return plain(t + at<W>(r, g * 8 + h * 4));
+  }
+  template <int W> __device__ __forceinline__ static Frag rowc(const float* t, int r, int g, int h) {
+    return row<W>(t, r, g, h);
+  }
+  template <int W> __device__ __forceinline__ static Frag col(const float* t, int n0, int g, int lane) {
+    Frag f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = t[at<W>(g * 8 + (lane >> 5) * 4 + e, n0 + (lane & 31))];
+    return f;
+  }
+  __device__ __forceinline__ static int col_k(int g, int h) { return g * 8 + h * 4; }
+  template <int N> __device__ __forceinline__ static void split(const float (&x)[4], Frag (&f)[N]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[0][e] = x[e];
+  }
+  static constexpr int FN = 4;
+};
+
+// The sums lg of one piece and what follows from them, in LDS.
+template <int P> struct Decays {
+  double lg[P];   // inclusive sums of g, in log 2
+  float gam[P];   // 2^lg: what is left of the piece's start
+  float w[P];     // 2^(lg_last - lg): what the piece's end has left of each row
+  float total;    // 2^lg_last
+};
+
+template <int P>
+__device__ __forceinline__ void decays(float g, int lane, Decays<P>& d, double* sum) {
+  g = g < kLgFloor ? kLgFloor : g;  // NaN stays
+  double x = lane < P ? (double)g * kLog2e : 0.0;
+#pragma unroll
+  for (int o = 1; o < P; o <<= 1) {
+    const double y = __shfl_up(x, o, 64);
+    if (lane >= o) x += y;
+  }
+  const double last = __shfl(x, P - 1, 64);
+  if (lane < P) {
+    d.lg[lane] = x;
+    d.gam[lane] = exp2_((float)x);
+    d.w[lane] = exp2_((float)(last - x));
+  }
+  if (lane == 0) d.total = exp2_((float)last);
+  *sum += last;
+}
+
+template <class T, int DK, int DV, bool OUT, int EXTRA> struct LaShared {
+  using O = La<T>;
+  alignas(16) T x1[OUT ? O::template size<DK>() : 8];
+  alignas(16) T x2[O::template size<DK>()];
+  alignas(16) T x3[O::template size<DV>()];
+  alignas(16) T x4[EXTRA ? O::template size<DV>() : 8];
+  alignas(16) T sc[OUT ? O::P * O::PS : 8];
+  Decays<O::P> d[2];
+  float dot[EXTRA ? DV / 32 : 1][O::P];
+  float erow[EXTRA > 1 ? 3 : 1][32], ecol[EXTRA > 1 ? 3 : 1][32];
+};
+
+// One workgroup of DV / 32 waves runs one segment of one row.  OUT: outputs from the state in front
+// of the segment; else the segment's state (from init, or zero).  EXTRA: the products with x4 that
+// the decays' gradient takes.
+template <class T, int DK, int DV, bool OUT, bool REV, int EXTRA>
+__global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
+  using O = La<T>;
+  using Frag = typename O::Frag;
+  constexpr int P = O::P, NT = DV * 2, NW = DV / 32, MT = DK / 32, IT = P / 32, V = 16 / (int)sizeof(T);
+  constexpr int N1 = P * DK / V / NT, N3 = P * DV / V / NT;  // 16-byte pieces a thread moves of each tile
+  __shared__ LaShared<T, DK, DV, OUT, EXTRA> sh;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, c = lane & 31;
+  const int64_t row = blockIdx.x / a.nseg;
+  const int seg = blockIdx.x % a.nseg;
+  if (!OUT && a.loc && !a.whole && seg == (REV ? 0 : a.nseg - 1)) return;  // no segment starts behind it
+  const int64_t b = row / a.H;
+  const int head = (int)(row % a.H);
+  int64_t Tb = a.T;
+  if (a.lens) {
+    Tb = a.lens[b];
+    Tb = Tb < 0 ? 0 : (Tb > a.T ? a.T : Tb);
+  }
+  const int64_t first = (int64_t)seg * a.seg_pieces;            // this segment's pieces
+  int64_t end = first + a.seg_pieces;
+  const int64_t all = (a.T + P - 1) / P, live = (Tb + P - 1) / P;
+  end = end < all ? end : all;
+  const int64_t last = end < live ? end : live;                 // [first, last) hold tokens
+  const int64_t n = last > first ? last - first : 0;
+
+  const int G1 = (int)(a.H / (a.x1.heads ? a.x1.heads : 1)), G2 = (int)(a.H / a.x2.heads), G3 = (int)(a.H / a.x3.heads);
+  const T* p1 = OUT ? (const T*)a.x1.p + (b * a.x1.ld * a.x1.heads + head / G1) * DK : nullptr;
+  const T* p2 = (const T*)a.x2.p + (b * a.x2.ld * a.x2.heads + head / G2) * DK;
+  const T* p3 = (const T*)a.x3.p + (b * a.x3.ld * a.x3.heads + head / G3) * DV;
+  const T* p4 = nullptr;
+  if constexpr (EXTRA) p4 = (const T*)a.x4.p + (b * a.x4.ld * a.x4.heads + head / (int)(a.H / a.x4.heads)) * DV;
+  const float* gp = a.per_head ? a.g + head : a.g + b * a.ld_g * a.H + head;
+
+  // row r of piece p is token P p + r, or counted from the piece's end
+  auto token = [&](int64_t p, int r) -> int64_t { return p * P + (REV ? P - 1 - r : r); };
+  auto load_g = [&](int64_t p) -> float {
+    if (lane >= P) return 0.f;
+    const int64_t t = token(p, lane) + (REV ? 1 : 0);
+    return t < Tb ? (a.per_head ? gp[0] : gp[t * a.H]) : 0.f;
+  };
+  uint4 r1[OUT ? N1 : 1], r2[N1], r3[N3], r4[EXTRA ? N3 : 1];
+  auto load_tile = [&](const T* base, int64_t stride, int width, int64_t p, uint4* regs, int count) {
+    const int cpr = width / V;
+#pragma unroll
+    for (int i = 0; i < count; ++i) {
+      const int id = i * NT + tid;
+      const int64_t t = token(p, id / cpr);
+      regs[i] = t < Tb ? *reinterpret_cast<const uint4*>(base + t * stride + (id % cpr) * V) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto load = [&](int64_t p) {
+    if constexpr (OUT) load_tile(p1, (int64_t)a.x1.heads * DK, DK, p, r1, N1);
+    load_tile(p2, (int64_t)a.x2.heads * DK, DK, p, r2, N1);
+    load_tile(p3, (int64_t)a.x3.heads * DV, DV, p, r3, N3);
+    if constexpr (EXTRA) load_tile(p4, (int64_t)a.x4.heads * DV, DV, p, r4, N3);
+  };
+  auto store = [&]() {
+#pragma unroll
+    for (int i = 0; i < N1; ++i) {
+      const int id = i * NT + tid, at = O::template at<DK>(id / (DK / V), id % (DK / V) * V);
+      if constexpr (OUT) *reinterpret_cast<uint4*>(sh.x1 + at) = r1[i];
+      *reinterpret_cast<uint4*>(sh.x2 + at) = r2[i];
+    }
+#pragma unroll
+    for (int i = 0; i < N3; ++i) {
+      const int id = i * NT + tid, at = O::template at<DV>(id / (DV / V), id % (DV / V) * V);
+      *reinterpret_cast<uint4*>(sh.x3 + at) = r3[i];
+      if constexpr (EXTRA) *reinterpret_cast<uint4*>(sh.x4 + at) = r4[i];
+    }
+  };
+  auto piece = [&](int64_t i) { return REV ? last - 1 - i : first + i; };
+
+  f32x16 M[MT];
+  const int col = 32 * w + c;
+  if (a.init) {
+    const float* s0 = a.init + row * a.init_row + (int64_t)seg * DK * DV;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int r = 32 * m + acc_row(e, h);
+        M[m][e] = a.init_t ? s0[col * DK + r] : s0[r * DV + col];
+      }
+  } else {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) M[m] = zero16();
+  }
+
+  double decay = 0.0;
+  if (n) {
+    load(piece(0));
+    if (w == NW - 1) decays<P>(load_g(piece(0)), lane, sh.d[0], &decay);
+  }
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t p = piece(i);
+    const Decays<P>& d = sh.d[i & 1];
+    store();
+    __syncthreads();
+    float gnext = 0.f;
+    if (i + 1 < n) {
+      load(piece(i + 1));
+      if (w == NW - 1) gnext = load_g(piece(i + 1));
+    }
+    f32x16 acc[IT];
+    if constexpr (OUT) {
+      // decayed scores, transposed: rows j, column i, so that a lane writes runs of one row
+      constexpr int TILES = IT == 2 ? 3 : 1;
+      for (int tile = w; tile < TILES; tile += NW) {
+        const int I = tile ? 1 : 0, J = tile == 2 ? 1 : 0;
+        f32x16 s = zero16();
+#pragma unroll
+        for (int g = 0; g < DK / O::KG; ++g)
+          s = O::mma(O::template row<DK>(sh.x2, 32 * J + c, g, h), O::template row<DK>(sh.x1, 32 * I + c, g, h), s);
+        const int ii = 32 * I + c;
+        const double lgi = d.lg[ii];
+        float D[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = 32 * J + acc_row(e, h);
+          D[e] = j <= ii ? exp2_((float)(lgi - d.lg[j])) : 0.f;
+          s[e] = j <= ii ? s[e] * D[e] : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          T* to = sh.sc + ii * O::PS + 32 * J + q * 8 + h * 4;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e] = (T)s[4 * q + e];
+        }
+        if constexpr (EXTRA > 1) {
+          // E_ij = D_ij (x1_i . x2_j)(x4_i . x3_j) for j < i: its sums over each row and each column
+          f32x16 u = zero16();
+#pragma unroll
+          for (int g = 0; g < DV / O::KG; ++g)
+            u = O::mma(O::template row<DV>(sh.x3, 32 * J + c, g, h), O::template row<DV>(sh.x4, 32 * I + c, g, h), u);
+          float rs = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = 32 * J + acc_row(e, h);
+            const float x = j < ii ? s[e] * u[e] : 0.f;
+            rs += x;
+            const float cs = lane_group_sum<32>(x);
+            if (c == 0) sh.ecol[tile][acc_row(e, h)] = cs;
+          }
+          rs = swap32_sum(rs);
+          if (h == 0) sh.erow[tile][c] = rs;
+        }
+      }
+      // what the piece's start gives: Q M, rows scaled by what is left of it
+#pragma unroll
+      for (int I = 0; I < IT; ++I) acc[I] = zero16();
+#pragma unroll
+      for (int g = 0; g < DK / O::KG; ++g) {
+        constexpr int GT = 32 / O::KG, TERMS = EXTRA || O::TERMS < 2 ? O::TERMS : 2;
+        float x[O::FN];
+        Frag f[TERMS];
+#pragma unroll
+        for (int e = 0; e < O::FN; ++e) x[e] = M[g / GT][O::FN * (g % GT) + e];
+        O::split(x, f);
+#pragma unroll
+        for (int I = 0; I < IT; ++I) {
+          const Frag q = O::template rowc<DK>(sh.x1, 32 * I + c, g, h);
+#pragma unroll
+          for (int t = TERMS - 1; t >= 0; --t) acc[I] = O::mma(q, f[t], acc[I]);
+        }
+      }
+#pragma unroll
+      for (int I = 0; I < IT; ++I)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = 32 * I + acc_row(e, h);
+          acc[I][e] *= d.gam[r];
+          if constexpr (EXTRA) {
+            const float x = lane_group_sum<32>(acc[I][e] * (float)sh.x4[O::template at<DV>(r, col)]);
+            if (c == 0) sh.dot[w][r] = x;
+          }
+        }
+    }
+    if (i + 1 < n && w == NW - 1) decays<P>(gnext, lane, sh.d[(i + 1) & 1], &decay);
+    if constexpr (OUT) __syncthreads();
+    // the decayed values join the state; the scores meet the values as they are
+    const float total = d.total;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) M[m][e] *= total;
+#pragma unroll
+    for (int g = 0; g < P / O::KG; ++g) {
+      const Frag v = O::template col<DV>(sh.x3, 32 * w, g, lane);
+      if constexpr (OUT) {
+#pragma unroll
+        for (int I = 0; I < IT; ++I)
+          if (g * O::KG < 32 * (I + 1))
+            acc[I] = O::mma(O::plain(sh.sc + (32 * I + c) * O::PS + O::col_k(g, h)), v, acc[I]);
+      }
+      float x[O::FN];
+      Frag f[O::TERMS];
+      const int k0 = O::col_k(g, h);
+#pragma unroll
+      for (int e = 0; e < O::FN; ++e) x[e] = (float)v[e] * d.w[k0 + e];
+      O::split(x, f);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const Frag k = O::template col<DK>(sh.x2, 32 * m, g, lane);
+#pragma unroll
+        for (int t = O::TERMS - 1; t >= 0; --t) M[m] = O::mma(k, f[t], M[m]);
+      }
+    }
+    if constexpr (OUT) {
+      const int64_t o0 = (b * a.T * a.H + head) * DV + col;
+#pragma unroll
+      for (int I = 0; I < IT; ++I)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t t = token(p, 32 * I + acc_row(e, h));
+          if (t >= a.T) continue;
+          const float x = t < Tb ? acc[I][e] : 0.f;
+          const int64_t at = o0 + t * a.H * DV;
+          if (a.out_f32) static_cast<float*>(a.out)[at] = x;
+          else static_cast<T*>(a.out)[at] = (T)x;
+        }
+      if constexpr (EXTRA) {
+        if (tid < P) {
+          const int64_t t = token(p, tid);
+          if (t < a.T) {
+            float x = 0.f;
+            for (int q = 0; q < NW; ++q) x += sh.dot[q][tid];
+            a.dot[row * a.T + t] = t < Tb ? x : 0.f;
+            if constexpr (EXTRA > 1) {
+              const int i5 = tid & 31;
+              float y;
+              if (IT == 1) y = sh.erow[0][i5] - sh.ecol[0][i5];
+              else if (tid < 32) y = sh.erow[0][i5] - sh.ecol[0][i5] - sh.ecol[1][i5];
+              else y = sh.erow[1][i5] + sh.erow[2][i5] - sh.ecol[2][i5];
+              a.esum[row * a.T + t] = t < Tb ? y : 0.f;
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if constexpr (OUT) {  // tokens behind the row's length
+    const int64_t t0 = (last > first ? last : first) * P, t1 = end * P < a.T ? end * P : a.T;
+    for (int64_t t = t0; t < t1; ++t) {
+      const int64_t at = ((b * a.T + t) * a.H + head) * DV + tid;
+      if (tid < DV) {
+        if (a.out_f32) static_cast<float*>(a.out)[at] = 0.f;
+        else static_cast<T*>(a.out)[at] = (T)0.f;
+      }
+      if constexpr (EXTRA) {
+        if (tid == 0) {
+          a.dot[row * a.T + t] = 0.f;
+          if constexpr (EXTRA > 1) a.esum[row * a.T + t] = 0.f;
+        }
+      }
+    }
+  }
+  float* to = nullptr;
+  float last_decay = 1.f;
+  if (a.loc) {
+    to = a.loc + row * a.loc_row + (int64_t)seg * DK * DV;
+  } else if (a.fin && seg == (REV ? 0 : a.nseg - 1)) {
+    to = a.fin + row * a.fin_row;
+    if (REV && Tb > 0) last_decay = decay_of(gp[0]);
+  }
+  if (to) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) to[(32 * m + acc_row(e, h)) * DV + col] = M[m][e] * last_decay;
+  }
+  if (a.decay && tid == NT - 64) a.decay[row * a.nseg + seg] = decay;
+}
+
+// The states in front of every segment from the segments' states from zero, in place.
+__global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
+  const int n = a.dk * a.dv;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = id / n;
+  if (row >= a.rows) return;
+  const int i = (int)(id % n);
+  float cur = 0.f;
+  if (a.init) cur = a.init[row * n + (a.init_t ? (i % a.dv) * a.dk + i / a.dv : i)];
+  for (int s = 0; s < a.nseg; ++s) {
+    const int at = a.reverse ? a.nseg - 1 - s : s;
+    float* p = a.state + row * a.state_row + (int64_t)at * n + i;
+    if (s + 1 == a.nseg && !a.fin) {  // nothing starts behind the last one
+      *p = cur;
+      break;
+    }
+    const float own = *p;
+    *p = cur;
+    cur = cur * exp2_((float)a.decay[row * a.nseg + at]) + own;
+  }
+  if (a.fin) a.fin[row * a.fin_row + i] = cur;
+}
+
+// dL/dg_t = exp(g_t) <G_t, M_{t-1}>.  In a piece with M_0 in front, dM the gradient of its last state
+// and gamma the decay of all its tokens, that is
+//     gamma <dM, M_0> + sum_{j<t} b_j + sum_{i>=t} c_i + sum_{i>=t>j} E_ij
+// (b_j = k_j . the part of dk_j that comes from behind the piece, c_i = q_i . the part of dq_i from in
+// front of it, E_ij the score pairs): the double sum is that of (row - column) sums from t on.  The
+// first term is X = <dM, M_P> - sum b, with <dM, M_P> a product of whole states at the segment's end
+// and X + sum c at every other piece's.  Where gamma < 2^-24, X is zero to float32 and is taken as that,
+// so that the difference's rounding does not stand in for it.  One wave runs one segment.
+template <int P>
+__global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t row = blockIdx.x / a.nseg;
+  const int seg = blockIdx.x % a.nseg;
+  const int64_t b = row / a.H;
+  const int head = (int)(row % a.H);
+  int64_t Tb = a.T;
+  if (a.lens) {
+    Tb = a.lens[b];
+    Tb = Tb < 0 ? 0 : (Tb > a.T ? a.T : Tb);
+  }
+  auto g_at = [&](int64_t t) -> float {
+    const float g = a.per_head ? a.g[head] : a.g[(b * a.ld_g + t) * a.H + head];
+    return g < kLgFloor ? kLgFloor : g;
+  };
+  auto out = [&](int64_t t) -> float* { return a.dg + (a.per_head ? row * a.T + t : (b * a.T + t) * a.H + head); };
+  const int64_t all = (a.T + P - 1) / P, live = (Tb + P - 1) / P, first = (int64_t)seg * a.seg_pieces;
+  const int64_t end = first + a.seg_pieces < all ? first + a.seg_pieces : all, last = end < live ? end : live;
+  __shared__ double part[4];
+  // <dM, M> behind the segment
+  double x = 0.0;
+  if (first < last) {
+    const float* m = a.fwd + (row * (a.nseg + 1) + seg + 1) * (int64_t)a.n;
+    const bool behind = seg + 1 < a.nseg;
+    const float* r = behind ? a.rev + (row * a.nseg + seg) * (int64_t)a.n : a.dS ? a.dS + row * a.n : nullptr;
+    if (r) {
+      const int w = a.w, tall = a.n / w;
+      for (int i = tid; i < a.n; i += 256) x += (double)m[i] * r[behind ? i : (i % w) * tall + i / w];
+    }
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
+  if (lane == 0) part[tid >> 6] = x;
+  __syncthreads();
+  if (tid >= 64) return;
+  double phi = part[0] + part[1] + part[2] + part[3];
+  if (last > first && last * P < Tb) phi *= decay_of(g_at(last * P));
+  for (int64_t t = (last > first ? last : first) * P + lane; t < end * P && t < a.T; t += 64) *out(t) = 0.f;
+  for (int64_t p = last - 1; p >= first; --p) {
+    const int64_t t = p * P + lane;
+    const bool on = lane < P && t < Tb;
+    const float bb = on ? a.b[row * a.T + t] : 0.f, cc = on ? a.c[row * a.T + t] : 0.f;
+    const float ee = on ? a.e[row * a.T + t] : 0.f, g = on ? g_at(t) : 0.f;
+    double before = bb, behind = (double)cc + ee, lg = g, sc = cc;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double y = __shfl_up(before, o, 64), z = __shfl_down(behind, o, 64);
+      if (lane >= o) before += y;
+      if (lane + o < 64) behind += z;
+      lg += __shfl_xor(lg, o, 64);
+      sc += __shfl_xor(sc, o, 64);
+    }
+    const double sb = __shfl(before, 63, 64);
+    const double X = lg * kLog2e > -24.0 ? phi - sb : 0.0;
+    if (lane < P && t < a.T) *out(t) = on && g > -104.f ? (float)(X + (before - bb) + behind) : 0.f;
+    phi = X + sc;
+  }
+}
+
+// The gradient of one decay for each head: the sum over its rows' tokens, in a fixed order.
+__global__ __launch_bounds__(1024) void la_head_sum_kernel(const float* x, float* y, int64_t B, int64_t H, int64_t T) {
+  double s = 0.0;
+  for (int64_t b = 0; b < B; ++b)
+    for (int64_t t = threadIdx.x; t < T; t += 1024) s += x[(b * H + blockIdx.x) * T + t];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+  __shared__ double part[16];
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) s += part[i];
+    y[blockIdx.x] = (float)s;
+  }
+}
+
+// Gradients of shared heads: the sum over each group of the heads' float32 gradients.
+template <class T>
+__global__ __launch_bounds__(256) void la_group_sum_kernel(LaGroup a) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t per = (int64_t)a.heads * a.width / 4;
+  if (id >= a.tokens * per) return;
+  const int64_t t = id / per;
+  const int e = (int)(id % per) * 4, head = e / a.width, i = e % a.width;
+  const float* p = a.x + (t * a.heads * a.group + (int64_t)head * a.group) * a.width + i;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int g = 0; g < a.group; ++g) {
+    const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)g * a.width);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  T* y = static_cast<T*>(a.y) + t * a.heads * a.width + e;
+  y[0] = (T)s.x; y[1] = (T)s.y; y[2] = (T)s.z; y[3] = (T)s.w;
+}
+
+// One token of every row: the state is read, updated and written in one pass.
+template <class T, int DK, int DV>
+__global__ __launch_bounds__(256) void la_step_kernel(LaStep a) {
+  constexpr int CPR = DV / 4, RPP = 256 / CPR, NP = DK / RPP;
+  const int tid = threadIdx.x, col = (tid % CPR) * 4, r0 = tid / CPR;
+  const int64_t row = blockIdx.x;
+  const int head = (int)(row % a.H);
+  const int64_t krow = row / a.H * (a.H / a.group) + head / a.group;
+  const T* q = static_cast<const T*>(a.q) + krow * DK;
+  const T* k = static_cast<const T*>(a.k) + krow * DK;
+  const T* v = static_cast<const T*>(a.v) + row * DV + col;
+  float* S = a.S + row * DK * DV + col;
+  const float decay = decay_of(a.per_head ? a.g[head] : a.g[row]);
+  const float4 vv = make_float4((float)v[0], (float)v[1], (float)v[2], (float)v[3]);
+  float4 m[NP], o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) m[p] = *reinterpret_cast<const float4*>(S + (p * RPP + r0) * DV);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int r = p * RPP + r0;
+    const float kr = (float)k[r], qr = (float)q[r];
+    m[p].x = decay * m[p].x + kr * vv.x; m[p].y = decay * m[p].y + kr * vv.y;
+    m[p].z = decay * m[p].z + kr * vv.z; m[p].w = decay * m[p].w + kr * vv.w;
+    o.x += qr * m[p].x; o.y += qr * m[p].y; o.z += qr * m[p].z; o.w += qr * m[p].w;
+    *reinterpret_cast<float4*>(S + r * DV) = m[p];
+  }
+  __shared__ float4 red[RPP][CPR];
+  red[r0][tid % CPR] = o;
+  __syncthreads();
+  if (tid < DV) {
+    float s = 0.f;
+    for (int r = 0; r < RPP; ++r) s += reinterpret_cast<const float*>(red[r])[tid];
+    static_cast<T*>(a.o)[row * DV + tid] = (T)s;
+  }
+}
+
+template <class T, int DK, int DV, bool OUT, bool REV, int EXTRA>
+hipError_t sweep(const LaSweep& a, hipStream_t s) {
+  static_assert(2 * sizeof(LaShared<T, DK, DV, OUT, EXTRA>) <= 160 * 1024, "two workgroups share a compute unit's LDS");
+  hipLaunchKernelGGL((la_sweep_kernel<T, DK, DV, OUT, REV, EXTRA>), dim3((unsigned)(a.B * a.H * a.nseg)), dim3(DV * 2), 0, s, a);
+  return hipGetLastError();
+}
+
+template <class T, int DK, int DV>
+hipError_t sweep_d(const LaSweep& a, bool state_only, bool reverse, hipStream_t s) {
+  if (state_only) return reverse ? sweep<T, DK, DV, false, true, 0>(a, s) : sweep<T, DK, DV, false, false, 0>(a, s);
+  if (a.dot) return reverse ? sweep<T, DK, DV, true, true, 1>(a, s) : sweep<T, DK, DV, true, false, 2>(a, s);
+  return reverse ? sweep<T, DK, DV, true, true, 0>(a, s) : sweep<T, DK, DV, true, false, 0>(a, s);
+}
+
+template <class T>
+hipError_t sweep_t(const LaSweep& a, int dk, int dv, bool state_only, bool reverse, hipStream_t s) {
+  if (dk == 64) return dv == 64 ? sweep_d<T, 64, 64>(a, state_only, reverse, s) : sweep_d<T, 64, 128>(a, state_only, reverse, s);
+  return dv == 64 ? sweep_d<T, 128, 64>(a, state_only, reverse, s) : sweep_d<T, 128, 128>(a, state_only, reverse, s);
+}
+
+template <class T>
+hipError_t step_t(const LaStep& a, int dk, int dv, hipStream_t s) {
+  const dim3 grid((unsigned)(a.Bs * a.H)), block(256);
+  if (dk == 64 && dv == 64) hipLaunchKernelGGL((la_step_kernel<T, 64, 64>), grid, block, 0, s, a);
+  else if (dk == 64) hipLaunchKernelGGL((la_step_kernel<T, 64, 128>), grid, block, 0, s, a);
+  else if (dv == 64) hipLaunchKernelGGL((la_step_kernel<T, 128, 64>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((la_step_kernel<T, 128, 128>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+unsigned blocks(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
+
+}  // namespace
+
+int la_piece(int dtype) { return dtype == HLA_BF16 ? La<bf16>::P : La<float>::P; }
+
+hipError_t launch_la_sweep(const LaSweep& a, int dtype, int dk, int dv, bool state_only, bool reverse, hipStream_t s) {
+  return dtype == HLA_BF16 ? sweep_t<bf16>(a, dk, dv, state_only, reverse, s) : sweep_t<float>(a, dk, dv, state_only, reverse, s);
+}
+
+hipError_t launch_la_scan(const LaScan& a, hipStream_t s) {
+  hipLaunchKernelGGL(la_scan_kernel, dim3(blocks(a.rows * a.dk * a.dv, 256)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_la_decay(const LaDecay& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.B * a.H * a.nseg));
+  if (a.piece == 64) hipLaunchKernelGGL(la_decay_kernel<64>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(la_decay_kernel<32>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_la_head_sum(const float* x, float* y, int64_t B, int64_t H, int64_t T, hipStream_t s) {
+  hipLaunchKernelGGL(la_head_sum_kernel, dim3((unsigned)H), dim3(1024), 0, s, x, y, B, H, T);
+  return hipGetLastError();
+}
+
+hipError_t launch_la_group_sum(const LaGroup& a, int dtype, hipStream_t s) {
+  const dim3 grid(blocks(a.tokens * a.heads * a.width / 4, 256));
+  if (dtype == HLA_BF16) hipLaunchKernelGGL(la_group_sum_kernel<bf16>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(la_group_sum_kernel<float>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_la_step(const LaStep& a, int dtype, int dk, int dv, hipStream_t s) {
+  return dtype == HLA_BF16 ? step_t<bf16>(a, dk, dv, s) : step_t<float>(a, dk, dv, s);
+}
+
+}  // namespace hla

@@ -49,7 +49,13 @@ class _Cache8Struct(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("maps", "reps", "scale", "order", "count", "weight")])
 
 
+class _LaDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "T", "H", "Hk", "ld_T")]
+                + [(n, ctypes.c_int32) for n in ("dk", "dv", "dtype", "decay_per_head")])
+
+
 _P = ctypes.c_void_p
+_LA = ctypes.POINTER(_LaDims)
 _C8 = ctypes.POINTER(_Cache8Struct)
 _SIGS = {
     "hla_abi_version": (ctypes.c_int32, []),
@@ -97,6 +103,12 @@ _SIGS = {
                                           _P]),
     "hla_evict_chunks": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, ctypes.c_int32,
                                           ctypes.c_int32, _P, _P, _P, _P]),
+    "hla_la_prefill": (ctypes.c_int32, [_LA, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "hla_la_prefill_backward": (ctypes.c_int32, [_LA, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                 ctypes.c_size_t, _P]),
+    "hla_la_workspace_bytes": (ctypes.c_int32, [ctypes.c_int32, _LA, ctypes.POINTER(ctypes.c_size_t)]),
+    "hla_la_decode": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.c_int32, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P]),
     "hla_timing_enable": (ctypes.c_int32, [ctypes.c_int32]),
     "hla_timing_read": (ctypes.c_int32, [ctypes.c_int32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]),
     "hla_gdn_decode": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
@@ -944,6 +956,105 @@ def prefill_to_cache8(cache, r, T, C=CHUNK, tau=None, budget=None, n_recent=1, g
                      for t in (Bc, At))
     S = torch.zeros((B, H, dk, dv), dtype=torch.float32, device=At.device)
     return S, torch.eye(dk, dtype=torch.float32, device=At.device).repeat(B, H, 1, 1)
+
+
+# -------------------------------------------- linear attention with a decay for each head
+LA_PREFILL, LA_PREFILL_BACKWARD = 0, 1
+
+
+def _la_inputs(q, k, v, log_decay, lens):
+    B, T, H, dv, ld_T = _token_view(v, "v")
+    Bk, Tk, Hk, dk, ldk = _token_view(k, "k")
+    dev = v.device
+    if (Bk, Tk, ldk) != (B, T, ld_T) or k.dtype != v.dtype or k.device != dev:
+        raise ValueError("k must match v's batch, tokens, row length, dtype and device")
+    if q is not None and (_token_view(q, "q") != (B, T, Hk, dk, ld_T) or q.dtype != v.dtype or q.device != dev):
+        raise ValueError("q must match k")
+    if log_decay.device != dev:
+        raise ValueError(f"log_decay must be on {dev}")
+    if log_decay.dim() == 1:
+        _need_on(log_decay, (H,), torch.float32, dev, "log_decay")
+    else:
+        _scalar_view(log_decay, B, T, H, ld_T, "log_decay")
+    _need_on(lens, (B,), torch.int32, dev, "lens")
+    return _LaDims(B, T, H, Hk, ld_T, dk, dv, _dtype_code(v), 1 if log_decay.dim() == 1 else 0), dev
+
+
+def _la_workspace(fn, d, ws, dev):
+    n = ctypes.c_size_t(0)
+    _check(library().hla_la_workspace_bytes(fn, ctypes.byref(d), ctypes.byref(n)), "hla_la_workspace_bytes")
+    if ws is None:
+        return _workspace(n.value, dev)
+    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    return ws
+
+
+def la_workspace_bytes(fn, q, k, v, log_decay) -> int:
+    """Bytes of la_prefill's (LA_PREFILL) or la_prefill_backward's (LA_PREFILL_BACKWARD) workspace."""
+    d, _ = _la_inputs(q, k, v, log_decay, None)
+    n = ctypes.c_size_t(0)
+    _check(library().hla_la_workspace_bytes(fn, ctypes.byref(d), ctypes.byref(n)), "hla_la_workspace_bytes")
+    return n.value
+
+
+def la_prefill(q, k, v, log_decay, S0=None, lens=None, want_o=True, want_state=True, o=None, S_final=None, ws=None):
+    """Linear attention with a decay for each head, M_t = exp(g_t) M_{t-1} + k_t v_t^T, o_t = M_t^T q_t.
+    q, k [B, T, Hk, dk], v [B, T, H, dv] (Hk divides H); log_decay float32 [B, T, H], or [H]; lens
+    int32 [B] or None.  Returns (o [B, T, H, dv] in v's dtype or None, S_final [B, H, dk, dv] float32
+    or None)."""
+    d, dev = _la_inputs(q if want_o else None, k, v, log_decay, lens)
+    if want_o and o is None:
+        o = torch.empty((d.B, d.T, d.H, d.dv), dtype=v.dtype, device=dev)
+    if want_state and S_final is None:
+        S_final = torch.empty((d.B, d.H, d.dk, d.dv), dtype=torch.float32, device=dev)
+    o, S_final = o if want_o else None, S_final if want_state else None
+    _need_on(S0, (d.B, d.H, d.dk, d.dv), torch.float32, dev, "S0")
+    _need_on(o, (d.B, d.T, d.H, d.dv), v.dtype, dev, "o")
+    _need_on(S_final, (d.B, d.H, d.dk, d.dv), torch.float32, dev, "S_final")
+    ws = _la_workspace(LA_PREFILL, d, ws, dev)
+    _call("hla_la_prefill", dev, ctypes.byref(d), _addr(q) if want_o else None, _addr(k), _addr(v), _addr(log_decay),
+          _addr(lens), _addr(S0), _addr(o), _addr(S_final), _addr(ws), 0 if ws is None else ws.numel())
+    return o, S_final
+
+
+def la_prefill_backward(q, k, v, log_decay, dO, dS_final=None, S0=None, lens=None, want_dS0=True, ws=None):
+    """Gradients of la_prefill for dO [B, T, H, dv] (v's dtype) and dS_final [B, H, dk, dv] float32 (None:
+    zero).  Returns dict(dq, dk, dv in v's dtype, dlog_decay float32 of log_decay's shape, dS0 float32 or
+    None)."""
+    d, dev = _la_inputs(q, k, v, log_decay, lens)
+    _need_on(dO, (d.B, d.T, d.H, d.dv), v.dtype, dev, "dO")
+    for t, name in ((dS_final, "dS_final"), (S0, "S0")):
+        _need_on(t, (d.B, d.H, d.dk, d.dv), torch.float32, dev, name)
+    out = dict(dq=torch.empty((d.B, d.T, d.Hk, d.dk), dtype=v.dtype, device=dev),
+               dk=torch.empty((d.B, d.T, d.Hk, d.dk), dtype=v.dtype, device=dev),
+               dv=torch.empty((d.B, d.T, d.H, d.dv), dtype=v.dtype, device=dev),
+               dlog_decay=torch.empty(tuple(log_decay.shape), dtype=torch.float32, device=dev),
+               dS0=torch.empty((d.B, d.H, d.dk, d.dv), dtype=torch.float32, device=dev) if want_dS0 else None)
+    ws = _la_workspace(LA_PREFILL_BACKWARD, d, ws, dev)
+    _call("hla_la_prefill_backward", dev, ctypes.byref(d), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(lens),
+          _addr(S0), _addr(dO), _addr(dS_final), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]),
+          _addr(out["dlog_decay"]), _addr(out["dS0"]), _addr(ws), ws.numel())
+    return out
+
+
+def la_decode(q, k, v, log_decay, S, o=None):
+    """One token of linear attention with a decay for each head: S [Bs, H, dk, dv] float32 is updated in
+    place.  q, k [Bs, Hk, dk], v [Bs, H, dv]; log_decay float32 [Bs, H] or [H].  Returns o [Bs, H, dv]."""
+    if v.dim() != 3 or k.dim() != 3:
+        raise ValueError("k and v must be [Bs, heads, width]")
+    (Bs, H, dv), (_, Hk, dk), dev = v.shape, k.shape, v.device
+    _need_on(v, (Bs, H, dv), v.dtype, dev, "v")
+    for t, name in ((q, "q"), (k, "k")):
+        _need_on(t, (Bs, Hk, dk), v.dtype, dev, name)
+    _need_on(log_decay, (H,) if log_decay.dim() == 1 else (Bs, H), torch.float32, dev, "log_decay")
+    _need_on(S, (Bs, H, dk, dv), torch.float32, dev, "S")
+    if o is None:
+        o = torch.empty((Bs, H, dv), dtype=v.dtype, device=dev)
+    _need_on(o, (Bs, H, dv), v.dtype, dev, "o")
+    _call("hla_la_decode", dev, Bs, H, Hk, dk, dv, _dtype_code(v), _addr(q), _addr(k), _addr(v), _addr(log_decay),
+          1 if log_decay.dim() == 1 else 0, _addr(S), _addr(o))
+    return o
 
 
 def timing_enable(on: bool = True) -> None:

@@ -662,6 +662,72 @@ hla_status_t hla_chunk_reps_backward(const hla_dims_t* d, const void* k, int32_t
                                      float* dWk, float* dWv, float* dWp, float* dWr, void* ws,
                                      size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Linear attention with a decay for each head: the additive recurrence without the delta rule's
+ * erase, which hybrid models mix with it.  Per (batch row, head), M [dk, dv] in float32:
+ *     M_t = exp(g_t) M_{t-1} + k_t v_t^T,     o_t = M_t^T q_t        (S = M^T in math orientation)
+ *   q, k      [B, ld_T, Hk, dk], v [B, ld_T, H, dv] (dtype); Hk divides H, and value heads
+ *             h = i H/Hk .. (i + 1) H/Hk - 1 share query and key head i.  q is not scaled.
+ *   log_decay g <= 0, float32: [B, ld_T, H] (decay_per_head = 0) or [H] (1).  Below -1e4, -inf
+ *             included, it clears the state.
+ *   lens      [B] int32 or NULL (T): tokens of each row, clamped to 0 .. T.  Tokens behind a row's
+ *             length are not read; outputs and gradients there are zero.
+ * dtype is that of q, k, v, o and of their gradients; states, log_decay and their gradients are
+ * float32.  Arithmetic: float32 sums, sums of log_decay in float64.  Over bf16 tensors what is float32
+ * enters the matrix cores as bf16 terms: three (24 bits) where the result is float32, two for the
+ * states and one (2^-8) for the decayed scores where it is rounded to bf16.  A number that is not
+ * finite spreads over its own 64-token piece, to earlier tokens of the piece too.  Sums have a fixed
+ * order: a call repeats its bits.
+ */
+typedef struct {
+  int64_t B, T, H, Hk, ld_T;
+  int32_t dk, dv, dtype, decay_per_head;
+} hla_la_dims_t;
+typedef enum { HLA_LA_PREFILL = 0, HLA_LA_PREFILL_BACKWARD = 1 } hla_la_fn_t;
+
+/*
+ * hla_la_prefill -- the chunked form over a prompt.
+ *   S0       [B, H, dk, dv] float32 or NULL (zero).
+ *   o        [B, T, H, dv] (dtype, out) or NULL;  S_final [B, H, dk, dv] float32 (out) or NULL: the
+ *            state behind every row's last token.  At least one; q may be NULL without o.
+ *   ws       hla_la_workspace_bytes(HLA_LA_PREFILL) bytes: the states in front of the segments that
+ *            long rows are cut into where there are few rows (0 otherwise).
+ * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE, HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN (log_decay and lens
+ *         4 bytes, the others 16), HLA_ERR_WORKSPACE, HLA_ERR_HIP.
+ */
+hla_status_t hla_la_prefill(const hla_la_dims_t* d, const void* q, const void* k, const void* v,
+                            const float* log_decay, const int32_t* lens, const float* S0, void* o,
+                            float* S_final, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * hla_la_prefill_backward -- gradients of hla_la_prefill, for dO = dL/do and dS_final = dL/dS_final.
+ * With G_t = exp(g_{t+1}) G_{t+1} + q_t dO_t^T (dS_final behind the last token):
+ *     dq_t = M_t dO_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  dg_t = exp(g_t) <G_t, M_{t-1}>,
+ *     dS0 = exp(g_1) G_1; shared heads' dq and dk and a head's one dg are sums.
+ * dg is the gradient of log_decay; it is 0 where a decay clears the state.
+ *   dO [B, T, H, dv] (dtype);  dS_final [B, H, dk, dv] float32 or NULL (zero).
+ *   dq, dk [B, T, Hk, dk], dv [B, T, H, dv] (dtype, out);  dlog_decay [B, T, H] or [H] float32 (out);
+ *   dS0 [B, H, dk, dv] float32 (out) or NULL.
+ *   ws hla_la_workspace_bytes(HLA_LA_PREFILL_BACKWARD) bytes.
+ * Errors: as hla_la_prefill.
+ */
+hla_status_t hla_la_prefill_backward(const hla_la_dims_t* d, const void* q, const void* k, const void* v,
+                                     const float* log_decay, const int32_t* lens, const float* S0,
+                                     const void* dO, const float* dS_final, void* dq, void* dk, void* dv,
+                                     float* dlog_decay, float* dS0, void* ws, size_t ws_bytes,
+                                     hipStream_t stream);
+hla_status_t hla_la_workspace_bytes(int32_t fn, const hla_la_dims_t* d, size_t* out);
+
+/*
+ * hla_la_decode -- one token of Bs sequences: S [Bs, H, dk, dv] float32 is updated in place and read.
+ *   q, k [Bs, Hk, dk], v [Bs, H, dv] (dtype, 4-byte aligned);  log_decay [Bs, H] or [H] float32;
+ *   o [Bs, H, dv] (dtype, out, 4-byte aligned).  S is 16-byte aligned.
+ * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE, HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN, HLA_ERR_HIP.
+ */
+hla_status_t hla_la_decode(int64_t Bs, int64_t H, int64_t Hk, int32_t dk, int32_t dv, int32_t dtype,
+                           const void* q, const void* k, const void* v, const float* log_decay,
+                           int32_t decay_per_head, float* S, void* o, hipStream_t stream);
+
 /* Workspace bytes that entry point `fn` needs for dims `d`; n_rep is the number of
  * representatives per chunk for HLA_FN_CHUNK_REPS (C / window; it must divide C), whether
  * Wr is given (0 or 1) for HLA_FN_CHUNK_REPS_BACKWARD, and ignored otherwise.  `out` is a
