@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libhla.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["chunk.hip", "scan.hip", "prefill.hip", "route.hip", "compose.hip", "decode.hip", "reps.hip", "reps_bwd.hip", "gdn2.hip", "compose_bwd.hip", "chunk_bwd.hip", "gdn2_bwd.hip", "router_bwd.hip", "cache8.hip", "cache8_fill.hip", "la.hip", "abi.cpp", "abi_cache8.cpp", "abi_la.cpp", "timing.cpp"]
+SOURCES = ["chunk.hip", "scan.hip", "prefill.hip", "route.hip", "compose.hip", "decode.hip", "reps.hip", "reps_bwd.hip", "gdn2.hip", "compose_bwd.hip", "chunk_bwd.hip", "gdn2_bwd.hip", "router_bwd.hip", "cache8.hip", "cache8_fill.hip", "la.hip", "tree.hip", "abi.cpp", "abi_cache8.cpp", "abi_la.cpp", "abi_tree.cpp", "timing.cpp"]
 
 # Packed fp32 VALU ops are disabled for the device: the kernels are written with scalar
 # fp32 arithmetic and must not be turned into v_pk_* instructions.
@@ -34,8 +34,10 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", os.path.
 # Its state pass also scales and converts the MFMA accumulators (the state, E and O^T) with
 # vector instructions every piece: with the accumulators in ordinary VGPRs (they fit, 239
 # registers at one wave per SIMD) those need no accumulator-register moves (about 256 per
-# piece otherwise).
-SOURCE_FLAGS = {"prefill.hip": ["-mllvm", "-disable-promote-alloca-to-lds", "-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# piece otherwise).  la.hip and tree.hip prefetch the same way.
+SOURCE_FLAGS = {"la.hip": ["-mllvm", "-disable-promote-alloca-to-lds"],
+                "tree.hip": ["-mllvm", "-disable-promote-alloca-to-lds"],
+                "prefill.hip": ["-mllvm", "-disable-promote-alloca-to-lds", "-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def _compile(src: str) -> str:
@@ -66,7 +68,7 @@ def build_library(verbose: bool = False) -> str:
 
 # Host code only (the C ABI's argument checks, workspace sizing and launch set-up) under
 # AddressSanitizer and UndefinedBehaviorSanitizer; every flag is scoped to the host pass.
-HOST_SOURCES = ("abi.cpp", "abi_cache8.cpp", "abi_la.cpp", "timing.cpp")
+HOST_SOURCES = ("abi.cpp", "abi_cache8.cpp", "abi_la.cpp", "abi_tree.cpp", "timing.cpp")
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer"]
 

@@ -8,7 +8,7 @@
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 24;    // rows times segments: a launch counts its threads in 32 bits
+constexpr int64_t kMaxRows = ((int64_t)1 << 24) - 1;    // rows times segments: a launch counts its threads in 32 bits
 constexpr int64_t kMaxTokens = (int64_t)1 << 36;
 
 template <int A, class... P>

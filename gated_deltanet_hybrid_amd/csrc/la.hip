@@ -19,6 +19,7 @@
 // as float32: the decayed values, which enter the states, and the state where the decays' gradient is
 // formed from it.  Two (2^-16 at most) for the state that outputs read, and one (2^-8) for the decayed
 // scores: these reach bf16 outputs only, which round to 2^-8 themselves.
+#include "operands.hpp"
 #include "la.hpp"
 #include "kernels.hpp"
 #include "timing.hpp"
@@ -26,9 +27,6 @@
 namespace hla {
 
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kLgFloor = -1.0e4f;  // stands for -inf: 2^-14427 is zero in every type used here
@@ -38,93 +36,6 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 __device__ __forceinline__ float decay_of(float g) {
   return exp2_((float)((double)(g < kLgFloor ? kLgFloor : g) * kLog2e));
 }
-
-// The operands of a product over K: `Frag` is what a lane holds of KG consecutive k.
-// bf16: one 32x32x16 instruction, 8 values a lane.  float32: four 32x32x2, slot e of the group is
-// k = 4 h + e, which is also the order in which an accumulator holds its rows.
-template <class T> struct La;
-
-template <> struct La<bf16> {
-  static constexpr int P = 64, KG = 16, TERMS = 3;
-  using Frag = bf16x8;
-  // An LDS tile of W columns: rows of 16-byte chunks, permuted by the row so that the row reads (16
-  // rows, one chunk) and the transposing reads (4 rows, 4 chunks) both meet every bank once.
-  template <int W> __device__ __forceinline__ static int at(int row, int col) {
-    const int s = W == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-    return row * W + (((col >> 3) ^ s) << 3) + (col & 7);
-  }
-  template <int W> static constexpr int size() { return P * W; }
-  static constexpr int PS = P + 8;  // row stride of the decayed scores
-  __device__ __forceinline__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-  }
-  // k = 16 g + 8 h + e of one row
-  __device__ __forceinline__ static Frag plain(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
-  template <int W> __device__ __forceinline__ static Frag row(const bf16* t, int r, int g, int h) {
-    return plain(t + at<W>(r, g * 16 + h * 8));
-  }
-  // k = 16 g + 8 (e / 4) + 4 h + e % 4: the accumulators' order
-  template <int W> __device__ __forceinline__ static Frag rowc(const bf16* t, int r, int g, int h) {
-    const bf16x4 lo = *reinterpret_cast<const bf16x4*>(t + at<W>(r, g * 16 + h * 4));
-    const bf16x4 hi = *reinterpret_cast<const bf16x4*>(t + at<W>(r, g * 16 + 8 + h * 4));
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-  // column n0 + lane % 32, rows k = 16 g + 8 h + e: the transposing LDS read hands lane i of 16 the
-  // i-th column of the four rows that its 16 lanes address (4 lanes a row, 4 columns each)
-  template <int W> __device__ __forceinline__ static Frag col(const bf16* t, int n0, int g, int lane) {
-    const int k = g * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3), c = n0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + at<W>(k, c)));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + at<W>(k + 4, c)));
-    return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  }
-  __device__ __forceinline__ static int col_k(int g, int h) { return g * 16 + h * 8; }  // first of 8 k
-  // the first N bf16 terms of 8 float32 values
-  template <int N> __device__ __forceinline__ static void split(const float (&x)[8], Frag (&f)[N]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float r = x[e];
-#pragma unroll
-      for (int t = 0; t < N; ++t) {
-        f[t][e] = (bf16)r;
-        r -= (float)f[t][e];
-      }
-    }
-  }
-  static constexpr int FN = 8;
-};
-
-template <> struct La<float> {
-  static constexpr int P = 32, KG = 8, TERMS = 1;
-  using Frag = f32x4;
-  template <int W> __device__ __forceinline__ static int at(int row, int col) { return row * (W + 8) + col; }
-  template <int W> static constexpr int size() { return P * (W + 8); }
-  static constexpr int PS = P + 8;
-  __device__ __forceinline__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
-    return c;
-  }
-  __device__ __forceinline__ static Frag plain(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-  template <int W> __device__ __forceinline__ static Frag row(const float* t, int r, int g, int h) {
-    return plain(t + at<W>(r, g * 8 + h * 4));
-  }
-  template <int W> __device__ __forceinline__ static Frag rowc(const float* t, int r, int g, int h) {
-    return row<W>(t, r, g, h);
-  }
-  template <int W> __device__ __forceinline__ static Frag col(const float* t, int n0, int g, int lane) {
-    Frag f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = t[at<W>(g * 8 + (lane >> 5) * 4 + e, n0 + (lane & 31))];
-    return f;
-  }
-  __device__ __forceinline__ static int col_k(int g, int h) { return g * 8 + h * 4; }
-  template <int N> __device__ __forceinline__ static void split(const float (&x)[4], Frag (&f)[N]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[0][e] = x[e];
-  }
-  static constexpr int FN = 4;
-};
 
 // The sums lg of one piece and what follows from them, in LDS.
 template <int P> struct Decays {
@@ -208,14 +119,14 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
     const int64_t t = token(p, lane) + (REV ? 1 : 0);
     return t < Tb ? (a.per_head ? gp[0] : gp[t * a.H]) : 0.f;
   };
-  uint4 r1[OUT ? N1 : 1], r2[N1], r3[N3], r4[EXTRA ? N3 : 1];
-  auto load_tile = [&](const T* base, int64_t stride, int width, int64_t p, uint4* regs, int count) {
+  u32x4 r1[OUT ? N1 : 1], r2[N1], r3[N3], r4[EXTRA ? N3 : 1];
+  auto load_tile = [&](const T* base, int64_t stride, int width, int64_t p, u32x4* regs, int count) {
     const int cpr = width / V;
 #pragma unroll
     for (int i = 0; i < count; ++i) {
       const int id = i * NT + tid;
       const int64_t t = token(p, id / cpr);
-      regs[i] = t < Tb ? *reinterpret_cast<const uint4*>(base + t * stride + (id % cpr) * V) : make_uint4(0, 0, 0, 0);
+      regs[i] = t < Tb ? *reinterpret_cast<const u32x4*>(base + t * stride + (id % cpr) * V) : u32x4{0, 0, 0, 0};
     }
   };
   auto load = [&](int64_t p) {
@@ -228,14 +139,14 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
 #pragma unroll
     for (int i = 0; i < N1; ++i) {
       const int id = i * NT + tid, at = O::template at<DK>(id / (DK / V), id % (DK / V) * V);
-      if constexpr (OUT) *reinterpret_cast<uint4*>(sh.x1 + at) = r1[i];
-      *reinterpret_cast<uint4*>(sh.x2 + at) = r2[i];
+      if constexpr (OUT) *reinterpret_cast<u32x4*>(sh.x1 + at) = r1[i];
+      *reinterpret_cast<u32x4*>(sh.x2 + at) = r2[i];
     }
 #pragma unroll
     for (int i = 0; i < N3; ++i) {
       const int id = i * NT + tid, at = O::template at<DV>(id / (DV / V), id % (DV / V) * V);
-      *reinterpret_cast<uint4*>(sh.x3 + at) = r3[i];
-      if constexpr (EXTRA) *reinterpret_cast<uint4*>(sh.x4 + at) = r4[i];
+      *reinterpret_cast<u32x4*>(sh.x3 + at) = r3[i];
+      if constexpr (EXTRA) *reinterpret_cast<u32x4*>(sh.x4 + at) = r4[i];
     }
   };
   auto piece = [&](int64_t i) { return REV ? last - 1 - i : first + i; };

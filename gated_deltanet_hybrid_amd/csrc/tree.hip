@@ -1,0 +1,619 @@
+// Trees of drafted tokens over the decode state of a gated delta rule and its cached chunk maps.
+//
+// Node i with parent p continues p's state (the live state M_0 for p = -1):
+//     M_i = alpha_i (I - beta_i k_i k_i^T) M_p + beta_i k_i v_i^T
+// With D_ij the product of alpha over the path below ancestor j down to i (1 for j = i), gamma_i the one
+// from the live state and L_jl = beta_j D_jl (k_j . k_l) for the strict ancestors l of j, the updates that
+// the nodes make solve (I + L) U = diag(beta) V and (I + L) W = diag(beta gamma) K -- parents come before
+// their children, so L is strictly lower -- and with P_ij = D_ij (q_i . k_j) over i's ancestors and itself
+//     r_i = gamma_i q_i - sum_j P_ij w_j,    o_i = sum_j P_ij u_j + M_0^T r_i,    z_i = At_cur^T r_i.
+// The z_i then meet the cached chunks, newest first, with every node's own gates:
+//     o_i += g_ij Bc_j^T z_i;   z_i <- z_i + g_ij (At_j^T z_i - z_i)
+// so the live matrices and every chunk's maps and representatives are read once for all nodes.
+#include "../../include/hla.h"
+
+#include "tree.hpp"
+#include "kernels.hpp"
+#include "operands.hpp"
+
+namespace hla {
+
+namespace {
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A lane's node: its ancestors and itself as bits (0 where the node is absent: a parent out of range, or
+// an absent ancestor), and the sum of `lg` over them.  Six rounds of pointer doubling by the whole wave.
+struct Path { unsigned long long mask; double lg; };
+__device__ __forceinline__ Path tree_path(const int32_t* parent, int n, int lane, double lg) {
+  int p = lane < n ? parent[lane] : -2;
+  int bad = p < -1 || p >= lane;
+  p = bad ? -1 : p;
+  unsigned long long m = 1ull << lane;
+#pragma unroll
+  for (int r = 0; r < 6; ++r) {
+    const int from = p < 0 ? lane : p;
+    const unsigned long long pm = __shfl(m, from, 64);
+    const double pl = __shfl(lg, from, 64);
+    const int pb = __shfl(bad, from, 64), pp = __shfl(p, from, 64);
+    if (p >= 0) {
+      m |= pm;
+      lg += pl;
+      bad |= pb;
+      p = pp;
+    }
+  }
+  return {bad ? 0ull : m, lg};
+}
+
+template <class T, int DK, int DV, int N> struct LiveShared {
+  using O = La<T>;
+  static constexpr int RD = DK + 4, OD = DV + 4;
+  union {
+    struct {
+      alignas(16) T k[N * O::template rs<DK>()];
+      alignas(16) T q[N * O::template rs<DK>()];
+    } in;
+    struct {
+      alignas(16) float r[N * RD];
+      alignas(16) float o[N * OD];
+    } out;
+  };
+  alignas(16) float L[N][N + 4], P[N][N + 4];
+  double lg[N];
+  unsigned long long mask[N];
+  float gamma[N], beta[N];
+};
+
+// The live part of every node: r, then o = P U + M_0^T r and z = At_cur^T r.  One workgroup a row.
+// The solve runs one thread a column (dk of W, dv of U), its values in registers.
+template <class T, int DK, int DV, int N>
+__global__ __launch_bounds__(256) void tree_live_kernel(TreeArgs a) {
+  using O = La<T>;
+  using S = LiveShared<T, DK, DV, N>;
+  constexpr int V = 16 / (int)sizeof(T), NT = (N + 31) / 32;
+  __shared__ S sh;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, c = lane & 31;
+  const int64_t row = blockIdx.x, b = row / a.H;
+  const int head = (int)(row % a.H), n = a.n;
+  if (w == 0) {
+    double lg = 0.0;
+    float beta = 0.f;
+    if (lane < n) {
+      const int64_t at = (b * n + lane) * a.H + head;
+      const float l = __log2f(a.alpha[at]);
+      lg = l < -1.0e4f ? -1.0e4 : (double)l;  // alpha = 0 clears; NaN stays
+      beta = a.beta[at];
+    }
+    const Path p = tree_path(a.parent + b * n, n, lane, lg);
+    if (lane < N) {
+      sh.lg[lane] = p.lg;
+      sh.mask[lane] = p.mask;
+      sh.gamma[lane] = p.mask ? exp2_((float)p.lg) : 0.f;
+      sh.beta[lane] = p.mask ? beta : 0.f;
+    }
+  }
+  __syncthreads();
+  for (int id = tid; id < N * DK / V; id += 256) {  // absent nodes enter as zeros
+    const int i = id / (DK / V), e = id % (DK / V) * V;
+    uint4 kk = make_uint4(0, 0, 0, 0), qq = kk;
+    if (sh.mask[i]) {
+      const int64_t at = ((b * n + i) * a.H + head) * DK + e;
+      kk = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + at);
+      qq = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + at);
+    }
+    *reinterpret_cast<uint4*>(sh.in.k + O::template at<DK>(i, e)) = kk;
+    *reinterpret_cast<uint4*>(sh.in.q + O::template at<DK>(i, e)) = qq;
+  }
+  __syncthreads();
+  // L and P by 32 x 32 tiles, transposed: rows j, column i
+  for (int job = w; job < 2 * NT * NT; job += 4) {
+    const int which = job & 1, I = (job >> 1) / NT, J = (job >> 1) % NT;
+    if (J > I) continue;
+    const int i = (32 * I + c) % N, jr = (32 * J + c) % N;
+    f32x16 s = zero16();
+    const T* other = which ? sh.in.q : sh.in.k;
+#pragma unroll
+    for (int g = 0; g < DK / O::KG; ++g)
+      s = O::mma(O::template row<DK>(sh.in.k, jr, g, h), O::template row<DK>(other, i, g, h), s);
+    if (32 * I + c < N) {
+      const unsigned long long m = sh.mask[i];
+      const double lgi = sh.lg[i];
+      const float bi = sh.beta[i];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = 32 * J + acc_row(e, h);
+        if (j >= N) continue;
+        float x = 0.f;
+        if ((m >> j) & 1) x = s[e] * exp2_((float)(lgi - sh.lg[j]));
+        if (which) sh.P[i][j] = x;
+        else sh.L[i][j] = j == i ? 0.f : x * bi;
+      }
+    }
+  }
+  __syncthreads();
+  float x[N];
+  if (tid < DK + DV) {
+    const bool is_k = tid < DK;
+    const int col = is_k ? tid : tid - DK;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.f;
+      if (is_k) s = sh.gamma[i] * (float)sh.in.k[O::template at<DK>(i, col)];
+      else if (sh.mask[i]) s = (float)static_cast<const T*>(a.v)[((b * n + i) * a.H + head) * DV + col];
+      x[i] = s * sh.beta[i];
+    }
+#pragma unroll
+    for (int i = 1; i < N; ++i) {
+#pragma unroll
+      for (int j = 0; j < i; j += 4) {
+        const f32x4 l = *reinterpret_cast<const f32x4*>(&sh.L[i][j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < i) x[i] -= l[e] * x[j + e];
+      }
+      sched_fence();
+    }
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j <= i; j += 4) {
+        const f32x4 p = *reinterpret_cast<const f32x4*>(&sh.P[i][j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e <= i) s += p[e] * x[j + e];
+      }
+      x[i] = s;
+      sched_fence();
+    }
+    if (is_k) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = sh.gamma[i] * (float)sh.in.q[O::template at<DK>(i, col)] - x[i];
+    }
+  }
+  __syncthreads();
+  if (tid < DK) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sh.out.r[i * S::RD + tid] = x[i];
+  } else if (tid < DK + DV) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sh.out.o[i * S::OD + tid - DK] = x[i];
+  }
+  __syncthreads();
+  // M^T r, 32 columns of M a tile (float32 matrix cores; M's rows come straight from memory)
+  const int tiles = DV / 32 + (a.At_cur ? DK / 32 : 0);
+  for (int t = w; t < tiles; t += 4) {
+    const bool state = t < DV / 32;
+    const int W = state ? DV : DK, n0 = state ? 32 * t : 32 * t - DV;
+    const float* M = (state ? a.S_cur + row * DK * DV : a.At_cur + row * DK * DK) + n0 + c;
+    f32x16 acc[NT];
+#pragma unroll
+    for (int I = 0; I < NT; ++I) acc[I] = zero16();
+#pragma unroll 8
+    for (int g = 0; g < DK / 8; ++g) {
+      float m[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[e] = M[(g * 8 + h * 4 + e) * W];
+#pragma unroll
+      for (int I = 0; I < NT; ++I) {
+        const f32x4 r = *reinterpret_cast<const f32x4*>(sh.out.r + ((32 * I + c) % N) * S::RD + g * 8 + h * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[I] = __builtin_amdgcn_mfma_f32_32x32x2f32(m[e], r[e], acc[I], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int I = 0; I < NT; ++I) {
+      const int i = 32 * I + c;
+      if (i >= n) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int at = n0 + q * 8 + h * 4;
+        f32x4 y = {acc[I][4 * q], acc[I][4 * q + 1], acc[I][4 * q + 2], acc[I][4 * q + 3]};
+        if (state) {
+          const f32x4 u = *reinterpret_cast<const f32x4*>(sh.out.o + i * S::OD + at);
+          *reinterpret_cast<f32x4*>(a.o + ((b * n + i) * a.H + head) * DV + at) = y + u;
+        } else {
+          *reinterpret_cast<f32x4*>(a.z + (row * n + i) * DK + at) = y;
+        }
+      }
+    }
+  }
+}
+
+// Gates of every node for the held chunks, a wave a chunk: sigmoid of the log-mean-exp of the node's
+// scores over the chunk's representatives (rows of the product; nodes are its columns).
+template <class T, int DK, int NT>
+__global__ __launch_bounds__(256) void tree_gates_kernel(TreeArgs a, int per_block) {
+  using O = La<T>;
+  using Frag = typename O::Frag;
+  constexpr int GN = DK / O::KG;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h = lane >> 5, c = lane & 31;
+  const int64_t row = blockIdx.x, b = row / a.H;
+  const int head = (int)(row % a.H), n = a.n;
+  int nc = a.n_cache[b];
+  nc = nc < 0 ? 0 : (nc > a.n_cap ? a.n_cap : nc);
+  const unsigned long long here = __ballot(tree_path(a.parent + b * n, n, lane, 0.0).mask != 0);
+  Frag q[NT][GN];
+  if (!a.gates_in) {
+#pragma unroll
+    for (int I = 0; I < NT; ++I) {
+      const int i = 32 * I + c < n ? 32 * I + c : n - 1;
+#pragma unroll
+      for (int g = 0; g < GN; ++g)
+        q[I][g] = O::plain(static_cast<const T*>(a.q) + ((b * n + i) * a.H + head) * DK + g * O::KG + h * (O::KG / 2));
+    }
+  }
+  const float scale = 1.f / sqrtf((float)DK);
+  const int end = (blockIdx.y + 1) * per_block < a.n_cap ? (blockIdx.y + 1) * per_block : a.n_cap;
+  for (int j = blockIdx.y * per_block + w; j < end; j += 4) {
+    float m[NT], sum[NT];
+#pragma unroll
+    for (int I = 0; I < NT; ++I) { m[I] = -INFINITY; sum[I] = 0.f; }
+    if (j < nc && !a.gates_in) {
+      const T* reps = static_cast<const T*>(a.reps_cache) + (row * a.n_cap + j) * (int64_t)a.n_rep * DK;
+      for (int r0 = 0; r0 < a.n_rep; r0 += 32) {
+        const int r = r0 + c < a.n_rep ? r0 + c : a.n_rep - 1;
+        f32x16 s[NT];
+#pragma unroll
+        for (int I = 0; I < NT; ++I) s[I] = zero16();
+#pragma unroll
+        for (int g = 0; g < GN; ++g) {
+          const Frag k = O::plain(reps + (int64_t)r * DK + g * O::KG + h * (O::KG / 2));
+#pragma unroll
+          for (int I = 0; I < NT; ++I) s[I] = O::mma(k, q[I][g], s[I]);
+        }
+#pragma unroll
+        for (int I = 0; I < NT; ++I) {
+          float top = m[I];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (r0 + acc_row(e, h) < a.n_rep) top = fmaxf(top, s[I][e] * scale);
+          float add = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (r0 + acc_row(e, h) < a.n_rep) add += expf(s[I][e] * scale - top);
+          sum[I] = (m[I] > -INFINITY ? sum[I] * expf(m[I] - top) : 0.f) + add;
+          m[I] = top;
+        }
+      }
+    }
+    int any = 0;
+#pragma unroll
+    for (int I = 0; I < NT; ++I) {
+      const int i = 32 * I + c;
+      float g = 0.f;
+      if (j < nc) {
+        if (a.gates_in) {
+          if (i < n) g = a.gates_in[((b * n + i) * a.H + head) * a.n_cap + j];
+        } else {
+          const float m2 = __shfl_xor(m[I], 32, 64), s2 = __shfl_xor(sum[I], 32, 64);
+          const float top = fmaxf(m[I], m2);
+          const float all = (m[I] > -INFINITY ? sum[I] * expf(m[I] - top) : 0.f) + (m2 > -INFINITY ? s2 * expf(m2 - top) : 0.f);
+          g = 1.f / (1.f + expf(-(top + logf(all / (float)a.n_rep))));
+        }
+      }
+      if (!((here >> (i & 63)) & 1)) g = 0.f;
+      const bool keep = j < nc && ((here >> (i & 63)) & 1) && g >= a.tau;
+      any |= __any(keep);
+      if (h == 0 && i < n) {
+        if (a.gates_out) a.gates_out[((b * n + i) * a.H + head) * a.n_cap + j] = g;
+        if (j < nc) a.gate[(row * a.n_cap + j) * n + i] = keep ? g : 0.f;
+      }
+    }
+    if (lane == 0 && j < nc) a.active[row * a.n_cap + j] = any;
+  }
+}
+
+// The chain over the cached chunks, one workgroup a row.  A wave owns 32 columns of At (their z, as
+// accumulator tiles: rows the columns, column the node) or of Bc (their o).  bf16 maps go through LDS,
+// which hands them out transposed; z enters as three bf16 terms, float32 to its last bit.
+template <class T, int DK, int DV, int N>
+__global__ __launch_bounds__(256) void tree_chain_kernel(TreeArgs a) {
+  using O = La<T>;
+  using Frag = typename O::Frag;
+  constexpr bool BF = sizeof(T) == 2;
+  constexpr int NT = (N + 31) / 32, TILES = (DK + DV) / 32, TW = (TILES + 3) / 4, GN = DK / O::KG;
+  constexpr int RZ = O::template rs<DK>(), LD = BF ? DK * (DK + DV) / 8 / 256 : 1, LF = BF ? 1 : DK / 2;
+  __shared__ alignas(16) T at[BF ? DK * DK : 8], bt[BF ? DK * DV : 8];
+  __shared__ alignas(16) T zs[O::TERMS][N * RZ];
+  __shared__ unsigned char act[kTreeSlots];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, c = lane & 31;
+  const int64_t row = blockIdx.x, b = row / a.H;
+  const int head = (int)(row % a.H), n = a.n;
+  int nc = a.n_cache[b];
+  nc = nc < 0 ? 0 : (nc > a.n_cap ? a.n_cap : nc);
+  for (int j = tid; j < nc; j += 256) act[j] = (unsigned char)a.active[row * a.n_cap + j];
+  __syncthreads();
+  auto next = [&](int j) {
+    --j;
+    while (j >= 0 && !act[j]) --j;
+    return j;
+  };
+  const T* Ac = static_cast<const T*>(a.At_cache) + row * a.n_cap * DK * DK;
+  const T* Bc = static_cast<const T*>(a.Bc_cache) + row * a.n_cap * DK * DV;
+  u32x4 raw[LD];
+  float rawf[TW][LF];
+  float gn[NT];
+  auto load = [&](int j) {
+    if constexpr (BF) {
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        const int id = i * 256 + tid;
+        const T* p = id < DK * DK / 8 ? Ac + (int64_t)j * DK * DK + id * 8 : Bc + (int64_t)j * DK * DV + (id - DK * DK / 8) * 8;
+        raw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < TW; ++i) {
+        const int t = w + 4 * i;
+        if (t >= TILES) continue;
+        const bool isA = t < DK / 32;
+        const int W = isA ? DK : DV;
+        const T* p = isA ? Ac + (int64_t)j * DK * DK + 32 * t + c : Bc + (int64_t)j * DK * DV + 32 * t - DK + c;
+#pragma unroll
+        for (int k = 0; k < LF; ++k) rawf[i][k] = (float)p[((k >> 2) * 8 + h * 4 + (k & 3)) * W];
+      }
+    }
+#pragma unroll
+    for (int I = 0; I < NT; ++I) gn[I] = 32 * I + c < n ? a.gate[(row * a.n_cap + j) * n + 32 * I + c] : 0.f;
+  };
+  f32x16 v[TW][NT];  // z of this wave's columns of At, or o of its columns of Bc
+  auto put_z = [&](int t, int I, const f32x16& z) {
+    const int node = 32 * I + c;
+    if (node >= N) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = 32 * t + q * 8 + h * 4;
+      float r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = z[4 * q + e];
+#pragma unroll
+      for (int s = 0; s < O::TERMS; ++s) {
+        T* to = zs[s] + O::template at<DK>(node, col);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const T x = (T)r[e];
+          to[e] = x;
+          r[e] -= (float)x;
+        }
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    const int t = w + 4 * i;
+#pragma unroll
+    for (int I = 0; I < NT; ++I) {
+      v[i][I] = zero16();
+      if (t < DK / 32) {
+        const int node = 32 * I + c;
+        if (node < n) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(a.z + (row * n + node) * DK + 32 * t + q * 8 + h * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][I][4 * q + e] = x[e];
+          }
+        }
+        put_z(t, I, v[i][I]);
+      }
+    }
+  }
+  int j = next(nc);
+  if (j >= 0) load(j);
+  while (j >= 0) {
+    float g[NT];
+    Frag m[BF ? 1 : TW][GN];
+#pragma unroll
+    for (int I = 0; I < NT; ++I) g[I] = gn[I];
+    if constexpr (BF) {
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        const int id = i * 256 + tid;
+        if (id < DK * DK / 8) *reinterpret_cast<u32x4*>(at + O::template at<DK>(id / (DK / 8), id % (DK / 8) * 8)) = raw[i];
+        else {
+          const int k = id - DK * DK / 8;
+          *reinterpret_cast<u32x4*>(bt + O::template at<DV>(k / (DV / 8), k % (DV / 8) * 8)) = raw[i];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < TW; ++i)
+#pragma unroll
+        for (int k = 0; k < LF; ++k) m[i][k / 4][k % 4] = rawf[i][k];
+    }
+    __syncthreads();
+    const int jn = next(j);
+    if (jn >= 0) load(jn);
+    f32x16 acc[TW][NT];
+#pragma unroll
+    for (int i = 0; i < TW; ++i) {
+      const int t = w + 4 * i;
+#pragma unroll
+      for (int I = 0; I < NT; ++I) acc[i][I] = zero16();
+      if (t >= TILES) continue;
+#pragma unroll
+      for (int k = 0; k < GN; ++k) {
+        Frag f;
+        if constexpr (BF) f = t < DK / 32 ? O::template col<DK>(at, 32 * t, k, lane) : O::template col<DV>(bt, 32 * t - DK, k, lane);
+        else f = m[i][k];
+#pragma unroll
+        for (int I = 0; I < NT; ++I)
+#pragma unroll
+          for (int s = O::TERMS - 1; s >= 0; --s)
+            acc[i][I] = O::mma(f, O::template row<DK>(zs[s], (32 * I + c) % N, k, h), acc[i][I]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TW; ++i) {
+      const int t = w + 4 * i;
+      if (t >= TILES) continue;
+      const bool isA = t < DK / 32;
+#pragma unroll
+      for (int I = 0; I < NT; ++I) {
+        if (g[I] != 0.f) {  // a node that skips the chunk keeps its values, whatever the chunk holds
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[i][I][e] += g[I] * (acc[i][I][e] - (isA ? v[i][I][e] : 0.f));
+        }
+        if (isA) put_z(t, I, v[i][I]);
+      }
+    }
+    j = jn;
+  }
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    const int t = w + 4 * i;
+    if (t < DK / 32 || t >= TILES) continue;
+#pragma unroll
+    for (int I = 0; I < NT; ++I) {
+      const int node = 32 * I + c;
+      if (node >= n) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4* p = reinterpret_cast<f32x4*>(a.o + ((b * n + node) * a.H + head) * DV + 32 * t - DK + q * 8 + h * 4);
+        f32x4 x = *p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += v[i][I][4 * q + e];
+        *p = x;
+      }
+    }
+  }
+}
+
+// The accepted path enters the live matrices: a thread holds a whole column (its dk values), so the
+// tokens of the path follow one another without any exchange; the matrices are read and written once.
+template <class T, int DK, int DV>
+__global__ __launch_bounds__(DK + DV) void tree_accept_kernel(TreeAccept a) {
+  __shared__ alignas(16) float ks[kTreeNodes][DK];
+  __shared__ float al[kTreeNodes], be[kTreeNodes];
+  __shared__ int idx[kTreeNodes];
+  __shared__ int len_;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t row = blockIdx.x, b = row / a.H;
+  const int head = (int)(row % a.H), n = a.n;
+  if (tid < 64) {
+    const unsigned long long m = tree_path(a.parent + b * n, n, lane, 0.0).mask;
+    const int node = a.node[b];
+    const unsigned long long path = __shfl(m, node < 0 || node >= n ? 0 : node, 64);
+    const unsigned long long on = node < 0 || node >= n ? 0ull : path;
+    if ((on >> lane) & 1) {
+      const int at = __popcll(on & ((1ull << lane) - 1));
+      idx[at] = lane;
+      al[at] = a.alpha[(b * n + lane) * a.H + head];
+      be[at] = a.beta[(b * n + lane) * a.H + head];
+    }
+    if (lane == 0) len_ = __popcll(on);
+  }
+  __syncthreads();
+  const int len = len_;
+  bool commit = false;
+  int slot = 0;
+  if (a.commit && a.commit[b] != 0) {
+    slot = a.n_cache[b];
+    commit = slot >= 0 && slot < a.n_cap;
+  }
+  if (!len && !commit) return;
+  for (int id = tid; id < len * DK; id += DK + DV)
+    ks[id / DK][id % DK] = (float)static_cast<const T*>(a.k)[((b * n + idx[id / DK]) * a.H + head) * DK + id % DK];
+  const bool state = tid < DV;
+  const int col = state ? tid : tid - DV, W = state ? DV : DK;
+  float* p = state ? a.S_cur + row * DK * DV + col : a.At_cur ? a.At_cur + row * DK * DK + col : nullptr;
+  float x[DK];
+  if (p) {
+#pragma unroll
+    for (int r = 0; r < DK; ++r) x[r] = p[r * W];
+  }
+  __syncthreads();
+  if (!p) return;
+  for (int i = 0; i < len; ++i) {
+    const float alpha = al[i], beta = be[i];
+    const float v = state ? (float)static_cast<const T*>(a.v)[((b * n + idx[i]) * a.H + head) * DV + col] : 0.f;
+    float u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < DK; r += 4) {
+      const f32x4 k = *reinterpret_cast<const f32x4*>(&ks[i][r]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] += k[e] * x[r + e];
+    }
+    const float add = beta * (v - alpha * ((u[0] + u[1]) + (u[2] + u[3])));
+#pragma unroll
+    for (int r = 0; r < DK; r += 4) {
+      const f32x4 k = *reinterpret_cast<const f32x4*>(&ks[i][r]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[r + e] = alpha * x[r + e] + k[e] * add;
+    }
+  }
+  if (commit) {
+    T* to = state ? static_cast<T*>(a.Bc_cache) + (row * a.n_cap + slot) * DK * DV + col
+                  : static_cast<T*>(a.At_cache) + (row * a.n_cap + slot) * DK * DK + col;
+#pragma unroll
+    for (int r = 0; r < DK; ++r) {
+      to[r * W] = (T)x[r];
+      x[r] = !state && r == col ? 1.f : 0.f;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < DK; ++r) p[r * W] = x[r];
+}
+
+__global__ void tree_advance_kernel(int32_t* n_cache, const int32_t* commit, int32_t n_cap, int64_t Bs) {
+  const int64_t b = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  if (b < Bs && commit[b] != 0 && n_cache[b] >= 0 && n_cache[b] < n_cap) n_cache[b] += 1;
+}
+
+template <class T, int DK, int DV, int N>
+hipError_t decode_n(const TreeArgs& a, hipStream_t s) {
+  const unsigned rows = (unsigned)(a.Bs * a.H);
+  hipLaunchKernelGGL((tree_live_kernel<T, DK, DV, N>), dim3(rows), dim3(256), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.At_cur) return e;
+  // four chunks a wave, fewer where there are few rows
+  int per = 16;
+  while (per > 4 && (int64_t)rows * ((a.n_cap + per - 1) / per) < 512) per -= 4;
+  hipLaunchKernelGGL((tree_gates_kernel<T, DK, (N + 31) / 32>), dim3(rows, (a.n_cap + per - 1) / per), dim3(256), 0, s, a, per);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, N>), dim3(rows), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <class T, int DK, int DV>
+hipError_t decode_d(const TreeArgs& a, hipStream_t s) {
+  if (a.n <= 16) return decode_n<T, DK, DV, 16>(a, s);
+  if (a.n <= 32) return decode_n<T, DK, DV, 32>(a, s);
+  return decode_n<T, DK, DV, 64>(a, s);
+}
+
+template <class T>
+hipError_t decode_t(const TreeArgs& a, int dk, int dv, hipStream_t s) {
+  if (dk == 64) return dv == 64 ? decode_d<T, 64, 64>(a, s) : decode_d<T, 64, 128>(a, s);
+  return dv == 64 ? decode_d<T, 128, 64>(a, s) : decode_d<T, 128, 128>(a, s);
+}
+
+template <class T>
+void accept_t(const TreeAccept& a, int dk, int dv, hipStream_t s) {
+  const dim3 grid((unsigned)(a.Bs * a.H));
+  if (dk == 64 && dv == 64) hipLaunchKernelGGL((tree_accept_kernel<T, 64, 64>), grid, dim3(128), 0, s, a);
+  else if (dk == 64) hipLaunchKernelGGL((tree_accept_kernel<T, 64, 128>), grid, dim3(192), 0, s, a);
+  else if (dv == 64) hipLaunchKernelGGL((tree_accept_kernel<T, 128, 64>), grid, dim3(192), 0, s, a);
+  else hipLaunchKernelGGL((tree_accept_kernel<T, 128, 128>), grid, dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+hipError_t launch_tree_decode(const TreeArgs& a, int dtype, int dk, int dv, hipStream_t s) {
+  return dtype == HLA_BF16 ? decode_t<bf16>(a, dk, dv, s) : decode_t<float>(a, dk, dv, s);
+}
+
+hipError_t launch_tree_accept(const TreeAccept& a, int dtype, int dk, int dv, hipStream_t s) {
+  if (dtype == HLA_BF16) accept_t<bf16>(a, dk, dv, s);
+  else accept_t<float>(a, dk, dv, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.commit) return e;
+  hipLaunchKernelGGL(tree_advance_kernel, dim3((unsigned)((a.Bs + 255) / 256)), dim3(256), 0, s, a.n_cache, a.commit,
+                     a.n_cap, a.Bs);
+  return hipGetLastError();
+}
+
+}  // namespace hla

@@ -109,6 +109,13 @@ _SIGS = {
     "hla_la_workspace_bytes": (ctypes.c_int32, [ctypes.c_int32, _LA, ctypes.POINTER(ctypes.c_size_t)]),
     "hla_la_decode": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                        ctypes.c_int32, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P]),
+    "hla_gdn_tree_decode": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64] + [ctypes.c_int32] * 4 + [_P] * 11
+                            + [ctypes.c_int32, _P, ctypes.c_int32, _P, ctypes.c_float, _P, _P, _P, ctypes.c_size_t,
+                               _P]),
+    "hla_gdn_tree_workspace_bytes": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64] + [ctypes.c_int32] * 4
+                                     + [ctypes.POINTER(ctypes.c_size_t)]),
+    "hla_gdn_tree_accept": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64] + [ctypes.c_int32] * 4 + [_P] * 11
+                            + [ctypes.c_int32, _P, _P]),
     "hla_timing_enable": (ctypes.c_int32, [ctypes.c_int32]),
     "hla_timing_read": (ctypes.c_int32, [ctypes.c_int32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]),
     "hla_gdn_decode": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
@@ -1055,6 +1062,87 @@ def la_decode(q, k, v, log_decay, S, o=None):
     _call("hla_la_decode", dev, Bs, H, Hk, dk, dv, _dtype_code(v), _addr(q), _addr(k), _addr(v), _addr(log_decay),
           1 if log_decay.dim() == 1 else 0, _addr(S), _addr(o))
     return o
+
+
+# ------------------------------------------------- trees of drafted tokens (speculative decoding)
+MAX_TREE_NODES = 64
+
+
+def _tree_inputs(k, v, beta, alpha, parent, S_cur, At_cur):
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("k and v must be [Bs, n, H, width]")
+    (Bs, n, H, dk), dv, dev = k.shape, v.shape[-1], k.device
+    _need_on(k, (Bs, n, H, dk), k.dtype, dev, "k")
+    _need_on(v, (Bs, n, H, dv), k.dtype, dev, "v")
+    _need_on(beta, (Bs, n, H), torch.float32, dev, "beta")
+    _need_on(alpha, (Bs, n, H), torch.float32, dev, "alpha")
+    _need_on(parent, (Bs, n), torch.int32, dev, "parent")
+    _need_on(S_cur, (Bs, H, dk, dv), torch.float32, dev, "S_cur")
+    _need_on(At_cur, (Bs, H, dk, dk), torch.float32, dev, "At_cur")
+    return Bs, n, H, dk, dv, _dtype_code(k), dev
+
+
+def _tree_cache(At_cache, Bc_cache, n_cache, k, Bs, H, dk, dv, dev):
+    n_cap = At_cache.shape[2]
+    _need_on(At_cache, (Bs, H, n_cap, dk, dk), k.dtype, dev, "At_cache")
+    _need_on(Bc_cache, (Bs, H, n_cap, dk, dv), k.dtype, dev, "Bc_cache")
+    _need_on(n_cache, (Bs,), torch.int32, dev, "n_cache")
+    return n_cap
+
+
+def gdn_tree_workspace_bytes(Bs, H, n, dk, dv, n_cap) -> int:
+    out = ctypes.c_size_t(0)
+    _check(library().hla_gdn_tree_workspace_bytes(Bs, H, n, dk, dv, n_cap, ctypes.byref(out)),
+           "hla_gdn_tree_workspace_bytes")
+    return out.value
+
+
+def gdn_tree_decode(q, k, v, beta, alpha, parent, S_cur, At_cur=None, At_cache=None, Bc_cache=None, reps_cache=None,
+                    n_cache=None, gates_in=None, tau=1e-3, o=None, gates_out=None, ws=None):
+    """Every node of a tree of drafted tokens answered as gdn_decode would after its ancestors; nothing is
+    updated.  q, k [Bs, n, H, dk], v [Bs, n, H, dv]; beta, alpha [Bs, n, H]; parent int32 [Bs, n] (-1: the
+    live state; a node whose parent is out of range is absent).  Live matrices, cache and tau as for
+    gdn_decode; gates_in, gates_out [Bs, n, H, n_cap].  Returns o [Bs, n, H, dv] float32."""
+    Bs, n, H, dk, dv, dt, dev = _tree_inputs(k, v, beta, alpha, parent, S_cur, At_cur)
+    _need_on(q, (Bs, n, H, dk), k.dtype, dev, "q")
+    n_cap, n_rep = 0, 0
+    if At_cur is not None:
+        n_cap = _tree_cache(At_cache, Bc_cache, n_cache, k, Bs, H, dk, dv, dev)
+        if reps_cache is not None:
+            n_rep = reps_cache.shape[3]
+            _need_on(reps_cache, (Bs, H, n_cap, n_rep, dk), k.dtype, dev, "reps_cache")
+        _need_on(gates_in, (Bs, n, H, n_cap), torch.float32, dev, "gates_in")
+        _need_on(gates_out, (Bs, n, H, n_cap), torch.float32, dev, "gates_out")
+        if ws is None:
+            ws = _workspace(gdn_tree_workspace_bytes(Bs, H, n, dk, dv, n_cap), dev)
+        elif ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    if o is None:
+        o = torch.empty((Bs, n, H, dv), dtype=torch.float32, device=dev)
+    _need_on(o, (Bs, n, H, dv), torch.float32, dev, "o")
+    _call("hla_gdn_tree_decode", dev, Bs, H, n, dk, dv, dt, _addr(q), _addr(k), _addr(v), _addr(beta), _addr(alpha),
+          _addr(parent), _addr(S_cur), _addr(At_cur), _addr(At_cache), _addr(Bc_cache), _addr(reps_cache), n_rep,
+          _addr(n_cache), n_cap, _addr(gates_in), ctypes.c_float(tau), _addr(o), _addr(gates_out), _addr(ws),
+          0 if ws is None else ws.numel())
+    return o
+
+
+def gdn_tree_accept(k, v, beta, alpha, parent, node, S_cur, At_cur=None, At_cache=None, Bc_cache=None, n_cache=None,
+                    commit=None):
+    """The tokens on the path to `node` (int32 [Bs]; -1: none) enter S_cur and At_cur, in place.  commit
+    (int32 [Bs]): afterwards the live chunk of these sequences is appended to the cache and begins again,
+    as gdn_decode's commit.  Token arguments as for gdn_tree_decode."""
+    Bs, n, H, dk, dv, dt, dev = _tree_inputs(k, v, beta, alpha, parent, S_cur, At_cur)
+    _need_on(node, (Bs,), torch.int32, dev, "node")
+    n_cap = 0
+    if commit is not None:
+        _need_on(commit, (Bs,), torch.int32, dev, "commit")
+        if At_cur is None or At_cache is None or Bc_cache is None or n_cache is None:
+            raise ValueError("commit needs At_cur, At_cache, Bc_cache and n_cache")
+        n_cap = _tree_cache(At_cache, Bc_cache, n_cache, k, Bs, H, dk, dv, dev)
+    _call("hla_gdn_tree_accept", dev, Bs, H, n, dk, dv, dt, _addr(k), _addr(v), _addr(beta), _addr(alpha),
+          _addr(parent), _addr(node), _addr(S_cur), _addr(At_cur), _addr(At_cache), _addr(Bc_cache), _addr(n_cache),
+          n_cap, _addr(commit))
 
 
 def timing_enable(on: bool = True) -> None:

@@ -728,6 +728,59 @@ hla_status_t hla_la_decode(int64_t Bs, int64_t H, int64_t Hk, int32_t dk, int32_
                            const void* q, const void* k, const void* v, const float* log_decay,
                            int32_t decay_per_head, float* S, void* o, hipStream_t stream);
 
+/*
+ * Trees of drafted tokens (speculative decoding) over the state of hla_gdn_decode.  A sequence drafts
+ * up to n <= 64 tokens that form a tree; node i continues its parent's state by the gated delta rule
+ * (the live state for parent -1), and each is answered as hla_gdn_decode would answer it after its own
+ * ancestors.  hla_gdn_tree_decode answers all nodes and changes nothing; hla_gdn_tree_accept lets the
+ * path to an accepted node into the live state.
+ *   parent [Bs, n] int32 (device): -1 <= parent[i] < i.  Any other value (as -2 for the places behind a
+ *          smaller tree) marks node i absent, and so are the nodes below it: their inputs are not used,
+ *          their outputs and gates are zero.
+ *   q, k [Bs, n, H, dk], v [Bs, n, H, dv] (dtype);  beta, alpha [Bs, n, H] float32.
+ *   S_cur, At_cur, At_cache, Bc_cache, reps_cache, n_rep, n_cache, n_cap, tau: as for hla_gdn_decode;
+ *          n_cap <= 1024.  At_cur = NULL: no cache is read.
+ * q, k, v, o and the caches and live matrices are 16-byte aligned, the others 4-byte.
+ */
+
+/*
+ * hla_gdn_tree_decode
+ *   gates_in  [Bs, n, H, n_cap] float32 or NULL (then n_rep >= 1): every node's own gates.
+ *   o         [Bs, n, H, dv] float32 out.
+ *   gates_out [Bs, n, H, n_cap] float32 out or NULL: the gates in front of the threshold, 0 behind
+ *             n_cache[b] and at absent nodes.
+ *   ws        hla_gdn_tree_workspace_bytes() bytes (0 without At_cur, n_cap = 0), for one call at a time.
+ * Every chunk that any node reads is read once for all of them.  A NaN gate is below every threshold.
+ * float32 accumulation; over bf16 maps z enters as three bf16 terms (24 bits).
+ * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE (sizes, NaN tau), HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN,
+ *         HLA_ERR_WORKSPACE, HLA_ERR_HIP.
+ */
+hla_status_t hla_gdn_tree_decode(int64_t Bs, int64_t H, int32_t n, int32_t dk, int32_t dv, int32_t dtype,
+                                 const void* q, const void* k, const void* v, const float* beta,
+                                 const float* alpha, const int32_t* parent, const float* S_cur,
+                                 const float* At_cur, const void* At_cache, const void* Bc_cache,
+                                 const void* reps_cache, int32_t n_rep, const int32_t* n_cache,
+                                 int32_t n_cap, const float* gates_in, float tau, float* o,
+                                 float* gates_out, void* ws, size_t ws_bytes, hipStream_t stream);
+hla_status_t hla_gdn_tree_workspace_bytes(int64_t Bs, int64_t H, int32_t n, int32_t dk, int32_t dv,
+                                          int32_t n_cap, size_t* out);
+
+/*
+ * hla_gdn_tree_accept
+ *   node   [Bs] int32 (device): the accepted node, whose ancestors and itself enter S_cur (and At_cur)
+ *          in order; an absent or out-of-range one (-1): none.
+ *   commit [Bs] int32 (device) or NULL: where not 0, the live chunk is appended afterwards at slot
+ *          n_cache[b] (cast to dtype), At_cur is reset to I and S_cur to 0 and n_cache[b] advances, as
+ *          hla_gdn_decode's commit; a sequence whose cache is full is left as it is.  Needs At_cur and
+ *          the cache.
+ * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE, HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN, HLA_ERR_HIP.
+ */
+hla_status_t hla_gdn_tree_accept(int64_t Bs, int64_t H, int32_t n, int32_t dk, int32_t dv, int32_t dtype,
+                                 const void* k, const void* v, const float* beta, const float* alpha,
+                                 const int32_t* parent, const int32_t* node, float* S_cur, float* At_cur,
+                                 void* At_cache, void* Bc_cache, int32_t* n_cache, int32_t n_cap,
+                                 const int32_t* commit, hipStream_t stream);
+
 /* Workspace bytes that entry point `fn` needs for dims `d`; n_rep is the number of
  * representatives per chunk for HLA_FN_CHUNK_REPS (C / window; it must divide C), whether
  * Wr is given (0 or 1) for HLA_FN_CHUNK_REPS_BACKWARD, and ignored otherwise.  `out` is a
