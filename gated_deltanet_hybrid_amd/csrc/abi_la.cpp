@@ -31,7 +31,7 @@ hla_status_t check_dims(const hla_la_dims_t* d) {
   if (d->B < 1 || d->T < 1 || d->H < 1 || d->Hk < 1 || d->ld_T < d->T || d->H % d->Hk) return HLA_ERR_BAD_SHAPE;
   if ((d->dk != 64 && d->dk != 128) || (d->dv != 64 && d->dv != 128)) return HLA_ERR_BAD_SHAPE;
   if (d->decay_per_head != 0 && d->decay_per_head != 1) return HLA_ERR_BAD_SHAPE;
-  if ((double)d->B * (double)d->H > (double)kMaxRows || d->T > kMaxTokens) return HLA_ERR_BAD_SHAPE;
+  if (d->H > 65536 || (double)d->B * (double)d->H > (double)kMaxRows || d->T > kMaxTokens) return HLA_ERR_BAD_SHAPE;
   if ((double)d->B * (double)d->ld_T * (double)d->H * 128.0 > 4.0e18) return HLA_ERR_BAD_SHAPE;
   return HLA_OK;
 }

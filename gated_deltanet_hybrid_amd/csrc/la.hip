@@ -113,27 +113,39 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
   const float* gp = a.per_head ? a.g + head : a.g + b * a.ld_g * a.H + head;
 
   // row r of piece p is token P p + r, or counted from the piece's end
-  auto token = [&](int64_t p, int r) -> int64_t { return p * P + (REV ? P - 1 - r : r); };
+  auto row_of = [](int r) { return REV ? P - 1 - r : r; };
+  auto token = [&](int64_t p, int r) -> int64_t { return p * P + row_of(r); };
   auto load_g = [&](int64_t p) -> float {
     if (lane >= P) return 0.f;
     const int64_t t = token(p, lane) + (REV ? 1 : 0);
     return t < Tb ? (a.per_head ? gp[0] : gp[t * a.H]) : 0.f;
   };
   u32x4 r1[OUT ? N1 : 1], r2[N1], r3[N3], r4[EXTRA ? N3 : 1];
-  auto load_tile = [&](const T* base, int64_t stride, int width, int64_t p, u32x4* regs, int count) {
-    const int cpr = width / V;
+  // A thread moves the same columns of every RS-th row of a tile, so its addresses are one 32-bit offset
+  // (64 rows of heads * width elements stay below 2^31 bytes: the host checks) from uniform pointers.
+  auto load_tile = [&](const T* base, int heads, auto width, int64_t p, u32x4* regs) {
+    constexpr int W = decltype(width)::value, CPR = W / V, RS = NT / CPR, N = P * W / V / NT;
+    const int stride = own_s(heads * W);
+    const int r0 = tid / CPR, t0 = REV ? P - 1 - r0 : r0;
+    const unsigned off = (unsigned)(t0 * stride + tid % CPR * V);
+    const T* at = base + p * P * stride;
+    const int64_t left = Tb - p * P;
 #pragma unroll
-    for (int i = 0; i < count; ++i) {
-      const int id = i * NT + tid;
-      const int64_t t = token(p, id / cpr);
-      regs[i] = t < Tb ? *reinterpret_cast<const u32x4*>(base + t * stride + (id % cpr) * V) : u32x4{0, 0, 0, 0};
+    for (int i = 0; i < N; ++i) {
+      const int step = REV ? -RS * i : RS * i;
+      const T* u = at + (int64_t)(REV ? 0 : step) * stride;
+      const unsigned o = REV ? off - (unsigned)(RS * i * stride) : off;
+      if (left >= P) regs[i] = *reinterpret_cast<const u32x4*>(u + o);
+      else regs[i] = t0 + step < left ? *reinterpret_cast<const u32x4*>(u + o) : u32x4{0, 0, 0, 0};
     }
   };
   auto load = [&](int64_t p) {
-    if constexpr (OUT) load_tile(p1, (int64_t)a.x1.heads * DK, DK, p, r1, N1);
-    load_tile(p2, (int64_t)a.x2.heads * DK, DK, p, r2, N1);
-    load_tile(p3, (int64_t)a.x3.heads * DV, DV, p, r3, N3);
-    if constexpr (EXTRA) load_tile(p4, (int64_t)a.x4.heads * DV, DV, p, r4, N3);
+    using WK = std::integral_constant<int, DK>;
+    using WV = std::integral_constant<int, DV>;
+    if constexpr (OUT) load_tile(p1, a.x1.heads, WK{}, p, r1);
+    load_tile(p2, a.x2.heads, WK{}, p, r2);
+    load_tile(p3, a.x3.heads, WV{}, p, r3);
+    if constexpr (EXTRA) load_tile(p4, a.x4.heads, WV{}, p, r4);
   };
   auto store = [&]() {
 #pragma unroll
@@ -167,6 +179,9 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
     for (int m = 0; m < MT; ++m) M[m] = zero16();
   }
 
+  const int rk0 = O::template row_base<DK>(lane), rv0 = O::template row_base<DV>(lane);
+  const int rc0 = O::template rowc_base<DK>(lane), ck0 = O::template col_base<DK>(lane), cv0 = O::template col_base<DV>(lane);
+  (void)rk0; (void)rv0; (void)rc0;
   double decay = 0.0;
   if (n) {
     load(piece(0));
@@ -175,6 +190,8 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
   for (int64_t i = 0; i < n; ++i) {
     const int64_t p = piece(i);
     const Decays<P>& d = sh.d[i & 1];
+    const int rk = own(rk0), rv = own(rv0), rc = own(rc0), ck = own(ck0), cv = own(cv0);
+    (void)rk; (void)rv; (void)rc;
     store();
     __syncthreads();
     float gnext = 0.f;
@@ -191,7 +208,8 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
         f32x16 s = zero16();
 #pragma unroll
         for (int g = 0; g < DK / O::KG; ++g)
-          s = O::mma(O::template row<DK>(sh.x2, 32 * J + c, g, h), O::template row<DK>(sh.x1, 32 * I + c, g, h), s);
+          s = O::mma(O::template row<DK>(sh.x2, rk, 32 * J, g), O::template row<DK>(sh.x1, rk, 32 * I, g), s);
+        sched_fence();
         const int ii = 32 * I + c;
         const double lgi = d.lg[ii];
         float D[16];
@@ -212,7 +230,7 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
           f32x16 u = zero16();
 #pragma unroll
           for (int g = 0; g < DV / O::KG; ++g)
-            u = O::mma(O::template row<DV>(sh.x3, 32 * J + c, g, h), O::template row<DV>(sh.x4, 32 * I + c, g, h), u);
+            u = O::mma(O::template row<DV>(sh.x3, rv, 32 * J, g), O::template row<DV>(sh.x4, rv, 32 * I, g), u);
           float rs = 0.f;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -232,17 +250,18 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
 #pragma unroll
       for (int g = 0; g < DK / O::KG; ++g) {
         constexpr int GT = 32 / O::KG, TERMS = EXTRA || O::TERMS < 2 ? O::TERMS : 2;
-        float x[O::FN];
+        typename O::Vals x;
         Frag f[TERMS];
 #pragma unroll
         for (int e = 0; e < O::FN; ++e) x[e] = M[g / GT][O::FN * (g % GT) + e];
         O::split(x, f);
 #pragma unroll
         for (int I = 0; I < IT; ++I) {
-          const Frag q = O::template rowc<DK>(sh.x1, 32 * I + c, g, h);
+          const Frag q = O::template rowc<DK>(sh.x1, rc, 32 * I, g);
 #pragma unroll
           for (int t = TERMS - 1; t >= 0; --t) acc[I] = O::mma(q, f[t], acc[I]);
         }
+        if (g % 2) sched_fence();
       }
 #pragma unroll
       for (int I = 0; I < IT; ++I)
@@ -266,14 +285,14 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
       for (int e = 0; e < 16; ++e) M[m][e] *= total;
 #pragma unroll
     for (int g = 0; g < P / O::KG; ++g) {
-      const Frag v = O::template col<DV>(sh.x3, 32 * w, g, lane);
+      const Frag v = O::template col<DV>(sh.x3, cv, w, g);
       if constexpr (OUT) {
 #pragma unroll
         for (int I = 0; I < IT; ++I)
           if (g * O::KG < 32 * (I + 1))
             acc[I] = O::mma(O::plain(sh.sc + (32 * I + c) * O::PS + O::col_k(g, h)), v, acc[I]);
       }
-      float x[O::FN];
+      typename O::Vals x;
       Frag f[O::TERMS];
       const int k0 = O::col_k(g, h);
 #pragma unroll
@@ -281,24 +300,43 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
       O::split(x, f);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const Frag k = O::template col<DK>(sh.x2, 32 * m, g, lane);
+        const Frag k = O::template col<DK>(sh.x2, ck, m, g);
 #pragma unroll
         for (int t = O::TERMS - 1; t >= 0; --t) M[m] = O::mma(k, f[t], M[m]);
       }
+      sched_fence();
     }
     if constexpr (OUT) {
-      const int64_t o0 = (b * a.T * a.H + head) * DV + col;
+      // rows 32 I + 8 q + 4 h + e: the lane's offset holds 4 h, a uniform pointer walks the rest
+      const int stride = own_s((int)a.H * DV);
+      const int rows = (int)(a.T - p * P < P ? a.T - p * P : P), live_rows = (int)(Tb - p * P < P ? Tb - p * P : P);
+      const unsigned off = (unsigned)((REV ? 4 - 4 * h : 4 * h) * stride + col);
+      const int64_t o0 = ((b * a.T + p * P) * a.H + head) * DV;
+      if (live_rows < P) {
 #pragma unroll
-      for (int I = 0; I < IT; ++I)
+        for (int I = 0; I < IT; ++I)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int64_t t = token(p, 32 * I + acc_row(e, h));
-          if (t >= a.T) continue;
-          const float x = t < Tb ? acc[I][e] : 0.f;
-          const int64_t at = o0 + t * a.H * DV;
-          if (a.out_f32) static_cast<float*>(a.out)[at] = x;
-          else static_cast<T*>(a.out)[at] = (T)x;
-        }
+          for (int e = 0; e < 16; ++e) acc[I][e] = row_of(32 * I + acc_row(e, h)) < live_rows ? acc[I][e] : 0.f;
+      }
+      auto put = [&](auto* out, auto whole) {
+        using TO = std::remove_pointer_t<decltype(out)>;
+        TO* at = out + (REV ? (int64_t)(P - 5) * stride : 0);
+#pragma unroll
+        for (int I = 0; I < IT; ++I)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (decltype(whole)::value || row_of(32 * I + acc_row(e, h)) < rows) at[off] = (TO)acc[I][e];
+            const int step = e % 4 == 3 ? 5 : 1;
+            at += REV ? -(step * stride) : step * stride;
+          }
+      };
+      if (rows == P) {
+        if (a.out_f32) put(static_cast<float*>(a.out) + o0, std::true_type{});
+        else put(static_cast<T*>(a.out) + o0, std::true_type{});
+      } else {
+        if (a.out_f32) put(static_cast<float*>(a.out) + o0, std::false_type{});
+        else put(static_cast<T*>(a.out) + o0, std::false_type{});
+      }
       if constexpr (EXTRA) {
         if (tid < P) {
           const int64_t t = token(p, tid);

@@ -13,6 +13,18 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // every LDS read to the front and spill.
 __device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
 
+// The value, as one that the compiler knows nothing of: in a loop, what is computed from it is computed
+// again each time and not kept in registers from before.
+__device__ __forceinline__ int own(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+__device__ __forceinline__ int own_s(int x) {  // of a uniform value
+  asm volatile("" : "+s"(x));
+  return x;
+}
+
 // The operands of a product over K: `Frag` is what a lane holds of KG consecutive k.
 // bf16: one 32x32x16 instruction, 8 values a lane.  float32: four 32x32x2, slot e of the group is
 // k = 4 h + e, which is also the order in which an accumulator holds its rows.
@@ -33,40 +45,44 @@ template <> struct La<bf16> {
   __device__ __forceinline__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  // k = 16 g + 8 h + e of one row
-  __device__ __forceinline__ static Frag plain(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
-  template <int W> __device__ __forceinline__ static Frag row(const bf16* t, int r, int g, int h) {
-    return plain(t + at<W>(r, g * 16 + h * 8));
+  // Element offsets that a lane's reads start from; the chunk permutation makes every further read an
+  // exclusive or of a constant.  `own` (see there) keeps these few in registers, not the reads' own.
+  template <int W> __device__ __forceinline__ static int row_base(int lane) { return at<W>(lane & 31, (lane >> 5) * 8); }
+  template <int W> __device__ __forceinline__ static int rowc_base(int lane) { return at<W>(lane & 31, (lane >> 5) * 4); }
+  template <int W> __device__ __forceinline__ static int col_base(int lane) {
+    return at<W>((lane >> 5) * 8 + ((lane >> 2) & 3), ((lane >> 4) & 1) * 16 + (lane & 3) * 4);
   }
-  // k = 16 g + 8 (e / 4) + 4 h + e % 4: the accumulators' order
-  template <int W> __device__ __forceinline__ static Frag rowc(const bf16* t, int r, int g, int h) {
-    const bf16x4 lo = *reinterpret_cast<const bf16x4*>(t + at<W>(r, g * 16 + h * 4));
-    const bf16x4 hi = *reinterpret_cast<const bf16x4*>(t + at<W>(r, g * 16 + 8 + h * 4));
+  // row r0 + lane % 32 (r0 a multiple of 16): k = 16 g + 8 h + e
+  __device__ __forceinline__ static Frag plain(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
+  template <int W> __device__ __forceinline__ static Frag row(const bf16* t, int base, int r0, int g) {
+    return plain(t + r0 * W + (base ^ (g << 4)));
+  }
+  // the same row, k = 16 g + 8 (e / 4) + 4 h + e % 4: the accumulators' order
+  template <int W> __device__ __forceinline__ static Frag rowc(const bf16* t, int base, int r0, int g) {
+    const bf16x4 lo = *reinterpret_cast<const bf16x4*>(t + r0 * W + (base ^ (g << 4)));
+    const bf16x4 hi = *reinterpret_cast<const bf16x4*>(t + r0 * W + (base ^ (g << 4) ^ 8));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
-  // column n0 + lane % 32, rows k = 16 g + 8 h + e: the transposing LDS read hands lane i of 16 the
+  // column 32 m + lane % 32, rows k = 16 g + 8 h + e: the transposing LDS read hands lane i of 16 the
   // i-th column of the four rows that its 16 lanes address (4 lanes a row, 4 columns each)
-  template <int W> __device__ __forceinline__ static Frag col(const bf16* t, int n0, int g, int lane) {
-    const int k = g * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3), c = n0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+  template <int W> __device__ __forceinline__ static Frag col(const bf16* t, int base, int m, int g) {
     typedef __attribute__((address_space(3))) s16x4 lds4;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + at<W>(k, c)));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + at<W>(k + 4, c)));
+    const bf16* p = t + g * 16 * W;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + (base ^ (m << 5))));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * W + (base ^ (m << 5) ^ 8)));
     return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
   __device__ __forceinline__ static int col_k(int g, int h) { return g * 16 + h * 8; }  // first of 8 k
+  static constexpr int FN = 8;
+  typedef float Vals __attribute__((ext_vector_type(8)));
   // the first N bf16 terms of 8 float32 values
-  template <int N> __device__ __forceinline__ static void split(const float (&x)[8], Frag (&f)[N]) {
+  template <int N> __device__ __forceinline__ static void split(Vals x, Frag (&f)[N]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float r = x[e];
-#pragma unroll
-      for (int t = 0; t < N; ++t) {
-        f[t][e] = (bf16)r;
-        r -= (float)f[t][e];
-      }
+    for (int t = 0; t < N; ++t) {
+      f[t] = __builtin_convertvector(x, Frag);
+      if (t + 1 < N) x -= __builtin_convertvector(f[t], Vals);
     }
   }
-  static constexpr int FN = 8;
 };
 
 template <> struct La<float> {
@@ -81,25 +97,26 @@ template <> struct La<float> {
     for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
     return c;
   }
+  template <int W> __device__ __forceinline__ static int row_base(int lane) { return at<W>(lane & 31, (lane >> 5) * 4); }
+  template <int W> __device__ __forceinline__ static int rowc_base(int lane) { return row_base<W>(lane); }
+  template <int W> __device__ __forceinline__ static int col_base(int lane) { return at<W>((lane >> 5) * 4, lane & 31); }
   __device__ __forceinline__ static Frag plain(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-  template <int W> __device__ __forceinline__ static Frag row(const float* t, int r, int g, int h) {
-    return plain(t + at<W>(r, g * 8 + h * 4));
+  template <int W> __device__ __forceinline__ static Frag row(const float* t, int base, int r0, int g) {
+    return plain(t + base + r0 * (W + 8) + g * 8);
   }
-  template <int W> __device__ __forceinline__ static Frag rowc(const float* t, int r, int g, int h) {
-    return row<W>(t, r, g, h);
+  template <int W> __device__ __forceinline__ static Frag rowc(const float* t, int base, int r0, int g) {
+    return row<W>(t, base, r0, g);
   }
-  template <int W> __device__ __forceinline__ static Frag col(const float* t, int n0, int g, int lane) {
+  template <int W> __device__ __forceinline__ static Frag col(const float* t, int base, int m, int g) {
     Frag f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = t[at<W>(g * 8 + (lane >> 5) * 4 + e, n0 + (lane & 31))];
+    for (int e = 0; e < 4; ++e) f[e] = t[base + (g * 8 + e) * (W + 8) + 32 * m];
     return f;
   }
   __device__ __forceinline__ static int col_k(int g, int h) { return g * 8 + h * 4; }
-  template <int N> __device__ __forceinline__ static void split(const float (&x)[4], Frag (&f)[N]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[0][e] = x[e];
-  }
   static constexpr int FN = 4;
+  typedef f32x4 Vals;
+  template <int N> __device__ __forceinline__ static void split(Vals x, Frag (&f)[N]) { f[0] = x; }
 };
 
 }  // namespace hla

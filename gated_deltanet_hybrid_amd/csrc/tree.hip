@@ -110,12 +110,12 @@ __global__ __launch_bounds__(256) void tree_live_kernel(TreeArgs a) {
   for (int job = w; job < 2 * NT * NT; job += 4) {
     const int which = job & 1, I = (job >> 1) / NT, J = (job >> 1) % NT;
     if (J > I) continue;
-    const int i = (32 * I + c) % N, jr = (32 * J + c) % N;
+    const int i = (32 * I + c) % N, rb = O::template row_base<DK>(lane % 32 % N + (lane & 32));
     f32x16 s = zero16();
     const T* other = which ? sh.in.q : sh.in.k;
 #pragma unroll
     for (int g = 0; g < DK / O::KG; ++g)
-      s = O::mma(O::template row<DK>(sh.in.k, jr, g, h), O::template row<DK>(other, i, g, h), s);
+      s = O::mma(O::template row<DK>(sh.in.k, rb, 32 * J, g), O::template row<DK>(other, rb, 32 * I, g), s);
     if (32 * I + c < N) {
       const unsigned long long m = sh.mask[i];
       const double lgi = sh.lg[i];
@@ -400,9 +400,13 @@ __global__ __launch_bounds__(256) void tree_chain_kernel(TreeArgs a) {
       }
     }
   }
+  const int rz0 = O::template row_base<DK>(lane % 32 % N + (lane & 32));
+  const int ck0 = O::template col_base<DK>(lane), cv0 = O::template col_base<DV>(lane);
   int j = next(nc);
   if (j >= 0) load(j);
   while (j >= 0) {
+    const int rz = own(rz0), ck = own(ck0), cv = own(cv0);
+    (void)ck; (void)cv;
     float g[NT];
     Frag m[BF ? 1 : TW][GN];
 #pragma unroll
@@ -436,13 +440,13 @@ __global__ __launch_bounds__(256) void tree_chain_kernel(TreeArgs a) {
 #pragma unroll
       for (int k = 0; k < GN; ++k) {
         Frag f;
-        if constexpr (BF) f = t < DK / 32 ? O::template col<DK>(at, 32 * t, k, lane) : O::template col<DV>(bt, 32 * t - DK, k, lane);
+        if constexpr (BF) f = t < DK / 32 ? O::template col<DK>(at, ck, t, k) : O::template col<DV>(bt, cv, t - DK / 32, k);
         else f = m[i][k];
 #pragma unroll
         for (int I = 0; I < NT; ++I)
 #pragma unroll
           for (int s = O::TERMS - 1; s >= 0; --s)
-            acc[i][I] = O::mma(f, O::template row<DK>(zs[s], (32 * I + c) % N, k, h), acc[i][I]);
+            acc[i][I] = O::mma(f, O::template row<DK>(zs[s], rz, 32 * I, k), acc[i][I]);
       }
     }
     __syncthreads();
