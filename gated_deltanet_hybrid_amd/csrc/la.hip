@@ -80,13 +80,13 @@ template <class T, int DK, int DV, bool OUT, int EXTRA> struct LaShared {
 // of the segment; else the segment's state (from init, or zero).  EXTRA: the products with x4 that
 // the decays' gradient takes.
 template <class T, int DK, int DV, bool OUT, bool REV, int EXTRA>
-__global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
+__global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_sweep_kernel(LaSweep a) {
   using O = La<T>;
   using Frag = typename O::Frag;
   constexpr int P = O::P, NT = DV * 2, NW = DV / 32, MT = DK / 32, IT = P / 32, V = 16 / (int)sizeof(T);
   constexpr int N1 = P * DK / V / NT, N3 = P * DV / V / NT;  // 16-byte pieces a thread moves of each tile
   __shared__ LaShared<T, DK, DV, OUT, EXTRA> sh;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, c = lane & 31;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h0 = lane >> 5, c0 = lane & 31;
   const int64_t row = blockIdx.x / a.nseg;
   const int seg = blockIdx.x % a.nseg;
   if (!OUT && a.loc && !a.whole && seg == (REV ? 0 : a.nseg - 1)) return;  // no segment starts behind it
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
   auto load_tile = [&](const T* base, int heads, auto width, int64_t p, u32x4* regs) {
     constexpr int W = decltype(width)::value, CPR = W / V, RS = NT / CPR, N = P * W / V / NT;
     const int stride = own_s(heads * W);
-    const int r0 = tid / CPR, t0 = REV ? P - 1 - r0 : r0;
+    const int r0 = own(tid) / CPR, t0 = REV ? P - 1 - r0 : r0;
     const unsigned off = (unsigned)(t0 * stride + tid % CPR * V);
     const T* at = base + p * P * stride;
     const int64_t left = Tb - p * P;
@@ -164,14 +164,14 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
   auto piece = [&](int64_t i) { return REV ? last - 1 - i : first + i; };
 
   f32x16 M[MT];
-  const int col = 32 * w + c;
+  const int col = 32 * w + c0;
   if (a.init) {
     const float* s0 = a.init + row * a.init_row + (int64_t)seg * DK * DV;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int r = 32 * m + acc_row(e, h);
+        const int r = 32 * m + acc_row(e, h0);
         M[m][e] = a.init_t ? s0[col * DK + r] : s0[r * DV + col];
       }
   } else {
@@ -183,22 +183,27 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
   const int rc0 = O::template rowc_base<DK>(lane), ck0 = O::template col_base<DK>(lane), cv0 = O::template col_base<DV>(lane);
   (void)rk0; (void)rv0; (void)rc0;
   double decay = 0.0;
-  if (n) {
+  float gnext = 0.f;  // two pieces ahead and in front of the tiles: memory answers in order, and the sums
+  if (n) {            // of the next piece must not wait for its tiles
+    if (w == NW - 1) {
+      const float g0 = load_g(piece(0));
+      if (n > 1) gnext = load_g(piece(1));
+      decays<P>(g0, lane, sh.d[0], &decay);
+    }
     load(piece(0));
-    if (w == NW - 1) decays<P>(load_g(piece(0)), lane, sh.d[0], &decay);
   }
   for (int64_t i = 0; i < n; ++i) {
     const int64_t p = piece(i);
     const Decays<P>& d = sh.d[i & 1];
+    const int h = own(h0), c = own(c0);  // row indices are formed again in every piece, not kept
     const int rk = own(rk0), rv = own(rv0), rc = own(rc0), ck = own(ck0), cv = own(cv0);
     (void)rk; (void)rv; (void)rc;
     store();
     __syncthreads();
-    float gnext = 0.f;
-    if (i + 1 < n) {
-      load(piece(i + 1));
-      if (w == NW - 1) gnext = load_g(piece(i + 1));
-    }
+    float gnow;  // a copy made here, where the tiles have arrived anyway, frees gnext for the next load
+    asm volatile("v_mov_b32 %0, %1" : "=v"(gnow) : "v"(gnext));
+    if (i + 2 < n && w == NW - 1) gnext = load_g(piece(i + 2));
+    if (i + 1 < n) load(piece(i + 1));
     f32x16 acc[IT];
     if constexpr (OUT) {
       // decayed scores, transposed: rows j, column i, so that a lane writes runs of one row
@@ -212,12 +217,12 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
         sched_fence();
         const int ii = 32 * I + c;
         const double lgi = d.lg[ii];
-        float D[16];
+        // selects and no branches: every sum is read, and what lies behind i becomes 2^-inf
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int j = 32 * J + acc_row(e, h);
-          D[e] = j <= ii ? exp2_((float)(lgi - d.lg[j])) : 0.f;
-          s[e] = j <= ii ? s[e] * D[e] : 0.f;
+          const float x = (float)(lgi - d.lg[j]);
+          s[e] = (j <= ii ? s[e] : 0.f) * exp2_(j <= ii ? x : -INFINITY);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -275,7 +280,7 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
           }
         }
     }
-    if (i + 1 < n && w == NW - 1) decays<P>(gnext, lane, sh.d[(i + 1) & 1], &decay);
+    if (i + 1 < n && w == NW - 1) decays<P>(gnow, lane, sh.d[(i + 1) & 1], &decay);
     if constexpr (OUT) __syncthreads();
     // the decayed values join the state; the scores meet the values as they are
     const float total = d.total;
@@ -386,7 +391,7 @@ __global__ __launch_bounds__(DV * 2, 2) void la_sweep_kernel(LaSweep a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) to[(32 * m + acc_row(e, h)) * DV + col] = M[m][e] * last_decay;
+      for (int e = 0; e < 16; ++e) to[(32 * m + acc_row(e, h0)) * DV + col] = M[m][e] * last_decay;
   }
   if (a.decay && tid == NT - 64) a.decay[row * a.nseg + seg] = decay;
 }

@@ -75,12 +75,21 @@ template <> struct La<bf16> {
   __device__ __forceinline__ static int col_k(int g, int h) { return g * 16 + h * 8; }  // first of 8 k
   static constexpr int FN = 8;
   typedef float Vals __attribute__((ext_vector_type(8)));
-  // the first N bf16 terms of 8 float32 values
+  // the first N bf16 terms of 8 float32 values (pairs: one conversion packs two)
   template <int N> __device__ __forceinline__ static void split(Vals x, Frag (&f)[N]) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-      f[t] = __builtin_convertvector(x, Frag);
-      if (t + 1 < N) x -= __builtin_convertvector(f[t], Vals);
+      unsigned u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{x[2 * e], x[2 * e + 1]}, bf16x2));
+        if (t + 1 < N) {
+          x[2 * e] -= __builtin_bit_cast(float, u[e] << 16);
+          x[2 * e + 1] -= __builtin_bit_cast(float, u[e] & 0xffff0000u);
+        }
+      }
+      f[t] = __builtin_bit_cast(Frag, u32x4{u[0], u[1], u[2], u[3]});
     }
   }
 };
