@@ -76,6 +76,26 @@ template <class T, int DK, int DV, bool OUT, int EXTRA> struct LaShared {
   float erow[EXTRA > 1 ? 3 : 1][32], ecol[EXTRA > 1 ? 3 : 1][32];
 };
 
+// s += rows [a0, a0 + 32) of `a` times rows [b0, b0 + 32) of `b`, W columns; eight reads ahead of their four products.
+template <int W, class T>
+__device__ __forceinline__ void score(f32x16& s, const T* a, const T* b, int base, int a0, int b0) {
+  using O = La<T>;
+  constexpr int GN = W / O::KG, ST = 4;
+#pragma unroll
+  for (int g0 = 0; g0 < GN; g0 += ST) {
+    typename O::Frag x[ST], y[ST];
+#pragma unroll
+    for (int g = 0; g < ST; ++g) {
+      x[g] = O::template row<W>(a, base, a0, g0 + g);
+      y[g] = O::template row<W>(b, base, b0, g0 + g);
+    }
+    sched_fence();
+#pragma unroll
+    for (int g = 0; g < ST; ++g) s = O::mma(x[g], y[g], s);
+    sched_fence();
+  }
+}
+
 // One workgroup of DV / 32 waves runs one segment of one row.  OUT: outputs from the state in front
 // of the segment; else the segment's state (from init, or zero).  EXTRA: the products with x4 that
 // the decays' gradient takes.
@@ -139,13 +159,15 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
       else regs[i] = t0 + step < left ? *reinterpret_cast<const u32x4*>(u + o) : u32x4{0, 0, 0, 0};
     }
   };
-  auto load = [&](int64_t p) {
+  // x1 and x4 are done with sooner than the others, and their next tiles are asked for then (EXTRA:
+  // registers are short) or with the others
+  auto load = [&](int64_t p, bool front, bool back) {
     using WK = std::integral_constant<int, DK>;
     using WV = std::integral_constant<int, DV>;
-    if constexpr (OUT) load_tile(p1, a.x1.heads, WK{}, p, r1);
-    load_tile(p2, a.x2.heads, WK{}, p, r2);
-    load_tile(p3, a.x3.heads, WV{}, p, r3);
-    if constexpr (EXTRA) load_tile(p4, a.x4.heads, WV{}, p, r4);
+    if constexpr (OUT) if (back) load_tile(p1, a.x1.heads, WK{}, p, r1);
+    if (front) load_tile(p2, a.x2.heads, WK{}, p, r2);
+    if (front) load_tile(p3, a.x3.heads, WV{}, p, r3);
+    if constexpr (EXTRA) if (back) load_tile(p4, a.x4.heads, WV{}, p, r4);
   };
   auto store = [&]() {
 #pragma unroll
@@ -180,7 +202,8 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
   }
 
   const int rk0 = O::template row_base<DK>(lane), rv0 = O::template row_base<DV>(lane);
-  const int rc0 = O::template rowc_base<DK>(lane), ck0 = O::template col_base<DK>(lane), cv0 = O::template col_base<DV>(lane);
+  const int rc0 = O::template rowc_base<DK>(lane), ck0 = O::template col_base<DK>(lane), cv0 = O::template col_base<DV>(lane),
+            xa0 = O::template acc_base<DV>(lane, col);
   (void)rk0; (void)rv0; (void)rc0;
   double decay = 0.0;
   float gnext = 0.f;  // two pieces ahead and in front of the tiles: memory answers in order, and the sums
@@ -190,20 +213,20 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
       if (n > 1) gnext = load_g(piece(1));
       decays<P>(g0, lane, sh.d[0], &decay);
     }
-    load(piece(0));
+    load(piece(0), true, true);
   }
   for (int64_t i = 0; i < n; ++i) {
     const int64_t p = piece(i);
     const Decays<P>& d = sh.d[i & 1];
     const int h = own(h0), c = own(c0);  // row indices are formed again in every piece, not kept
-    const int rk = own(rk0), rv = own(rv0), rc = own(rc0), ck = own(ck0), cv = own(cv0);
-    (void)rk; (void)rv; (void)rc;
+    const int rk = own(rk0), rv = own(rv0), rc = own(rc0), ck = own(ck0), cv = own(cv0), xa = own(xa0);
+    (void)rk; (void)rv; (void)rc; (void)xa;
     store();
     __syncthreads();
     float gnow;  // a copy made here, where the tiles have arrived anyway, frees gnext for the next load
     asm volatile("v_mov_b32 %0, %1" : "=v"(gnow) : "v"(gnext));
     if (i + 2 < n && w == NW - 1) gnext = load_g(piece(i + 2));
-    if (i + 1 < n) load(piece(i + 1));
+    if (i + 1 < n) load(piece(i + 1), true, !EXTRA);
     f32x16 acc[IT];
     if constexpr (OUT) {
       // decayed scores, transposed: rows j, column i, so that a lane writes runs of one row
@@ -211,10 +234,7 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
       for (int tile = w; tile < TILES; tile += NW) {
         const int I = tile ? 1 : 0, J = tile == 2 ? 1 : 0;
         f32x16 s = zero16();
-#pragma unroll
-        for (int g = 0; g < DK / O::KG; ++g)
-          s = O::mma(O::template row<DK>(sh.x2, rk, 32 * J, g), O::template row<DK>(sh.x1, rk, 32 * I, g), s);
-        sched_fence();
+        score<DK>(s, sh.x2, sh.x1, rk, 32 * J, 32 * I);
         const int ii = 32 * I + c;
         const double lgi = d.lg[ii];
         // selects and no branches: every sum is read, and what lies behind i becomes 2^-inf
@@ -233,40 +253,52 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
         if constexpr (EXTRA > 1) {
           // E_ij = D_ij (x1_i . x2_j)(x4_i . x3_j) for j < i: its sums over each row and each column
           f32x16 u = zero16();
-#pragma unroll
-          for (int g = 0; g < DV / O::KG; ++g)
-            u = O::mma(O::template row<DV>(sh.x3, rv, 32 * J, g), O::template row<DV>(sh.x4, rv, 32 * I, g), u);
-          float rs = 0.f;
+          score<DV>(u, sh.x3, sh.x4, rv, 32 * J, 32 * I);
+          float rs = 0.f, x[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int j = 32 * J + acc_row(e, h);
-            const float x = j < ii ? s[e] * u[e] : 0.f;
-            rs += x;
-            const float cs = lane_group_sum<32>(x);
-            if (c == 0) sh.ecol[tile][acc_row(e, h)] = cs;
+            x[e] = 32 * J + acc_row(e, h) < ii ? s[e] * u[e] : 0.f;
+            rs += x[e];
           }
           rs = swap32_sum(rs);
+          const float cs = rows_to_lanes(x, lane);
+          if (c < 16) sh.ecol[tile][acc_row(c, h)] = cs;
           if (h == 0) sh.erow[tile][c] = rs;
         }
       }
       // what the piece's start gives: Q M, rows scaled by what is left of it
 #pragma unroll
       for (int I = 0; I < IT; ++I) acc[I] = zero16();
+      {
+        // a step's queries are asked for a step ahead
+        constexpr int GT = 32 / O::KG, TERMS = EXTRA || O::TERMS < 2 ? O::TERMS : 2, ST = EXTRA && DK == 128 ? 1 : 2, STEPS = DK / O::KG / ST;
+        Frag q[2][IT][ST];
+        auto ask = [&](int step) {
 #pragma unroll
-      for (int g = 0; g < DK / O::KG; ++g) {
-        constexpr int GT = 32 / O::KG, TERMS = EXTRA || O::TERMS < 2 ? O::TERMS : 2;
-        typename O::Vals x;
-        Frag f[TERMS];
+          for (int I = 0; I < IT; ++I)
 #pragma unroll
-        for (int e = 0; e < O::FN; ++e) x[e] = M[g / GT][O::FN * (g % GT) + e];
-        O::split(x, f);
+            for (int g = 0; g < ST; ++g) q[step & 1][I][g] = O::template rowc<DK>(sh.x1, rc, 32 * I, step * ST + g);
+        };
+        ask(0);
 #pragma unroll
-        for (int I = 0; I < IT; ++I) {
-          const Frag q = O::template rowc<DK>(sh.x1, rc, 32 * I, g);
+        for (int step = 0; step < STEPS; ++step) {
+          if (step + 1 < STEPS) ask(step + 1);
+          sched_fence();
 #pragma unroll
-          for (int t = TERMS - 1; t >= 0; --t) acc[I] = O::mma(q, f[t], acc[I]);
+          for (int k = 0; k < ST; ++k) {
+            const int g = step * ST + k;
+            typename O::Vals x;
+            Frag f[TERMS];
+#pragma unroll
+            for (int e = 0; e < O::FN; ++e) x[e] = M[g / GT][O::FN * (g % GT) + e];
+            O::split(x, f);
+#pragma unroll
+            for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+              for (int I = 0; I < IT; ++I) acc[I] = O::mma(q[step & 1][I][k], f[t], acc[I]);
+          }
+          sched_fence();
         }
-        if (g % 2) sched_fence();
       }
 #pragma unroll
       for (int I = 0; I < IT; ++I)
@@ -274,42 +306,63 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
         for (int e = 0; e < 16; ++e) {
           const int r = 32 * I + acc_row(e, h);
           acc[I][e] *= d.gam[r];
-          if constexpr (EXTRA) {
-            const float x = lane_group_sum<32>(acc[I][e] * (float)sh.x4[O::template at<DV>(r, col)]);
-            if (c == 0) sh.dot[w][r] = x;
-          }
         }
+      if constexpr (EXTRA) {
+        float x[16 * IT];
+#pragma unroll
+        for (int I = 0; I < IT; ++I) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[16 * I + e] = acc[I][e] * O::template acc_el<DV>(sh.x4, xa, I, e);
+          sched_fence();
+        }
+        const float dot = rows_to_lanes(x, lane);
+        if (c < 16 * IT) sh.dot[w][32 * (c >> 4) + acc_row(c & 15, h)] = dot;
+      }
     }
     if (i + 1 < n && w == NW - 1) decays<P>(gnow, lane, sh.d[(i + 1) & 1], &decay);
     if constexpr (OUT) __syncthreads();
+    if (EXTRA && i + 1 < n) load(piece(i + 1), false, true);
     // the decayed values join the state; the scores meet the values as they are
     const float total = d.total;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int e = 0; e < 16; ++e) M[m][e] *= total;
+    {
+      // the values are asked for a step ahead, the keys in front of the conversions
+      constexpr int GN = P / O::KG;
+      Frag v = O::template col<DV>(sh.x3, cv, w, 0);
 #pragma unroll
-    for (int g = 0; g < P / O::KG; ++g) {
-      const Frag v = O::template col<DV>(sh.x3, cv, w, g);
-      if constexpr (OUT) {
+      for (int g = 0; g < GN; ++g) {
+        typename O::Vals x;
+        Frag f[O::TERMS], k[MT], sc[IT], vn = v;
+        const int k0 = O::col_k(g, h);
 #pragma unroll
-        for (int I = 0; I < IT; ++I)
-          if (g * O::KG < 32 * (I + 1))
-            acc[I] = O::mma(O::plain(sh.sc + (32 * I + c) * O::PS + O::col_k(g, h)), v, acc[I]);
+        for (int e = 0; e < O::FN; ++e) x[e] = d.w[k0 + e];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) k[m] = O::template col<DK>(sh.x2, ck, m, g);
+        if constexpr (OUT) {
+#pragma unroll
+          for (int I = 0; I < IT; ++I)
+            if (g * O::KG < 32 * (I + 1)) sc[I] = O::plain(sh.sc + (32 * I + c) * O::PS + k0);
+        }
+        if (g + 1 < GN) vn = O::template col<DV>(sh.x3, cv, w, g + 1);
+        sched_fence();
+#pragma unroll
+        for (int e = 0; e < O::FN; ++e) x[e] *= (float)v[e];
+        O::split(x, f);
+#pragma unroll
+        for (int t = O::TERMS - 1; t >= 0; --t)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) M[m] = O::mma(k[m], f[t], M[m]);
+        if constexpr (OUT) {
+#pragma unroll
+          for (int I = 0; I < IT; ++I)
+            if (g * O::KG < 32 * (I + 1)) acc[I] = O::mma(sc[I], v, acc[I]);
+        }
+        v = vn;
+        sched_fence();
       }
-      typename O::Vals x;
-      Frag f[O::TERMS];
-      const int k0 = O::col_k(g, h);
-#pragma unroll
-      for (int e = 0; e < O::FN; ++e) x[e] = (float)v[e] * d.w[k0 + e];
-      O::split(x, f);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const Frag k = O::template col<DK>(sh.x2, ck, m, g);
-#pragma unroll
-        for (int t = O::TERMS - 1; t >= 0; --t) M[m] = O::mma(k, f[t], M[m]);
-      }
-      sched_fence();
     }
     if constexpr (OUT) {
       // rows 32 I + 8 q + 4 h + e: the lane's offset holds 4 h, a uniform pointer walks the rest

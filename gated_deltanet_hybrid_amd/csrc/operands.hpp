@@ -25,6 +25,33 @@ __device__ __forceinline__ int own_s(int x) {  // of a uniform value
   return x;
 }
 
+// Sums of N (16 or 32) values over the 32 lanes of a half wave, lane c receiving that of v[c % N]: at every
+// step a lane hands its partner the values that the partner keeps.  (A half-row mirror pairs lane i with
+// i ^ 7; the two steps behind it add what that leaves in the quad.)
+template <int N>
+__device__ __forceinline__ float rows_to_lanes(const float (&v)[N], int lane) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if constexpr (N == 32) {
+      const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, v[i]), __builtin_bit_cast(unsigned, v[i + 16]),
+                                                      false, false);
+      x[i] = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+    } else {
+      x[i] = v[i];
+    }
+  }
+  const bool b3 = lane & 8, b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = (b3 ? x[i + 8] : x[i]) + dpp_f<0x128>(b3 ? x[i] : x[i + 8]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = (b2 ? x[i + 4] : x[i]) + dpp_f<0x141>(b2 ? x[i] : x[i + 4]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x[i] = (b1 ? x[i + 2] : x[i]) + dpp_f<0x4E>(b1 ? x[i] : x[i + 2]);
+  x[0] = (b0 ? x[1] : x[0]) + dpp_f<0xB1>(b0 ? x[0] : x[1]);
+  return N == 32 ? x[0] : swap16_sum(x[0]);
+}
+
 // The operands of a product over K: `Frag` is what a lane holds of KG consecutive k.
 // bf16: one 32x32x16 instruction, 8 values a lane.  float32: four 32x32x2, slot e of the group is
 // k = 4 h + e, which is also the order in which an accumulator holds its rows.
@@ -71,6 +98,12 @@ template <> struct La<bf16> {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + (base ^ (m << 5))));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * W + (base ^ (m << 5) ^ 8)));
     return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  // element (row 32 I + acc_row(e, h), column col): the tile in the accumulators' layout
+  template <int W> __device__ __forceinline__ static int acc_base(int lane, int col) { return at<W>(4 * (lane >> 5), col); }
+  template <int W> __device__ __forceinline__ static float acc_el(const bf16* t, int base, int I, int e) {
+    const int q = e >> 2, r = e & 3, x = (W == 128 ? r << 2 : (r >> 1) << 2) | ((2 * q) & 2);
+    return (float)t[(32 * I + 8 * q + r) * W + (base ^ (x << 3))];
   }
   __device__ __forceinline__ static int col_k(int g, int h) { return g * 16 + h * 8; }  // first of 8 k
   static constexpr int FN = 8;
@@ -121,6 +154,10 @@ template <> struct La<float> {
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = t[base + (g * 8 + e) * (W + 8) + 32 * m];
     return f;
+  }
+  template <int W> __device__ __forceinline__ static int acc_base(int lane, int col) { return at<W>(4 * (lane >> 5), col); }
+  template <int W> __device__ __forceinline__ static float acc_el(const float* t, int base, int I, int e) {
+    return t[base + (32 * I + acc_row(e, 0)) * (W + 8)];
   }
   __device__ __forceinline__ static int col_k(int g, int h) { return g * 8 + h * 4; }
   static constexpr int FN = 4;
