@@ -38,11 +38,13 @@ hla_status_t check_dims(const hla_la_dims_t* d) {
 
 hla_status_t plan(const hla_la_dims_t* d, bool backward, Plan* p) {
   const int64_t rows = d->B * d->H, piece = hla::la_piece(d->dtype), pieces = (d->T + piece - 1) / piece;
-  // Two workgroups a compute unit are wanted, of at least 8 pieces each: a segment costs a state
-  // written and read twice.  The backward call's segments are 32 pieces at most, since the decays'
+  // As many workgroups are wanted as run at once: two a compute unit, three of those that own 64 columns
+  // (by their LDS).  A segment costs a state written and read twice, as much as about two pieces' tokens,
+  // and is two pieces at least.  The backward call's segments are 32 pieces at most, since the decays'
   // gradient runs a difference of sums through a segment.
-  int64_t nseg = (512 + rows - 1) / rows;
-  if (nseg > pieces / 8) nseg = pieces / 8;
+  const int64_t wanted = d->dk == 128 && d->dv == 128 ? 512 : 768;
+  int64_t nseg = wanted / rows;
+  if (nseg > pieces / 2) nseg = pieces / 2;
   if (backward && nseg < (pieces + 31) / 32) nseg = (pieces + 31) / 32;
   if (nseg > hla::kLaSlots) nseg = hla::kLaSlots;
   if (nseg < 1) nseg = 1;

@@ -418,17 +418,15 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
   }
   if constexpr (OUT) {  // tokens behind the row's length
     const int64_t t0 = (last > first ? last : first) * P, t1 = end * P < a.T ? end * P : a.T;
-    for (int64_t t = t0; t < t1; ++t) {
-      const int64_t at = ((b * a.T + t) * a.H + head) * DV + tid;
-      if (tid < DV) {
-        if (a.out_f32) static_cast<float*>(a.out)[at] = 0.f;
-        else static_cast<T*>(a.out)[at] = (T)0.f;
-      }
-      if constexpr (EXTRA) {
-        if (tid == 0) {
-          a.dot[row * a.T + t] = 0.f;
-          if constexpr (EXTRA > 1) a.esum[row * a.T + t] = 0.f;
-        }
+    for (int64_t t = t0 + tid / DV; t < t1; t += NT / DV) {
+      const int64_t at = ((b * a.T + t) * a.H + head) * DV + tid % DV;
+      if (a.out_f32) static_cast<float*>(a.out)[at] = 0.f;
+      else static_cast<T*>(a.out)[at] = (T)0.f;
+    }
+    if constexpr (EXTRA) {
+      for (int64_t t = t0 + tid; t < t1; t += NT) {
+        a.dot[row * a.T + t] = 0.f;
+        if constexpr (EXTRA > 1) a.esum[row * a.T + t] = 0.f;
       }
     }
   }
@@ -458,16 +456,24 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
   const int i = (int)(id % n);
   float cur = 0.f;
   if (a.init) cur = a.init[row * n + (a.init_t ? (i % a.dv) * a.dk + i / a.dv : i)];
-  for (int s = 0; s < a.nseg; ++s) {
-    const int at = a.reverse ? a.nseg - 1 - s : s;
-    float* p = a.state + row * a.state_row + (int64_t)at * n + i;
-    if (s + 1 == a.nseg && !a.fin) {  // nothing starts behind the last one
-      *p = cur;
-      break;
-    }
-    const float own = *p;
-    *p = cur;
-    cur = cur * exp2_((float)a.decay[row * a.nseg + at]) + own;
+  const int64_t dir = a.reverse ? -(int64_t)n : n;
+  float* p = a.state + row * a.state_row + (a.reverse ? (int64_t)(a.nseg - 1) * n : 0) + i;
+  const double* d = a.decay + row * a.nseg;
+  const int count = a.fin ? a.nseg : a.nseg - 1;  // nothing starts behind the last one
+  for (int s0 = 0; s0 < a.nseg; s0 += 8) {
+    float own[8], f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k < count) {
+        own[k] = p[(s0 + k) * dir];
+        f[k] = exp2_((float)d[a.reverse ? a.nseg - 1 - s0 - k : s0 + k]);
+      }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k < a.nseg) {
+        p[(s0 + k) * dir] = cur;
+        if (s0 + k < count) cur = cur * f[k] + own[k];
+      }
   }
   if (a.fin) a.fin[row * a.fin_row + i] = cur;
 }
@@ -479,10 +485,12 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
 // front of it, E_ij the score pairs): the double sum is that of (row - column) sums from t on.  The
 // first term is X = <dM, M_P> - sum b, with <dM, M_P> a product of whole states at the segment's end
 // and X + sum c at every other piece's.  Where gamma < 2^-24, X is zero to float32 and is taken as that,
-// so that the difference's rounding does not stand in for it.  One wave runs one segment.
+// so that the difference's rounding does not stand in for it.  One workgroup runs one segment, a wave a
+// piece; only the chain of <dM, M> is one thread's.
+constexpr int kLaChain = 64;
 template <int P>
 __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.nseg;
   const int seg = blockIdx.x % a.nseg;
   const int64_t b = row / a.H;
@@ -508,36 +516,82 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
     const float* r = behind ? a.rev + (row * a.nseg + seg) * (int64_t)a.n : a.dS ? a.dS + row * a.n : nullptr;
     if (r) {
       const int w = a.w, tall = a.n / w;
-      for (int i = tid; i < a.n; i += 256) x += (double)m[i] * r[behind ? i : (i % w) * tall + i / w];
+      for (int i0 = tid; i0 < a.n; i0 += 256 * 16) {  // 4096 divides every dk dv
+        float u[16], v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int i = i0 + 256 * e;
+          u[e] = m[i];
+          v[e] = r[behind ? i : (i % w) * tall + i / w];
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x += (double)u[e] * v[e];
+      }
     }
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
-  if (lane == 0) part[tid >> 6] = x;
-  __syncthreads();
-  if (tid >= 64) return;
-  double phi = part[0] + part[1] + part[2] + part[3];
-  if (last > first && last * P < Tb) phi *= decay_of(g_at(last * P));
-  for (int64_t t = (last > first ? last : first) * P + lane; t < end * P && t < a.T; t += 64) *out(t) = 0.f;
-  for (int64_t p = last - 1; p >= first; --p) {
+  if (lane == 0) part[wave] = x;
+  // every piece's sums, then the chain of <dM, M> over the pieces, then the pieces' outputs
+  __shared__ double sum_b[kLaChain], sum_c[kLaChain], at_end[kLaChain];
+  __shared__ float gone[kLaChain];
+  auto take = [&](int64_t p, float& bb, float& cc, float& ee, float& g) {
     const int64_t t = p * P + lane;
     const bool on = lane < P && t < Tb;
-    const float bb = on ? a.b[row * a.T + t] : 0.f, cc = on ? a.c[row * a.T + t] : 0.f;
-    const float ee = on ? a.e[row * a.T + t] : 0.f, g = on ? g_at(t) : 0.f;
-    double before = bb, behind = (double)cc + ee, lg = g, sc = cc;
+    bb = on ? a.b[row * a.T + t] : 0.f;
+    cc = on ? a.c[row * a.T + t] : 0.f;
+    ee = on ? a.e[row * a.T + t] : 0.f;
+    g = on ? g_at(t) : 0.f;
+    return on;
+  };
+  double phi = 0.0;
+  for (int64_t hi = last; hi > first; hi -= kLaChain) {  // from the end, as many pieces as the chain holds
+    const int64_t lo = hi - kLaChain > first ? hi - kLaChain : first;
+    for (int64_t p = lo + wave; p < hi; p += 4) {
+      float bb, cc, ee, g;
+      take(p, bb, cc, ee, g);
+      double sb = bb, sc = cc, lg = g;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double y = __shfl_up(before, o, 64), z = __shfl_down(behind, o, 64);
-      if (lane >= o) before += y;
-      if (lane + o < 64) behind += z;
-      lg += __shfl_xor(lg, o, 64);
-      sc += __shfl_xor(sc, o, 64);
+      for (int o = 32; o >= 1; o >>= 1) {
+        sb += __shfl_xor(sb, o, 64);
+        sc += __shfl_xor(sc, o, 64);
+        lg += __shfl_xor(lg, o, 64);
+      }
+      if (lane == 0) {
+        sum_b[p - lo] = sb;
+        sum_c[p - lo] = sc;
+        gone[p - lo] = lg * kLog2e > -24.0 ? 0.f : 1.f;
+      }
     }
-    const double sb = __shfl(before, 63, 64);
-    const double X = lg * kLog2e > -24.0 ? phi - sb : 0.0;
-    if (lane < P && t < a.T) *out(t) = on && g > -104.f ? (float)(X + (before - bb) + behind) : 0.f;
-    phi = X + sc;
+    __syncthreads();
+    if (tid == 0) {
+      if (hi == last) {
+        phi = part[0] + part[1] + part[2] + part[3];
+        if (last * P < Tb) phi *= decay_of(g_at(last * P));
+      }
+      for (int64_t p = hi - 1; p >= lo; --p) {
+        const double X = gone[p - lo] != 0.f ? 0.0 : phi - sum_b[p - lo];
+        at_end[p - lo] = X;
+        phi = X + sum_c[p - lo];
+      }
+    }
+    __syncthreads();
+    for (int64_t p = lo + wave; p < hi; p += 4) {
+      float bb, cc, ee, g;
+      const bool on = take(p, bb, cc, ee, g);
+      double before = bb, behind = (double)cc + ee;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const double y = __shfl_up(before, o, 64), z = __shfl_down(behind, o, 64);
+        if (lane >= o) before += y;
+        if (lane + o < 64) behind += z;
+      }
+      const int64_t t = p * P + lane;
+      if (lane < P && t < a.T) *out(t) = on && g > -104.f ? (float)(at_end[p - lo] + (before - bb) + behind) : 0.f;
+    }
+    __syncthreads();
   }
+  for (int64_t t = (last > first ? last : first) * P + tid; t < end * P && t < a.T; t += 256) *out(t) = 0.f;
 }
 
 // The gradient of one decay for each head: the sum over its rows' tokens, in a fixed order.
