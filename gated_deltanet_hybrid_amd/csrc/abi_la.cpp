@@ -221,30 +221,27 @@ hla_status_t hla_la_prefill_backward(const hla_la_dims_t* d, const void* q, cons
     s.out = shared ? f(p.dq) : dq;
     s.out_f32 = shared;
     s.dot = f(p.c);
-    s.esum = f(p.e);
     if ((e = hla::launch_la_sweep(s, d->dtype, d->dv, d->dk, false, false, stream)) != hipSuccess) return status(e);
   }
-  {  // dk_t = G_t v_t
-    hla::LaSweep s = base;
-    s.x1 = rv; s.x2 = rdo; s.x3 = rq; s.x4 = rk;
-    s.init = many ? rev : dS_final;
-    s.init_row = many ? rev_row : p.n;
-    s.init_t = !many;
-    s.out = shared ? f(p.dk) : dk;
-    s.out_f32 = shared;
-    s.dot = f(p.b);
-    if ((e = hla::launch_la_sweep(s, d->dtype, d->dv, d->dk, false, true, stream)) != hipSuccess) return status(e);
-  }
-  {  // dv_t = G_t^T k_t
-    hla::LaSweep s = base;
-    s.x1 = rk; s.x2 = rq; s.x3 = rdo;
-    s.init = many ? rev : dS_final;
-    s.init_row = many ? rev_row : p.n;
-    s.init_t = many;
-    s.fin = dS0;
-    s.fin_row = p.n;
-    s.out = dv;
-    if ((e = hla::launch_la_sweep(s, d->dtype, d->dk, d->dv, false, true, stream)) != hipSuccess) return status(e);
+  {  // dk_t = G_t v_t, dv_t = G_t^T k_t
+    hla::LaReverse r{};
+    r.q = q; r.k = k; r.v = v; r.dO = dO;
+    r.g = log_decay;
+    r.lens = lens;
+    r.init = many ? rev : dS_final;
+    r.init_row = many ? rev_row : p.n;
+    r.init_t = !many;
+    r.dk = shared ? f(p.dk) : dk;
+    r.dv = dv;
+    r.dS0 = dS0;
+    r.dot = f(p.b);
+    r.esum = f(p.e);
+    r.B = d->B; r.T = d->T; r.H = d->H; r.Hk = d->Hk; r.ld_T = d->ld_T;
+    r.per_head = d->decay_per_head;
+    r.nseg = p.nseg;
+    r.seg_pieces = p.seg_pieces;
+    r.k_f32 = shared;
+    if ((e = hla::launch_la_reverse(r, d->dtype, d->dk, d->dv, stream)) != hipSuccess) return status(e);
   }
   hla::LaDecay c{};
   c.g = log_decay;

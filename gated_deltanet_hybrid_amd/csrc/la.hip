@@ -8,8 +8,8 @@
 // The gradients are the same recurrence with the roles changed.  With G_t = dL/dM_t (o_t included),
 // G_t = exp(g_{t+1}) G_{t+1} + q_t do_t^T, and
 //     dq_t = M_t do_t       roles (do, v, k), state M^T, forward
-//     dv_t = G_t^T k_t      roles (k, q, do), state G, reversed
 //     dk_t = G_t v_t        roles (v, do, q), state G^T, reversed
+//     dv_t = G_t^T k_t      roles (k, q, do), state G, reversed, with dk in one kernel
 //     exp(g_t) dL/d(exp g_t) = exp(g_t) <G_t, M_{t-1}>, see la_decay_kernel.
 //
 // The state lives in the accumulators of the matrix cores: wave w owns columns [32 w, 32 w + 32) and
@@ -64,7 +64,7 @@ __device__ __forceinline__ void decays(float g, int lane, Decays<P>& d, double* 
   *sum += last;
 }
 
-template <class T, int DK, int DV, bool OUT, int EXTRA> struct LaShared {
+template <class T, int DK, int DV, bool OUT, bool EXTRA> struct LaShared {
   using O = La<T>;
   alignas(16) T x1[OUT ? O::template size<DK>() : 8];
   alignas(16) T x2[O::template size<DK>()];
@@ -73,7 +73,6 @@ template <class T, int DK, int DV, bool OUT, int EXTRA> struct LaShared {
   alignas(16) T sc[OUT ? O::P * O::PS : 8];
   Decays<O::P> d[2];
   float dot[EXTRA ? DV / 32 : 1][O::P];
-  float erow[EXTRA > 1 ? 3 : 1][32], ecol[EXTRA > 1 ? 3 : 1][32];
 };
 
 // s += rows [a0, a0 + 32) of `a` times rows [b0, b0 + 32) of `b`, W columns; eight reads ahead of their four products.
@@ -96,15 +95,225 @@ __device__ __forceinline__ void score(f32x16& s, const T* a, const T* b, int bas
   }
 }
 
-// One workgroup of DV / 32 waves runs one segment of one row.  OUT: outputs from the state in front
-// of the segment; else the segment's state (from init, or zero).  EXTRA: the products with x4 that
-// the decays' gradient takes.
-template <class T, int DK, int DV, bool OUT, bool REV, int EXTRA>
-__global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_sweep_kernel(LaSweep a) {
+// A 32 x 32 tile of scores, transposed -- rows j = 32 J + acc_row(e, h), column i = 32 I + c -- so that a
+// lane writes runs of one row.  Tile 0: I = J = 0, 1: I = 1, J = 0, 2: I = J = 1.
+__device__ __forceinline__ int tile_i(int tile) { return tile ? 1 : 0; }
+__device__ __forceinline__ int tile_j(int tile) { return tile == 2 ? 1 : 0; }
+
+// D_ij.  Selects and no branches: every sum is read, and what lies behind i becomes 2^-inf.
+template <int P>
+__device__ __forceinline__ void tile_decays(float (&D)[16], const Decays<P>& d, int tile, int c, int h) {
+  const int ii = 32 * tile_i(tile) + c, last = ii - 32 * tile_j(tile) - 4 * h;
+  const double lgi = d.lg[ii];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float x = (float)(lgi - d.lg[32 * tile_j(tile) + acc_row(e, h)]);
+    D[e] = exp2_(acc_row(e, 0) <= last ? x : -INFINITY);
+  }
+}
+
+// s D into the piece's scores (rows i, columns j); what lies behind i is zero whatever s is.
+template <class T>
+__device__ __forceinline__ void put_scores(T* sc, const f32x16& s, const float (&D)[16], int tile, int c, int h) {
+  const int ii = 32 * tile_i(tile) + c, last = ii - 32 * tile_j(tile) - 4 * h;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    T* to = sc + ii * La<T>::PS + 32 * tile_j(tile) + q * 8 + h * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[e] = (T)(acc_row(4 * q + e, 0) <= last ? s[4 * q + e] * D[4 * q + e] : 0.f);
+  }
+}
+
+// What the piece's start gives: acc = X1 M (the first MT tiles of M), the rows scaled by what is left of
+// it.  The rows of a step (ST groups) are asked for a step ahead.
+template <int W, int TERMS, int ST, class T, int NM, int IT>
+__device__ __forceinline__ void inter(f32x16 (&acc)[IT], const f32x16 (&M)[NM], const T* x1, const Decays<La<T>::P>& d,
+                                      int base, int h) {
+  using O = La<T>;
+  constexpr int GT = 32 / O::KG, STEPS = W / O::KG / ST;
+#pragma unroll
+  for (int I = 0; I < IT; ++I) acc[I] = zero16();
+  typename O::Frag q[2][IT][ST];
+  auto ask = [&](int step) {
+#pragma unroll
+    for (int I = 0; I < IT; ++I)
+#pragma unroll
+      for (int g = 0; g < ST; ++g) q[step & 1][I][g] = O::template rowc<W>(x1, base, 32 * I, step * ST + g);
+  };
+  ask(0);
+#pragma unroll
+  for (int step = 0; step < STEPS; ++step) {
+    if (step + 1 < STEPS) ask(step + 1);
+    sched_fence();
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+      const int g = step * ST + k;
+      typename O::Vals x;
+      typename O::Frag f[TERMS];
+#pragma unroll
+      for (int e = 0; e < O::FN; ++e) x[e] = M[g / GT][O::FN * (g % GT) + e];
+      O::split(x, f);
+#pragma unroll
+      for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+        for (int I = 0; I < IT; ++I) acc[I] = O::mma(q[step & 1][I][k], f[t], acc[I]);
+    }
+    sched_fence();
+  }
+#pragma unroll
+  for (int I = 0; I < IT; ++I)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[I][e] *= d.gam[32 * I + acc_row(e, h)];
+}
+
+// to[row] = sum over the wave's 32 columns of acc times the tile x4, for every row of the piece.
+template <int W, class T, int IT>
+__device__ __forceinline__ void row_dots(const f32x16 (&acc)[IT], const T* x4, float* to, int base, int lane, int c, int h) {
+  float x[16 * IT];
+#pragma unroll
+  for (int I = 0; I < IT; ++I) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[16 * I + e] = acc[I][e] * La<T>::template acc_el<W>(x4, base, I, e);
+    sched_fence();
+  }
+  const float dot = rows_to_lanes(x, lane);
+  if (c < 16 * IT) to[32 * (c >> 4) + acc_row(c & 15, h)] = dot;
+}
+
+// The piece joins the state: M = total M + X2^T (w o X3), and with OUT the scores meet the values, acc +=
+// scores X3, for columns [32 w, 32 w + 32) of X3.  The values are asked for a step ahead, the keys in
+// front of the conversions.
+template <int WK, int WV, bool OUT, class T, int NM, int IT>
+__device__ __forceinline__ void absorb(f32x16 (&M)[NM], f32x16 (&acc)[IT], const T* x2, const T* x3, const T* scores,
+                                       const Decays<La<T>::P>& d, int ck, int cv, int w, int c, int h) {
   using O = La<T>;
   using Frag = typename O::Frag;
-  constexpr int P = O::P, NT = DV * 2, NW = DV / 32, MT = DK / 32, IT = P / 32, V = 16 / (int)sizeof(T);
-  constexpr int N1 = P * DK / V / NT, N3 = P * DV / V / NT;  // 16-byte pieces a thread moves of each tile
+  constexpr int GN = O::P / O::KG, MT = WK / 32;
+  const float total = d.total;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) M[m][e] *= total;
+  Frag v = O::template col<WV>(x3, cv, w, 0);
+#pragma unroll
+  for (int g = 0; g < GN; ++g) {
+    typename O::Vals x;
+    Frag f[O::TERMS], k[MT], sc[IT], vn = v;
+    const int k0 = O::col_k(g, h);
+#pragma unroll
+    for (int e = 0; e < O::FN; ++e) x[e] = d.w[k0 + e];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) k[m] = O::template col<WK>(x2, ck, m, g);
+    if constexpr (OUT) {
+#pragma unroll
+      for (int I = 0; I < IT; ++I)
+        if (g * O::KG < 32 * (I + 1)) sc[I] = O::plain(scores + (32 * I + c) * O::PS + k0);
+    }
+    if (g + 1 < GN) vn = O::template col<WV>(x3, cv, w, g + 1);
+    sched_fence();
+#pragma unroll
+    for (int e = 0; e < O::FN; ++e) x[e] *= (float)v[e];
+    O::split(x, f);
+#pragma unroll
+    for (int t = O::TERMS - 1; t >= 0; --t)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) M[m] = O::mma(k[m], f[t], M[m]);
+    if constexpr (OUT) {
+#pragma unroll
+      for (int I = 0; I < IT; ++I)
+        if (g * O::KG < 32 * (I + 1)) acc[I] = O::mma(sc[I], v, acc[I]);
+    }
+    v = vn;
+    sched_fence();
+  }
+}
+
+// A piece's outputs, columns W wide, 32 of them a wave.  `out`: the piece's first token of this head;
+// `rows` tokens lie in the tensor and `live` in the sequence (the rest are zero).  Rows 32 I + 8 q + 4 h + e:
+// the lane's offset holds 4 h, a uniform pointer walks the rest.
+template <bool REV, int P, class T, int IT>
+__device__ __forceinline__ void put_out(f32x16 (&acc)[IT], void* out, bool f32, int stride, int rows, int live, int col, int h) {
+  // whether row 32 I + acc_row(e, h) is one of the first n tokens, by one bound a lane
+  auto among = [](int n, int h) { return REV ? P - 4 * h - n : n - 4 * h; };
+  auto in = [](int I, int e, int bound) { return REV ? 32 * I + acc_row(e, 0) >= bound : 32 * I + acc_row(e, 0) < bound; };
+  const unsigned off = (unsigned)((REV ? 4 - 4 * h : 4 * h) * stride + col);
+  if (live < P) {
+    const int bound = among(live, h);
+#pragma unroll
+    for (int I = 0; I < IT; ++I)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[I][e] = in(I, e, bound) ? acc[I][e] : 0.f;
+  }
+  const int bound = among(rows, h);
+  auto put = [&](auto* to, auto whole) {
+    using TO = std::remove_pointer_t<decltype(to)>;
+    TO* at = to + (REV ? (int64_t)(P - 5) * stride : 0);
+#pragma unroll
+    for (int I = 0; I < IT; ++I)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (decltype(whole)::value || in(I, e, bound)) at[off] = (TO)acc[I][e];
+        const int step = e % 4 == 3 ? 5 : 1;
+        at += REV ? -(step * stride) : step * stride;
+      }
+  };
+  if (rows == P) {
+    if (f32) put(static_cast<float*>(out), std::true_type{});
+    else put(static_cast<T*>(out), std::true_type{});
+  } else {
+    if (f32) put(static_cast<float*>(out), std::false_type{});
+    else put(static_cast<T*>(out), std::false_type{});
+  }
+}
+
+// 16-byte pieces that a thread of NT moves of a P x W tile.  It moves the same columns of every RS-th row,
+// so its addresses are one 32-bit offset (64 rows of heads * width elements stay below 2^31 bytes: the host
+// checks) from uniform pointers.
+template <int NT, int P, int W, bool REV, class T> struct Mover {
+  static constexpr int V = 16 / (int)sizeof(T), CPR = W / V, RS = NT / CPR, ALL = P * CPR, N = (ALL + NT - 1) / NT;
+  static_assert(NT % CPR == 0, "a thread keeps its columns");
+  __device__ __forceinline__ static void load(const T* base, int heads, int64_t p, int64_t Tb, int tid, u32x4* regs) {
+    const int stride = own_s(heads * W);
+    const int r0 = own(tid) / CPR, t0 = REV ? P - 1 - r0 : r0;
+    const unsigned col = (unsigned)(tid % CPR * V);
+    const T* at = base + p * P * stride;
+    const int64_t left = Tb - p * P;
+    if (left >= P) {
+      const unsigned off = (unsigned)(t0 * stride) + col;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const T* u = REV ? at : at + (int64_t)(RS * i) * stride;
+        const unsigned o = REV ? off - (unsigned)(RS * i * stride) : off;
+        if (ALL % NT == 0 || i + 1 < N || r0 + RS * i < P) regs[i] = *reinterpret_cast<const u32x4*>(u + o);
+      }
+    } else {  // the last piece: rows behind the sequence are read from its first token and become zero
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int t = REV ? t0 - RS * i : t0 + RS * i;
+        const bool in = t >= 0 && t < left;
+        const u32x4 x = *reinterpret_cast<const u32x4*>(at + (unsigned)((in ? t : 0) * stride) + col);
+        regs[i] = in ? x : u32x4{0, 0, 0, 0};
+      }
+    }
+  }
+  __device__ __forceinline__ static void store(T* tile, int tid, const u32x4* regs) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = i * NT + tid;
+      if (ALL % NT == 0 || id < ALL) *reinterpret_cast<u32x4*>(tile + La<T>::template at<W>(id / CPR, id % CPR * V)) = regs[i];
+    }
+  }
+};
+
+template <int IT> constexpr int kTiles = IT == 2 ? 3 : 1;  // score tiles on and below the diagonal
+
+// One workgroup of DV / 32 waves runs one segment of one row.  OUT: outputs from the state in front
+// of the segment; else the segment's state (from init, or zero).  EXTRA: the products with x4 that
+// the decays' gradient takes (`dot`).
+template <class T, int DK, int DV, bool OUT, bool REV, bool EXTRA>
+__global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_sweep_kernel(LaSweep a) {
+  using O = La<T>;
+  constexpr int P = O::P, NT = DV * 2, NW = DV / 32, MT = DK / 32, IT = P / 32;
   __shared__ LaShared<T, DK, DV, OUT, EXTRA> sh;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h0 = lane >> 5, c0 = lane & 31;
   const int64_t row = blockIdx.x / a.nseg;
@@ -140,48 +349,22 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
     const int64_t t = token(p, lane) + (REV ? 1 : 0);
     return t < Tb ? (a.per_head ? gp[0] : gp[t * a.H]) : 0.f;
   };
-  u32x4 r1[OUT ? N1 : 1], r2[N1], r3[N3], r4[EXTRA ? N3 : 1];
-  // A thread moves the same columns of every RS-th row of a tile, so its addresses are one 32-bit offset
-  // (64 rows of heads * width elements stay below 2^31 bytes: the host checks) from uniform pointers.
-  auto load_tile = [&](const T* base, int heads, auto width, int64_t p, u32x4* regs) {
-    constexpr int W = decltype(width)::value, CPR = W / V, RS = NT / CPR, N = P * W / V / NT;
-    const int stride = own_s(heads * W);
-    const int r0 = own(tid) / CPR, t0 = REV ? P - 1 - r0 : r0;
-    const unsigned off = (unsigned)(t0 * stride + tid % CPR * V);
-    const T* at = base + p * P * stride;
-    const int64_t left = Tb - p * P;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int step = REV ? -RS * i : RS * i;
-      const T* u = at + (int64_t)(REV ? 0 : step) * stride;
-      const unsigned o = REV ? off - (unsigned)(RS * i * stride) : off;
-      if (left >= P) regs[i] = *reinterpret_cast<const u32x4*>(u + o);
-      else regs[i] = t0 + step < left ? *reinterpret_cast<const u32x4*>(u + o) : u32x4{0, 0, 0, 0};
-    }
-  };
-  // x1 and x4 are done with sooner than the others, and their next tiles are asked for then (EXTRA:
-  // registers are short) or with the others
+  using ML1 = Mover<NT, P, DK, REV, T>;
+  using ML3 = Mover<NT, P, DV, REV, T>;
+  u32x4 r1[OUT ? ML1::N : 1], r2[ML1::N], r3[ML3::N], r4[EXTRA ? ML3::N : 1];
+  // x1 and x4 are done with sooner than the others; their next tiles are asked for then (back), since
+  // registers are short until then
   auto load = [&](int64_t p, bool front, bool back) {
-    using WK = std::integral_constant<int, DK>;
-    using WV = std::integral_constant<int, DV>;
-    if constexpr (OUT) if (back) load_tile(p1, a.x1.heads, WK{}, p, r1);
-    if (front) load_tile(p2, a.x2.heads, WK{}, p, r2);
-    if (front) load_tile(p3, a.x3.heads, WV{}, p, r3);
-    if constexpr (EXTRA) if (back) load_tile(p4, a.x4.heads, WV{}, p, r4);
+    if constexpr (OUT) if (back) ML1::load(p1, a.x1.heads, p, Tb, tid, r1);
+    if (front) ML1::load(p2, a.x2.heads, p, Tb, tid, r2);
+    if (front) ML3::load(p3, a.x3.heads, p, Tb, tid, r3);
+    if constexpr (EXTRA) if (back) ML3::load(p4, a.x4.heads, p, Tb, tid, r4);
   };
   auto store = [&]() {
-#pragma unroll
-    for (int i = 0; i < N1; ++i) {
-      const int id = i * NT + tid, at = O::template at<DK>(id / (DK / V), id % (DK / V) * V);
-      if constexpr (OUT) *reinterpret_cast<u32x4*>(sh.x1 + at) = r1[i];
-      *reinterpret_cast<u32x4*>(sh.x2 + at) = r2[i];
-    }
-#pragma unroll
-    for (int i = 0; i < N3; ++i) {
-      const int id = i * NT + tid, at = O::template at<DV>(id / (DV / V), id % (DV / V) * V);
-      *reinterpret_cast<u32x4*>(sh.x3 + at) = r3[i];
-      if constexpr (EXTRA) *reinterpret_cast<u32x4*>(sh.x4 + at) = r4[i];
-    }
+    if constexpr (OUT) ML1::store(sh.x1, tid, r1);
+    ML1::store(sh.x2, tid, r2);
+    ML3::store(sh.x3, tid, r3);
+    if constexpr (EXTRA) ML3::store(sh.x4, tid, r4);
   };
   auto piece = [&](int64_t i) { return REV ? last - 1 - i : first + i; };
 
@@ -201,10 +384,10 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
     for (int m = 0; m < MT; ++m) M[m] = zero16();
   }
 
-  const int rk0 = O::template row_base<DK>(lane), rv0 = O::template row_base<DV>(lane);
+  const int rk0 = O::template row_base<DK>(lane);
   const int rc0 = O::template rowc_base<DK>(lane), ck0 = O::template col_base<DK>(lane), cv0 = O::template col_base<DV>(lane),
             xa0 = O::template acc_base<DV>(lane, col);
-  (void)rk0; (void)rv0; (void)rc0;
+  (void)rk0; (void)rc0;
   double decay = 0.0;
   float gnext = 0.f;  // two pieces ahead and in front of the tiles: memory answers in order, and the sums
   if (n) {            // of the next piece must not wait for its tiles
@@ -219,182 +402,35 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
     const int64_t p = piece(i);
     const Decays<P>& d = sh.d[i & 1];
     const int h = own(h0), c = own(c0);  // row indices are formed again in every piece, not kept
-    const int rk = own(rk0), rv = own(rv0), rc = own(rc0), ck = own(ck0), cv = own(cv0), xa = own(xa0);
-    (void)rk; (void)rv; (void)rc; (void)xa;
+    const int rk = own(rk0), rc = own(rc0), ck = own(ck0), cv = own(cv0), xa = own(xa0);
+    (void)rk; (void)rc; (void)xa;
     store();
     __syncthreads();
     float gnow;  // a copy made here, where the tiles have arrived anyway, frees gnext for the next load
     asm volatile("v_mov_b32 %0, %1" : "=v"(gnow) : "v"(gnext));
     if (i + 2 < n && w == NW - 1) gnext = load_g(piece(i + 2));
-    if (i + 1 < n) load(piece(i + 1), true, !EXTRA);
+    if (i + 1 < n) load(piece(i + 1), true, false);
     f32x16 acc[IT];
     if constexpr (OUT) {
-      // decayed scores, transposed: rows j, column i, so that a lane writes runs of one row
-      constexpr int TILES = IT == 2 ? 3 : 1;
-      for (int tile = w; tile < TILES; tile += NW) {
-        const int I = tile ? 1 : 0, J = tile == 2 ? 1 : 0;
+      for (int tile = w; tile < kTiles<IT>; tile += NW) {
         f32x16 s = zero16();
-        score<DK>(s, sh.x2, sh.x1, rk, 32 * J, 32 * I);
-        const int ii = 32 * I + c;
-        const double lgi = d.lg[ii];
-        // selects and no branches: every sum is read, and what lies behind i becomes 2^-inf
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = 32 * J + acc_row(e, h);
-          const float x = (float)(lgi - d.lg[j]);
-          s[e] = (j <= ii ? s[e] : 0.f) * exp2_(j <= ii ? x : -INFINITY);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          T* to = sh.sc + ii * O::PS + 32 * J + q * 8 + h * 4;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[e] = (T)s[4 * q + e];
-        }
-        if constexpr (EXTRA > 1) {
-          // E_ij = D_ij (x1_i . x2_j)(x4_i . x3_j) for j < i: its sums over each row and each column
-          f32x16 u = zero16();
-          score<DV>(u, sh.x3, sh.x4, rv, 32 * J, 32 * I);
-          float rs = 0.f, x[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            x[e] = 32 * J + acc_row(e, h) < ii ? s[e] * u[e] : 0.f;
-            rs += x[e];
-          }
-          rs = swap32_sum(rs);
-          const float cs = rows_to_lanes(x, lane);
-          if (c < 16) sh.ecol[tile][acc_row(c, h)] = cs;
-          if (h == 0) sh.erow[tile][c] = rs;
-        }
+        float D[16];
+        score<DK>(s, sh.x2, sh.x1, rk, 32 * tile_j(tile), 32 * tile_i(tile));
+        tile_decays(D, d, tile, c, h);
+        put_scores(sh.sc, s, D, tile, c, h);
       }
-      // what the piece's start gives: Q M, rows scaled by what is left of it
-#pragma unroll
-      for (int I = 0; I < IT; ++I) acc[I] = zero16();
-      {
-        // a step's queries are asked for a step ahead
-        constexpr int GT = 32 / O::KG, TERMS = EXTRA || O::TERMS < 2 ? O::TERMS : 2, ST = EXTRA && DK == 128 ? 1 : 2, STEPS = DK / O::KG / ST;
-        Frag q[2][IT][ST];
-        auto ask = [&](int step) {
-#pragma unroll
-          for (int I = 0; I < IT; ++I)
-#pragma unroll
-            for (int g = 0; g < ST; ++g) q[step & 1][I][g] = O::template rowc<DK>(sh.x1, rc, 32 * I, step * ST + g);
-        };
-        ask(0);
-#pragma unroll
-        for (int step = 0; step < STEPS; ++step) {
-          if (step + 1 < STEPS) ask(step + 1);
-          sched_fence();
-#pragma unroll
-          for (int k = 0; k < ST; ++k) {
-            const int g = step * ST + k;
-            typename O::Vals x;
-            Frag f[TERMS];
-#pragma unroll
-            for (int e = 0; e < O::FN; ++e) x[e] = M[g / GT][O::FN * (g % GT) + e];
-            O::split(x, f);
-#pragma unroll
-            for (int t = TERMS - 1; t >= 0; --t)
-#pragma unroll
-              for (int I = 0; I < IT; ++I) acc[I] = O::mma(q[step & 1][I][k], f[t], acc[I]);
-          }
-          sched_fence();
-        }
-      }
-#pragma unroll
-      for (int I = 0; I < IT; ++I)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int r = 32 * I + acc_row(e, h);
-          acc[I][e] *= d.gam[r];
-        }
-      if constexpr (EXTRA) {
-        float x[16 * IT];
-#pragma unroll
-        for (int I = 0; I < IT; ++I) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[16 * I + e] = acc[I][e] * O::template acc_el<DV>(sh.x4, xa, I, e);
-          sched_fence();
-        }
-        const float dot = rows_to_lanes(x, lane);
-        if (c < 16 * IT) sh.dot[w][32 * (c >> 4) + acc_row(c & 15, h)] = dot;
-      }
+      inter<DK, EXTRA || O::TERMS < 2 ? O::TERMS : 2, 1>(acc, M, sh.x1, d, rc, h);
+      if constexpr (EXTRA) row_dots<DV>(acc, sh.x4, sh.dot[w], xa, lane, c, h);
     }
     if (i + 1 < n && w == NW - 1) decays<P>(gnow, lane, sh.d[(i + 1) & 1], &decay);
     if constexpr (OUT) __syncthreads();
-    if (EXTRA && i + 1 < n) load(piece(i + 1), false, true);
-    // the decayed values join the state; the scores meet the values as they are
-    const float total = d.total;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) M[m][e] *= total;
-    {
-      // the values are asked for a step ahead, the keys in front of the conversions
-      constexpr int GN = P / O::KG;
-      Frag v = O::template col<DV>(sh.x3, cv, w, 0);
-#pragma unroll
-      for (int g = 0; g < GN; ++g) {
-        typename O::Vals x;
-        Frag f[O::TERMS], k[MT], sc[IT], vn = v;
-        const int k0 = O::col_k(g, h);
-#pragma unroll
-        for (int e = 0; e < O::FN; ++e) x[e] = d.w[k0 + e];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) k[m] = O::template col<DK>(sh.x2, ck, m, g);
-        if constexpr (OUT) {
-#pragma unroll
-          for (int I = 0; I < IT; ++I)
-            if (g * O::KG < 32 * (I + 1)) sc[I] = O::plain(sh.sc + (32 * I + c) * O::PS + k0);
-        }
-        if (g + 1 < GN) vn = O::template col<DV>(sh.x3, cv, w, g + 1);
-        sched_fence();
-#pragma unroll
-        for (int e = 0; e < O::FN; ++e) x[e] *= (float)v[e];
-        O::split(x, f);
-#pragma unroll
-        for (int t = O::TERMS - 1; t >= 0; --t)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) M[m] = O::mma(k[m], f[t], M[m]);
-        if constexpr (OUT) {
-#pragma unroll
-          for (int I = 0; I < IT; ++I)
-            if (g * O::KG < 32 * (I + 1)) acc[I] = O::mma(sc[I], v, acc[I]);
-        }
-        v = vn;
-        sched_fence();
-      }
-    }
+    if (OUT && i + 1 < n) load(piece(i + 1), false, true);
+    absorb<DK, DV, OUT>(M, acc, sh.x2, sh.x3, sh.sc, d, ck, cv, w, c, h);
     if constexpr (OUT) {
-      // rows 32 I + 8 q + 4 h + e: the lane's offset holds 4 h, a uniform pointer walks the rest
-      const int stride = own_s((int)a.H * DV);
       const int rows = (int)(a.T - p * P < P ? a.T - p * P : P), live_rows = (int)(Tb - p * P < P ? Tb - p * P : P);
-      const unsigned off = (unsigned)((REV ? 4 - 4 * h : 4 * h) * stride + col);
       const int64_t o0 = ((b * a.T + p * P) * a.H + head) * DV;
-      if (live_rows < P) {
-#pragma unroll
-        for (int I = 0; I < IT; ++I)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[I][e] = row_of(32 * I + acc_row(e, h)) < live_rows ? acc[I][e] : 0.f;
-      }
-      auto put = [&](auto* out, auto whole) {
-        using TO = std::remove_pointer_t<decltype(out)>;
-        TO* at = out + (REV ? (int64_t)(P - 5) * stride : 0);
-#pragma unroll
-        for (int I = 0; I < IT; ++I)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (decltype(whole)::value || row_of(32 * I + acc_row(e, h)) < rows) at[off] = (TO)acc[I][e];
-            const int step = e % 4 == 3 ? 5 : 1;
-            at += REV ? -(step * stride) : step * stride;
-          }
-      };
-      if (rows == P) {
-        if (a.out_f32) put(static_cast<float*>(a.out) + o0, std::true_type{});
-        else put(static_cast<T*>(a.out) + o0, std::true_type{});
-      } else {
-        if (a.out_f32) put(static_cast<float*>(a.out) + o0, std::false_type{});
-        else put(static_cast<T*>(a.out) + o0, std::false_type{});
-      }
+      void* to = a.out_f32 ? (void*)(static_cast<float*>(a.out) + o0) : (void*)(static_cast<T*>(a.out) + o0);
+      put_out<REV, P, T>(acc, to, a.out_f32, own_s((int)a.H * DV), rows, live_rows, col, h);
       if constexpr (EXTRA) {
         if (tid < P) {
           const int64_t t = token(p, tid);
@@ -402,14 +438,6 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
             float x = 0.f;
             for (int q = 0; q < NW; ++q) x += sh.dot[q][tid];
             a.dot[row * a.T + t] = t < Tb ? x : 0.f;
-            if constexpr (EXTRA > 1) {
-              const int i5 = tid & 31;
-              float y;
-              if (IT == 1) y = sh.erow[0][i5] - sh.ecol[0][i5];
-              else if (tid < 32) y = sh.erow[0][i5] - sh.ecol[0][i5] - sh.ecol[1][i5];
-              else y = sh.erow[1][i5] + sh.erow[2][i5] - sh.ecol[2][i5];
-              a.esum[row * a.T + t] = t < Tb ? y : 0.f;
-            }
           }
         }
       }
@@ -423,12 +451,8 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
       if (a.out_f32) static_cast<float*>(a.out)[at] = 0.f;
       else static_cast<T*>(a.out)[at] = (T)0.f;
     }
-    if constexpr (EXTRA) {
-      for (int64_t t = t0 + tid; t < t1; t += NT) {
-        a.dot[row * a.T + t] = 0.f;
-        if constexpr (EXTRA > 1) a.esum[row * a.T + t] = 0.f;
-      }
-    }
+    if constexpr (EXTRA)
+      for (int64_t t = t0 + tid; t < t1; t += NT) a.dot[row * a.T + t] = 0.f;
   }
   float* to = nullptr;
   float last_decay = 1.f;
@@ -445,6 +469,184 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
       for (int e = 0; e < 16; ++e) to[(32 * m + acc_row(e, h0)) * DV + col] = M[m][e] * last_decay;
   }
   if (a.decay && tid == NT - 64) a.decay[row * a.nseg + seg] = decay;
+}
+
+// The reversed sweep of both gradients that meet behind a token: dk_t = G_t v_t and dv_t = G_t^T k_t.  The
+// first DK / 32 waves hold G^T [DV, DK] and give dk (32 columns each), the others G [DK, DV] and give dv; the
+// four tiles are read once for both, and with both tiles of scores at hand, E and its sums too (see
+// la_decay_kernel).  One workgroup of (DK + DV) / 32 waves a segment.
+template <class T, int DK, int DV> struct LaReverseShared {
+  using O = La<T>;
+  alignas(16) T q[O::template size<DK>()];
+  alignas(16) T k[O::template size<DK>()];
+  alignas(16) T v[O::template size<DV>()];
+  alignas(16) T o[O::template size<DV>()];
+  alignas(16) T sk[O::P * O::PS];  // scores of dk: v_i . do_j
+  alignas(16) T sv[O::P * O::PS];  // of dv: k_i . q_j
+  Decays<O::P> d[2];
+  float dot[DK / 32][O::P];
+  float erow[3][32], ecol[3][32];
+};
+
+template <class T, int DK, int DV>
+__global__ __launch_bounds__((DK + DV) * 2, 2) void la_reverse_kernel(LaReverse a) {
+  using O = La<T>;
+  constexpr int P = O::P, NT = (DK + DV) * 2, NW = NT / 64, KW = DK / 32, IT = P / 32, NM = (DK > DV ? DK : DV) / 32;
+  using MK = Mover<NT, P, DK, true, T>;
+  using MV = Mover<NT, P, DV, true, T>;
+  __shared__ LaReverseShared<T, DK, DV> sh;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h0 = lane >> 5, c0 = lane & 31;
+  const int64_t row = blockIdx.x / a.nseg;
+  const int seg = blockIdx.x % a.nseg;
+  const int64_t b = row / a.H;
+  const int head = (int)(row % a.H), hk = head / (int)(a.H / a.Hk);
+  int64_t Tb = a.T;
+  if (a.lens) {
+    Tb = a.lens[b];
+    Tb = Tb < 0 ? 0 : (Tb > a.T ? a.T : Tb);
+  }
+  const int64_t all = (a.T + P - 1) / P, live = (Tb + P - 1) / P, first = (int64_t)seg * a.seg_pieces;
+  const int64_t end = first + a.seg_pieces < all ? first + a.seg_pieces : all, last = end < live ? end : live;
+  const int64_t n = last > first ? last - first : 0;
+  const T* pq = (const T*)a.q + (b * a.ld_T * a.Hk + hk) * DK;
+  const T* pk = (const T*)a.k + (b * a.ld_T * a.Hk + hk) * DK;
+  const T* pv = (const T*)a.v + (b * a.ld_T * a.H + head) * DV;
+  const T* po = (const T*)a.dO + (b * a.T * a.H + head) * DV;
+  const float* gp = a.per_head ? a.g + head : a.g + b * a.ld_T * a.H + head;
+  auto load_g = [&](int64_t p) -> float {  // row r is token P - 1 - r of the piece and takes the decay behind it
+    if (lane >= P) return 0.f;
+    const int64_t t = p * P + P - lane;
+    return t < Tb ? (a.per_head ? gp[0] : gp[t * a.H]) : 0.f;
+  };
+  u32x4 rq[MK::N], rk[MK::N], rv[MV::N], ro[MV::N];
+  auto load = [&](int64_t p) {
+    MV::load(pv, (int)a.H, p, Tb, tid, rv);
+    MV::load(po, (int)a.H, p, Tb, tid, ro);
+    MK::load(pq, (int)a.Hk, p, Tb, tid, rq);
+    MK::load(pk, (int)a.Hk, p, Tb, tid, rk);
+  };
+  const bool is_k = w < KW;
+  const int wc = is_k ? w : w - KW, col = 32 * wc + c0;
+  f32x16 M[NM];
+#pragma unroll
+  for (int m = 0; m < NM; ++m) M[m] = zero16();
+  if (a.init) {
+    const float* s0 = a.init + row * a.init_row + (int64_t)seg * DK * DV;
+    const int tall = is_k ? DV : DK, wide = is_k ? DK : DV;  // of this wave's state
+    const bool turned = is_k == (a.init_t != 0);             // stored [DV, DK], or [DK, DV] with init_t
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int r = 32 * m + acc_row(e, h0);
+        if (32 * m < tall) M[m][e] = turned ? s0[col * tall + r] : s0[r * wide + col];
+      }
+  }
+  const int fk0 = O::template row_base<DK>(lane), fv0 = O::template row_base<DV>(lane);
+  const int rk0 = O::template rowc_base<DK>(lane), rv0 = O::template rowc_base<DV>(lane);
+  const int ck0 = O::template col_base<DK>(lane), cv0 = O::template col_base<DV>(lane);
+  const int xa0 = O::template acc_base<DK>(lane, is_k ? col : c0);
+  double decay = 0.0;
+  float gnext = 0.f;
+  if (n) {
+    if (w == NW - 1) {
+      const float g0 = load_g(last - 1);
+      if (n > 1) gnext = load_g(last - 2);
+      decays<P>(g0, lane, sh.d[0], &decay);
+    }
+    load(last - 1);
+  }
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t p = last - 1 - i;
+    const Decays<P>& d = sh.d[i & 1];
+    const int h = own(h0), c = own(c0);
+    const int ck = own(ck0), cv = own(cv0);
+    MV::store(sh.v, tid, rv);
+    MV::store(sh.o, tid, ro);
+    MK::store(sh.q, tid, rq);
+    MK::store(sh.k, tid, rk);
+    __syncthreads();
+    float gnow;
+    asm volatile("v_mov_b32 %0, %1" : "=v"(gnow) : "v"(gnext));
+    if (i + 2 < n && w == NW - 1) gnext = load_g(p - 2);
+    if (i + 1 < n) load(p - 1);
+    for (int tile = w; tile < kTiles<IT>; tile += NW) {
+      const int I = tile_i(tile), J = tile_j(tile);
+      f32x16 s = zero16(), u = zero16();
+      float D[16], x[16], rs = 0.f;
+      score<DV>(s, sh.o, sh.v, own(fv0), 32 * J, 32 * I);
+      score<DK>(u, sh.q, sh.k, own(fk0), 32 * J, 32 * I);
+      tile_decays(D, d, tile, c, h);
+      put_scores(sh.sk, s, D, tile, c, h);
+      put_scores(sh.sv, u, D, tile, c, h);
+      const int before = 32 * I + c - 32 * J - 4 * h;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = acc_row(e, 0) < before ? s[e] * D[e] * u[e] : 0.f;
+        rs += x[e];
+      }
+      rs = swap32_sum(rs);
+      const float cs = rows_to_lanes(x, lane);
+      if (c < 16) sh.ecol[tile][acc_row(c, h)] = cs;
+      if (h == 0) sh.erow[tile][c] = rs;
+    }
+    f32x16 acc[IT];
+    if (is_k) {
+      inter<DV, O::TERMS, 1>(acc, M, sh.v, d, own(rv0), h);
+      row_dots<DK>(acc, sh.k, sh.dot[w], own(xa0), lane, c, h);
+    } else {
+      inter<DK, O::TERMS < 2 ? 1 : 2, 1>(acc, M, sh.k, d, own(rk0), h);
+    }
+    if (i + 1 < n && w == NW - 1) decays<P>(gnow, lane, sh.d[(i + 1) & 1], &decay);
+    __syncthreads();
+    const int rows = (int)(a.T - p * P < P ? a.T - p * P : P), live_rows = (int)(Tb - p * P < P ? Tb - p * P : P);
+    if (is_k) {
+      absorb<DV, DK, true>(M, acc, sh.o, sh.q, sh.sk, d, cv, ck, wc, c, h);
+      const int heads = a.k_f32 ? (int)a.H : (int)a.Hk;
+      const int64_t o0 = ((b * a.T + p * P) * heads + (a.k_f32 ? head : hk)) * DK;
+      void* to = a.k_f32 ? (void*)(static_cast<float*>(a.dk) + o0) : (void*)(static_cast<T*>(a.dk) + o0);
+      put_out<true, P, T>(acc, to, a.k_f32, own_s(heads * DK), rows, live_rows, col, h);
+    } else {
+      absorb<DK, DV, true>(M, acc, sh.q, sh.o, sh.sv, d, ck, cv, wc, c, h);
+      put_out<true, P, T>(acc, static_cast<T*>(a.dv) + ((b * a.T + p * P) * a.H + head) * DV, false, own_s((int)a.H * DV), rows,
+                          live_rows, col, h);
+    }
+    if (tid < P) {
+      const int64_t t = p * P + P - 1 - tid;
+      if (t < a.T) {
+        float x = 0.f;
+        for (int k = 0; k < KW; ++k) x += sh.dot[k][tid];
+        const int i5 = tid & 31;
+        float y;  // a row of E here is the earlier token's, a column the later one's
+        if (IT == 1) y = sh.ecol[0][i5] - sh.erow[0][i5];
+        else if (tid < 32) y = sh.ecol[0][i5] + sh.ecol[1][i5] - sh.erow[0][i5];
+        else y = sh.ecol[2][i5] - sh.erow[1][i5] - sh.erow[2][i5];
+        a.dot[row * a.T + t] = t < Tb ? x : 0.f;
+        a.esum[row * a.T + t] = t < Tb ? y : 0.f;
+      }
+    }
+    __syncthreads();
+  }
+  // tokens behind the row's length
+  for (int64_t t = (last > first ? last : first) * P + tid / 64; t < end * P && t < a.T; t += NW) {
+    const int64_t at = (b * a.T + t) * (a.k_f32 ? a.H : a.Hk) + (a.k_f32 ? head : hk);
+    for (int e = lane; e < DK; e += 64) {
+      if (a.k_f32) static_cast<float*>(a.dk)[at * DK + e] = 0.f;
+      else static_cast<T*>(a.dk)[at * DK + e] = (T)0.f;
+    }
+    for (int e = lane; e < DV; e += 64) static_cast<T*>(a.dv)[((b * a.T + t) * a.H + head) * DV + e] = (T)0.f;
+    if (lane == 0) {
+      a.dot[row * a.T + t] = 0.f;
+      a.esum[row * a.T + t] = 0.f;
+    }
+  }
+  if (!is_k && a.dS0 && seg == 0) {
+    const float f = Tb > 0 ? decay_of(gp[0]) : 1.f;
+#pragma unroll
+    for (int m = 0; m < KW; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) a.dS0[row * DK * DV + (32 * m + acc_row(e, h0)) * DV + col] = M[m][e] * f;
+  }
 }
 
 // The states in front of every segment from the segments' states from zero, in place.
@@ -664,18 +866,30 @@ __global__ __launch_bounds__(256) void la_step_kernel(LaStep a) {
   }
 }
 
-template <class T, int DK, int DV, bool OUT, bool REV, int EXTRA>
+template <class T, int DK, int DV, bool OUT, bool REV, bool EXTRA>
 hipError_t sweep(const LaSweep& a, hipStream_t s) {
   static_assert(2 * sizeof(LaShared<T, DK, DV, OUT, EXTRA>) <= 160 * 1024, "two workgroups share a compute unit's LDS");
   hipLaunchKernelGGL((la_sweep_kernel<T, DK, DV, OUT, REV, EXTRA>), dim3((unsigned)(a.B * a.H * a.nseg)), dim3(DV * 2), 0, s, a);
   return hipGetLastError();
 }
 
+// the sweeps that there are: states of segments in both directions; outputs, and outputs with dots, forward
 template <class T, int DK, int DV>
 hipError_t sweep_d(const LaSweep& a, bool state_only, bool reverse, hipStream_t s) {
-  if (state_only) return reverse ? sweep<T, DK, DV, false, true, 0>(a, s) : sweep<T, DK, DV, false, false, 0>(a, s);
-  if (a.dot) return reverse ? sweep<T, DK, DV, true, true, 1>(a, s) : sweep<T, DK, DV, true, false, 2>(a, s);
-  return reverse ? sweep<T, DK, DV, true, true, 0>(a, s) : sweep<T, DK, DV, true, false, 0>(a, s);
+  if (state_only) return reverse ? sweep<T, DK, DV, false, true, false>(a, s) : sweep<T, DK, DV, false, false, false>(a, s);
+  return a.dot ? sweep<T, DK, DV, true, false, true>(a, s) : sweep<T, DK, DV, true, false, false>(a, s);
+}
+
+template <class T, int DK, int DV>
+hipError_t reverse_d(const LaReverse& a, hipStream_t s) {
+  hipLaunchKernelGGL((la_reverse_kernel<T, DK, DV>), dim3((unsigned)(a.B * a.H * a.nseg)), dim3((DK + DV) * 2), 0, s, a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t reverse_t(const LaReverse& a, int dk, int dv, hipStream_t s) {
+  if (dk == 64) return dv == 64 ? reverse_d<T, 64, 64>(a, s) : reverse_d<T, 64, 128>(a, s);
+  return dv == 64 ? reverse_d<T, 128, 64>(a, s) : reverse_d<T, 128, 128>(a, s);
 }
 
 template <class T>
@@ -702,6 +916,10 @@ int la_piece(int dtype) { return dtype == HLA_BF16 ? La<bf16>::P : La<float>::P;
 
 hipError_t launch_la_sweep(const LaSweep& a, int dtype, int dk, int dv, bool state_only, bool reverse, hipStream_t s) {
   return dtype == HLA_BF16 ? sweep_t<bf16>(a, dk, dv, state_only, reverse, s) : sweep_t<float>(a, dk, dv, state_only, reverse, s);
+}
+
+hipError_t launch_la_reverse(const LaReverse& a, int dtype, int dk, int dv, hipStream_t s) {
+  return dtype == HLA_BF16 ? reverse_t<bf16>(a, dk, dv, s) : reverse_t<float>(a, dk, dv, s);
 }
 
 hipError_t launch_la_scan(const LaScan& a, hipStream_t s) {

@@ -32,10 +32,25 @@ struct LaSweep {
   int64_t fin_row;
   void* out;             // [B, T, H, width of x3], the call's dtype or float32
   float* dot;            // [rows, T]: x4_t . (the part of out_t that comes from the piece's start), or null
-  float* esum;           // [rows, T]: see la.hip
   int64_t B, T, H;
   int32_t per_head, nseg, seg_pieces, out_f32;
   int32_t whole;         // state pass: the last segment's state is asked for too
+};
+
+// dk_t = G_t v_t and dv_t = G_t^T k_t, reversed.
+struct LaReverse {
+  const void *q, *k, *v, *dO;
+  const float* g;
+  const int32_t* lens;
+  const float* init;     // the gradient that enters segment s of row r from behind: init + r init_row + s dk dv, or null
+  int64_t init_row;
+  int32_t init_t;        // stored [dk, dv], else [dv, dk]
+  void* dk;              // [B, T, Hk, dk] of the call's dtype, or (k_f32) [B, T, H, dk] float32: every head's part
+  void* dv;              // [B, T, H, dv]
+  float* dS0;            // [rows, dk, dv] or null
+  float *dot, *esum;     // [rows, T]: see la_decay_kernel
+  int64_t B, T, H, Hk, ld_T;
+  int32_t per_head, nseg, seg_pieces, k_f32;
 };
 
 struct LaScan {
@@ -73,6 +88,7 @@ struct LaStep {
 
 int la_piece(int dtype);                       // tokens of a piece
 hipError_t launch_la_sweep(const LaSweep& a, int dtype, int dk, int dv, bool state_only, bool reverse, hipStream_t s);
+hipError_t launch_la_reverse(const LaReverse& a, int dtype, int dk, int dv, hipStream_t s);
 hipError_t launch_la_scan(const LaScan& a, hipStream_t s);
 hipError_t launch_la_decay(const LaDecay& a, hipStream_t s);
 hipError_t launch_la_head_sum(const float* x, float* y, int64_t B, int64_t H, int64_t T, hipStream_t s);
