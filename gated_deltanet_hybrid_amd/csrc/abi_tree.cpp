@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kMaxRows = ((int64_t)1 << 24) - 1;  // a launch counts its threads in 32 bits
+constexpr int64_t kMaxRows = ((int64_t)1 << 23) - 1;  // a launch counts its threads (512 a row) in 32 bits
 
 template <int A, class... P>
 bool aligned(P... p) {

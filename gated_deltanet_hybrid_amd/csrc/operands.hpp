@@ -165,4 +165,47 @@ template <> struct La<float> {
   template <int N> __device__ __forceinline__ static void split(Vals x, Frag (&f)[N]) { f[0] = x; }
 };
 
+// The same for 16 x 16 tiles: rows (or columns) lane % 16, with G = lane / 16 four quarters of k; the
+// accumulator is rows 4 G + e, column lane % 16.
+template <class T> struct La16;
+
+template <> struct La16<bf16> {  // one 16x16x32, 8 values a lane: k = 32 g + 8 G + e
+  static constexpr int KG = 32, TERMS = 3;
+  using O = La<bf16>;
+  using Frag = bf16x8;
+  __device__ __forceinline__ static f32x4 mma(Frag a, Frag b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  template <int W> __device__ __forceinline__ static int row_base(int lane) { return O::at<W>(lane & 15, (lane >> 4) * 8); }
+  template <int W> __device__ __forceinline__ static Frag row(const bf16* t, int base, int r0, int g) {
+    return O::plain(t + r0 * W + (base ^ (g << 5)));
+  }
+  template <int W> __device__ __forceinline__ static int col_base(int lane) {
+    return O::at<W>((lane >> 4) * 8 + ((lane >> 2) & 3), (lane & 3) * 4);
+  }
+  // column 16 m + lane % 16, rows k
+  template <int W> __device__ __forceinline__ static Frag col(const bf16* t, int base, int m, int g) {
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const bf16* p = t + g * 32 * W;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + (base ^ (m << 4))));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * W + (base ^ (m << 4) ^ 8)));
+    return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+
+template <> struct La16<float> {  // four 16x16x4, 4 values a lane: k = 16 g + 4 G + e
+  static constexpr int KG = 16, TERMS = 1;
+  using O = La<float>;
+  using Frag = f32x4;
+  __device__ __forceinline__ static f32x4 mma(Frag a, Frag b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+  template <int W> __device__ __forceinline__ static int row_base(int lane) { return O::at<W>(lane & 15, (lane >> 4) * 4); }
+  template <int W> __device__ __forceinline__ static Frag row(const float* t, int base, int r0, int g) {
+    return O::plain(t + base + r0 * (W + 8) + g * 16);
+  }
+};
+
 }  // namespace hla

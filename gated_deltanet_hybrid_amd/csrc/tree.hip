@@ -278,7 +278,7 @@ __global__ __launch_bounds__(256) void tree_gates_kernel(TreeArgs a, int per_blo
         }
       }
     }
-    int any = 0;
+    unsigned any = 0;
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
       const int i = 32 * I + c;
@@ -295,171 +295,172 @@ __global__ __launch_bounds__(256) void tree_gates_kernel(TreeArgs a, int per_blo
       }
       if (!((here >> (i & 63)) & 1)) g = 0.f;
       const bool keep = j < nc && ((here >> (i & 63)) & 1) && g >= a.tau;
-      any |= __any(keep);
+      const unsigned long long kept = __ballot(keep);  // lanes 0 .. 15 and 16 .. 31 are two tiles of 16 nodes
+      any |= ((kept & 0xffff ? 1u : 0u) | (kept & 0xffff0000 ? 2u : 0u)) << (2 * I);
       if (h == 0 && i < n) {
         if (a.gates_out) a.gates_out[((b * n + i) * a.H + head) * a.n_cap + j] = g;
         if (j < nc) a.gate[(row * a.n_cap + j) * n + i] = keep ? g : 0.f;
       }
     }
-    if (lane == 0 && j < nc) a.active[row * a.n_cap + j] = any;
+    if (lane == 0 && j < nc) a.active[row * a.n_cap + j] = (int)any;
   }
 }
 
-// The chain over the cached chunks, one workgroup a row.  A wave owns 32 columns of At (their z, as
-// accumulator tiles: rows the columns, column the node) or of Bc (their o).  bf16 maps go through LDS,
-// which hands them out transposed; z enters as three bf16 terms, float32 to its last bit.
-template <class T, int DK, int DV, int N>
-__global__ __launch_bounds__(256) void tree_chain_kernel(TreeArgs a) {
-  using O = La<T>;
+// The chain over the cached chunks, for NT tiles of 16 nodes of a row.  Each of the 8 waves owns tiles of 16
+// columns of At (their z, as accumulators: rows the columns, column the node) or of Bc (their o).  bf16 maps
+// go through LDS, which hands them out transposed, and z enters as three bf16 terms, float32 to its last
+// bit; float32 maps come straight from memory, every value to the one lane that multiplies it.  The next
+// chunk that a node here reads is asked for while this one is worked on.
+template <class T, int DK, int DV, int NT>
+__global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeArgs a, int groups) {
+  using O = La16<T>;
   using Frag = typename O::Frag;
   constexpr bool BF = sizeof(T) == 2;
-  constexpr int NT = (N + 31) / 32, TILES = (DK + DV) / 32, TW = (TILES + 3) / 4, GN = DK / O::KG;
-  constexpr int RZ = O::template rs<DK>(), LD = BF ? DK * (DK + DV) / 8 / 256 : 1, LF = BF ? 1 : DK / 2;
+  constexpr int N = 16 * NT, TILES = (DK + DV) / 16, AT = DK / 16, TW = (TILES + 7) / 8, GN = DK / O::KG;
+  constexpr int RZ = La<T>::template rs<DK>(), LD = BF ? DK * (DK + DV) / 8 / 512 : 1;
   __shared__ alignas(16) T at[BF ? DK * DK : 8], bt[BF ? DK * DV : 8];
   __shared__ alignas(16) T zs[O::TERMS][N * RZ];
   __shared__ unsigned char act[kTreeSlots];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, c = lane & 31;
-  const int64_t row = blockIdx.x, b = row / a.H;
-  const int head = (int)(row % a.H), n = a.n;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, G = lane >> 4, c = lane & 15;
+  const int64_t row = blockIdx.x / groups, b = row / a.H;
+  const int head = (int)(row % a.H), n = a.n, n0 = (int)(blockIdx.x % groups) * N;
   int nc = a.n_cache[b];
   nc = nc < 0 ? 0 : (nc > a.n_cap ? a.n_cap : nc);
-  for (int j = tid; j < nc; j += 256) act[j] = (unsigned char)a.active[row * a.n_cap + j];
+  const unsigned mine = ((1u << NT) - 1) << (n0 / 16);
+  for (int j = tid; j < nc; j += 512) act[j] = (unsigned char)((a.active[row * a.n_cap + j] & mine) >> (n0 / 16));
   __syncthreads();
   auto next = [&](int j) {
     --j;
     while (j >= 0 && !act[j]) --j;
     return j;
   };
+  int j = next(nc);
+  if (j < 0) return;  // no node here reads a chunk: o is the live part
   const T* Ac = static_cast<const T*>(a.At_cache) + row * a.n_cap * DK * DK;
   const T* Bc = static_cast<const T*>(a.Bc_cache) + row * a.n_cap * DK * DV;
   u32x4 raw[LD];
-  float rawf[TW][LF];
+  Frag m[BF ? 1 : TW][GN];
   float gn[NT];
-  auto load = [&](int j) {
-    if constexpr (BF) {
+  auto load_map = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < LD; ++i) {
-        const int id = i * 256 + tid;
-        const T* p = id < DK * DK / 8 ? Ac + (int64_t)j * DK * DK + id * 8 : Bc + (int64_t)j * DK * DV + (id - DK * DK / 8) * 8;
-        raw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < TW; ++i) {
-        const int t = w + 4 * i;
-        if (t >= TILES) continue;
-        const bool isA = t < DK / 32;
-        const int W = isA ? DK : DV;
-        const T* p = isA ? Ac + (int64_t)j * DK * DK + 32 * t + c : Bc + (int64_t)j * DK * DV + 32 * t - DK + c;
-#pragma unroll
-        for (int k = 0; k < LF; ++k) rawf[i][k] = (float)p[((k >> 2) * 8 + h * 4 + (k & 3)) * W];
-      }
+    for (int i = 0; i < LD; ++i) {
+      const int id = i * 512 + tid;
+      const T* p = id < DK * DK / 8 ? Ac + (int64_t)j * DK * DK + id * 8 : Bc + (int64_t)j * DK * DV + (id - DK * DK / 8) * 8;
+      raw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
     }
-#pragma unroll
-    for (int I = 0; I < NT; ++I) gn[I] = 32 * I + c < n ? a.gate[(row * a.n_cap + j) * n + 32 * I + c] : 0.f;
   };
-  f32x16 v[TW][NT];  // z of this wave's columns of At, or o of its columns of Bc
-  auto put_z = [&](int t, int I, const f32x16& z) {
-    const int node = 32 * I + c;
-    if (node >= N) return;
+  auto load_tile = [&](int j, int i) {
+    const int t = w + 8 * i;
+    if (t >= TILES) return;
+    const int W = t < AT ? DK : DV;
+    const T* p = t < AT ? Ac + (int64_t)j * DK * DK + 16 * t + c : Bc + (int64_t)j * DK * DV + 16 * (t - AT) + c;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int col = 32 * t + q * 8 + h * 4;
-      float r[4];
+    for (int g = 0; g < GN; ++g)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = z[4 * q + e];
+      for (int e = 0; e < 4; ++e) m[i][g][e] = p[(16 * g + 4 * G + e) * W];
+  };
+  auto load_gates = [&](int j) {
 #pragma unroll
-      for (int s = 0; s < O::TERMS; ++s) {
-        T* to = zs[s] + O::template at<DK>(node, col);
+    for (int I = 0; I < NT; ++I) {
+      const int node = n0 + 16 * I + c;
+      gn[I] = node < n ? a.gate[(row * a.n_cap + j) * n + node] : 0.f;
+    }
+  };
+  load_gates(j);
+  if constexpr (BF) load_map(j);
+  else
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const T x = (T)r[e];
-          to[e] = x;
-          r[e] -= (float)x;
-        }
+    for (int i = 0; i < TW; ++i) load_tile(j, i);
+  f32x4 v[TW][NT];  // z of this wave's columns of At, or o of its columns of Bc
+  auto put_z = [&](int t, int I, f32x4 r) {
+#pragma unroll
+    for (int s = 0; s < O::TERMS; ++s) {
+      T* to = zs[s] + La<T>::template at<DK>(16 * I + c, 16 * t + 4 * G);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const T x = (T)r[e];
+        to[e] = x;
+        r[e] -= (float)x;
       }
     }
   };
 #pragma unroll
   for (int i = 0; i < TW; ++i) {
-    const int t = w + 4 * i;
+    const int t = w + 8 * i;
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
-      v[i][I] = zero16();
-      if (t < DK / 32) {
-        const int node = 32 * I + c;
-        if (node < n) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(a.z + (row * n + node) * DK + 32 * t + q * 8 + h * 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][I][4 * q + e] = x[e];
-          }
-        }
-        put_z(t, I, v[i][I]);
-      }
+      const int node = n0 + 16 * I + c;
+      v[i][I] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (t >= TILES) continue;
+      if (node < n)
+        v[i][I] = t < AT ? *reinterpret_cast<const f32x4*>(a.z + (row * n + node) * DK + 16 * t + 4 * G)
+                         : *reinterpret_cast<const f32x4*>(a.o + ((b * n + node) * a.H + head) * DV + 16 * (t - AT) + 4 * G);
     }
   }
-  const int rz0 = O::template row_base<DK>(lane % 32 % N + (lane & 32));
-  const int ck0 = O::template col_base<DK>(lane), cv0 = O::template col_base<DV>(lane);
-  int j = next(nc);
-  if (j >= 0) load(j);
+#pragma unroll
+  for (int i = 0; i < TW; ++i)
+    if (w + 8 * i < AT)
+#pragma unroll
+      for (int I = 0; I < NT; ++I) put_z(w + 8 * i, I, v[i][I]);
+  const int rz0 = O::template row_base<DK>(lane);
   while (j >= 0) {
-    const int rz = own(rz0), ck = own(ck0), cv = own(cv0);
-    (void)ck; (void)cv;
     float g[NT];
-    Frag m[BF ? 1 : TW][GN];
 #pragma unroll
     for (int I = 0; I < NT; ++I) g[I] = gn[I];
+    const unsigned read = act[j];
     if constexpr (BF) {
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int id = i * 256 + tid;
-        if (id < DK * DK / 8) *reinterpret_cast<u32x4*>(at + O::template at<DK>(id / (DK / 8), id % (DK / 8) * 8)) = raw[i];
-        else {
+        const int id = i * 512 + tid;
+        if (id < DK * DK / 8) {
+          *reinterpret_cast<u32x4*>(at + La<T>::template at<DK>(id / (DK / 8), id % (DK / 8) * 8)) = raw[i];
+        } else {
           const int k = id - DK * DK / 8;
-          *reinterpret_cast<u32x4*>(bt + O::template at<DV>(k / (DV / 8), k % (DV / 8) * 8)) = raw[i];
+          *reinterpret_cast<u32x4*>(bt + La<T>::template at<DV>(k / (DV / 8), k % (DV / 8) * 8)) = raw[i];
         }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < TW; ++i)
-#pragma unroll
-        for (int k = 0; k < LF; ++k) m[i][k / 4][k % 4] = rawf[i][k];
     }
     __syncthreads();
-    const int jn = next(j);
-    if (jn >= 0) load(jn);
-    f32x16 acc[TW][NT];
+    const int jn = next(j), rz = own(rz0);
+    if (jn >= 0) {
+      load_gates(jn);
+      if constexpr (BF) load_map(jn);
+    }
+    f32x4 acc[TW][NT];
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-      const int t = w + 4 * i;
+      const int t = w + 8 * i;
 #pragma unroll
-      for (int I = 0; I < NT; ++I) acc[i][I] = zero16();
+      for (int I = 0; I < NT; ++I) acc[i][I] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (t >= TILES) continue;
+      Frag f[GN];
 #pragma unroll
       for (int k = 0; k < GN; ++k) {
-        Frag f;
-        if constexpr (BF) f = t < DK / 32 ? O::template col<DK>(at, ck, t, k) : O::template col<DV>(bt, cv, t - DK / 32, k);
-        else f = m[i][k];
-#pragma unroll
-        for (int I = 0; I < NT; ++I)
-#pragma unroll
-          for (int s = O::TERMS - 1; s >= 0; --s)
-            acc[i][I] = O::mma(f, O::template row<DK>(zs[s], rz, 32 * I, k), acc[i][I]);
+        if constexpr (BF) f[k] = t < AT ? O::template col<DK>(at, O::template col_base<DK>(lane), t, k)
+                                        : O::template col<DV>(bt, O::template col_base<DV>(lane), t - AT, k);
+        else f[k] = m[i][k];
       }
+#pragma unroll
+      for (int I = 0; I < NT; ++I) {
+        if (NT > 1 && !((read >> I) & 1)) continue;  // no node of this tile reads the chunk
+#pragma unroll
+        for (int k = 0; k < GN; ++k)
+#pragma unroll
+          for (int s = O::TERMS - 1; s >= 0; --s) acc[i][I] = O::mma(f[k], O::template row<DK>(zs[s], rz, 16 * I, k), acc[i][I]);
+      }
+      if constexpr (!BF) if (jn >= 0) load_tile(jn, i);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-      const int t = w + 4 * i;
+      const int t = w + 8 * i;
       if (t >= TILES) continue;
-      const bool isA = t < DK / 32;
+      const bool isA = t < AT;
 #pragma unroll
       for (int I = 0; I < NT; ++I) {
         if (g[I] != 0.f) {  // a node that skips the chunk keeps its values, whatever the chunk holds
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[i][I][e] += g[I] * (acc[i][I][e] - (isA ? v[i][I][e] : 0.f));
+          for (int e = 0; e < 4; ++e) v[i][I][e] += g[I] * (acc[i][I][e] - (isA ? v[i][I][e] : 0.f));
         }
         if (isA) put_z(t, I, v[i][I]);
       }
@@ -468,20 +469,12 @@ __global__ __launch_bounds__(256) void tree_chain_kernel(TreeArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < TW; ++i) {
-    const int t = w + 4 * i;
-    if (t < DK / 32 || t >= TILES) continue;
+    const int t = w + 8 * i;
+    if (t < AT || t >= TILES) continue;
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
-      const int node = 32 * I + c;
-      if (node >= n) continue;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f32x4* p = reinterpret_cast<f32x4*>(a.o + ((b * n + node) * a.H + head) * DV + 32 * t - DK + q * 8 + h * 4);
-        f32x4 x = *p;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] += v[i][I][4 * q + e];
-        *p = x;
-      }
+      const int node = n0 + 16 * I + c;
+      if (node < n) *reinterpret_cast<f32x4*>(a.o + ((b * n + node) * a.H + head) * DV + 16 * (t - AT) + 4 * G) = v[i][I];
     }
   }
 }
@@ -578,7 +571,16 @@ hipError_t decode_n(const TreeArgs& a, hipStream_t s) {
   while (per > 4 && (int64_t)rows * ((a.n_cap + per - 1) / per) < 512) per -= 4;
   hipLaunchKernelGGL((tree_gates_kernel<T, DK, (N + 31) / 32>), dim3(rows, (a.n_cap + per - 1) / per), dim3(256), 0, s, a, per);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, N>), dim3(rows), dim3(256), 0, s, a);
+  // A workgroup takes 1, 2 or 4 tiles of 16 nodes.  Few rows: as few as give 512 workgroups at most, so that
+  // more compute units work, each reading the maps; many rows: all, so that maps are read once.
+  const int tiles = (a.n + 15) / 16;
+  int per_wg = 1;
+  while (per_wg < tiles && (int64_t)rows * ((tiles + per_wg - 1) / per_wg) > 512) per_wg *= 2;
+  const int groups = (tiles + per_wg - 1) / per_wg;
+  const dim3 grid(rows * groups);
+  if (per_wg == 1) hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 1>), grid, dim3(512), 0, s, a, groups);
+  else if (per_wg == 2) hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 2>), grid, dim3(512), 0, s, a, groups);
+  else hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 4>), grid, dim3(512), 0, s, a, groups);
   return hipGetLastError();
 }
 

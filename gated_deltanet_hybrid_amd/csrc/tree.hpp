@@ -18,7 +18,7 @@ struct TreeArgs {
   float *o, *gates_out;         // [Bs, n, H, dv]; [Bs, n, H, n_cap] or null
   float* z;                     // workspace [rows, n, dk]: the nodes' queries as the newest chunk meets them
   float* gate;                  // workspace [rows, n_cap, n]: gates after the threshold
-  int32_t* active;              // workspace [rows, n_cap]: whether any node reads the chunk
+  int32_t* active;              // workspace [rows, n_cap]: a bit for each 16 nodes of which any reads the chunk
   int64_t Bs, H;
   int32_t n, n_cap, n_rep;
   float tau;
