@@ -259,6 +259,7 @@ hla_status_t hla_la_prefill_backward(const hla_la_dims_t* d, const void* q, cons
   c.n = (int32_t)p.n;
   c.piece = hla::la_piece(d->dtype);
   c.w = d->dk;
+  c.from_zero = S0 == nullptr;
   if ((e = hla::launch_la_decay(c, stream)) != hipSuccess) return status(e);
   if (d->decay_per_head && (e = hla::launch_la_head_sum(c.dg, dlog_decay, d->B, d->H, d->T, stream)) != hipSuccess)
     return status(e);

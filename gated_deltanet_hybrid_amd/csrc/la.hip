@@ -684,10 +684,11 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
 // and gamma the decay of all its tokens, that is
 //     gamma <dM, M_0> + sum_{j<t} b_j + sum_{i>=t} c_i + sum_{i>=t>j} E_ij
 // (b_j = k_j . the part of dk_j that comes from behind the piece, c_i = q_i . the part of dq_i from in
-// front of it, E_ij the score pairs): the double sum is that of (row - column) sums from t on.  The
-// first term is X = <dM, M_P> - sum b, with <dM, M_P> a product of whole states at the segment's end
+// front of it, E_ij the score pairs): the double sum is, with e_s row s's sum less column s's, that of -e_s
+// over s < t.  The first term is X = <dM, M_P> - sum b, with <dM, M_P> a product of whole states at the segment's end
 // and X + sum c at every other piece's.  Where gamma < 2^-24, X is zero to float32 and is taken as that,
-// so that the difference's rounding does not stand in for it.  One workgroup runs one segment, a wave a
+// so that the difference's rounding does not stand in for it; so it is in the piece that starts from a zero
+// state.  One workgroup runs one segment, a wave a
 // piece; only the chain of <dM, M> is one thread's.
 constexpr int kLaChain = 64;
 template <int P>
@@ -716,18 +717,32 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
     const float* m = a.fwd + (row * (a.nseg + 1) + seg + 1) * (int64_t)a.n;
     const bool behind = seg + 1 < a.nseg;
     const float* r = behind ? a.rev + (row * a.nseg + seg) * (int64_t)a.n : a.dS ? a.dS + row * a.n : nullptr;
-    if (r) {
-      const int w = a.w, tall = a.n / w;
+    if (r && behind) {
       for (int i0 = tid; i0 < a.n; i0 += 256 * 16) {  // 4096 divides every dk dv
         float u[16], v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int i = i0 + 256 * e;
-          u[e] = m[i];
-          v[e] = r[behind ? i : (i % w) * tall + i / w];
+          u[e] = m[i0 + 256 * e];
+          v[e] = r[i0 + 256 * e];
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) x += (double)u[e] * v[e];
+      }
+    } else if (r) {  // dS is [dk, dv], M here [dv, dk]: 16 x 16 tiles, a lane four values of a row of dS
+      const int w = a.w, tall = a.n / w, tiles = a.n / 256, k = lane & 15, c = (lane >> 4) * 4;
+      for (int t0 = wave; t0 < tiles; t0 += 16) {  // 16 divides the number of tiles
+        float4 v[4];
+        float u[4][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = t0 + 4 * e, k0 = t % (w / 16) * 16 + k, c0 = t / (w / 16) * 16 + c;
+          v[e] = *reinterpret_cast<const float4*>(r + k0 * tall + c0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) u[e][q] = m[(c0 + q) * w + k0];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x += (double)u[e][0] * v[e].x + (double)u[e][1] * v[e].y + (double)u[e][2] * v[e].z + (double)u[e][3] * v[e].w;
       }
     }
   }
@@ -772,7 +787,7 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
         if (last * P < Tb) phi *= decay_of(g_at(last * P));
       }
       for (int64_t p = hi - 1; p >= lo; --p) {
-        const double X = gone[p - lo] != 0.f ? 0.0 : phi - sum_b[p - lo];
+        const double X = gone[p - lo] != 0.f || (a.from_zero && p == 0) ? 0.0 : phi - sum_b[p - lo];
         at_end[p - lo] = X;
         phi = X + sum_c[p - lo];
       }
@@ -781,7 +796,8 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
     for (int64_t p = lo + wave; p < hi; p += 4) {
       float bb, cc, ee, g;
       const bool on = take(p, bb, cc, ee, g);
-      double before = bb, behind = (double)cc + ee;
+      const double own_before = (double)bb - ee;
+      double before = own_before, behind = cc;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const double y = __shfl_up(before, o, 64), z = __shfl_down(behind, o, 64);
@@ -789,7 +805,7 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
         if (lane + o < 64) behind += z;
       }
       const int64_t t = p * P + lane;
-      if (lane < P && t < a.T) *out(t) = on && g > -104.f ? (float)(at_end[p - lo] + (before - bb) + behind) : 0.f;
+      if (lane < P && t < a.T) *out(t) = on && g > -104.f ? (float)(at_end[p - lo] + (before - own_before) + behind) : 0.f;
     }
     __syncthreads();
   }

@@ -73,6 +73,7 @@ struct LaDecay {         // the gradient of g from the sweeps' dot products
   float* dg;                  // [B, T, H], or [rows, T] (per_head)
   int64_t B, T, H;
   int32_t per_head, nseg, seg_pieces, n, piece, w;  // n = dk dv; w: the row width of fwd and rev
+  int32_t from_zero;          // no initial state
 };
 
 struct LaGroup { const float* x; void* y; int64_t tokens; int32_t group, width, heads; };

@@ -88,3 +88,14 @@ def test_decode_is_the_recurrence(dtype, Bs, H, Hk, dk, dv, per_head):
     got = torch.stack(outs, 1).float().cpu().numpy().astype(np.float64)
     lim = bound("f32", ro[0], ro[1], T + dk) + (2.0 ** -8 * np.abs(ro[0]) if dtype == "bf16" else 0.0)
     assert (np.abs(got - ro[0]) <= lim).all()
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("f32", 1), ("bf16", 200), ("f32", 200)])
+def test_nothing_decays_in_front_of_a_zero_state(dtype, T):
+    """The first token of a row meets a zero state: its decay has no effect, and its gradient is 0 and no
+    rounding of something else."""
+    note(f"la_prefill_backward from zero {dtype} {T}")
+    c = Case(3, T, 2, 2, 64, 128, dtype, start=False, lens=[T, 1, 0])
+    d = hla.la_prefill_backward(*c.args(), c.device("dO"), dS_final=torch.ones(3, 2, 64, 128, device="cuda"), **c.kw())
+    assert (d["dlog_decay"][:, 0] == 0).all()
+    assert (d["dlog_decay"][1:] == 0).all()
