@@ -66,16 +66,18 @@ template <class T, int DK, int DV, int N> struct LiveShared {
 };
 
 // The live part of every node: r, then o = P U + M_0^T r and z = At_cur^T r.  One workgroup a row.
-// The solve runs one thread a column (dk of W, dv of U), its values in registers.
+// The solve runs one thread a column (dk of W, dv of U), its values in registers; the live matrices come
+// straight from memory, every value to the one lane that multiplies it.
 template <class T, int DK, int DV, int N>
-__global__ __launch_bounds__(256) void tree_live_kernel(TreeArgs a) {
+__device__ __forceinline__ void live_part(const TreeArgs& a, LiveShared<T, DK, DV, N>& sh, int64_t row) {
   using O = La<T>;
   using S = LiveShared<T, DK, DV, N>;
-  constexpr int V = 16 / (int)sizeof(T), NT = (N + 31) / 32;
-  __shared__ S sh;
+  constexpr int V = 16 / (int)sizeof(T), NT = (N + 31) / 32, TW = (DK + DV + 127) / 128;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, c = lane & 31;
-  const int64_t row = blockIdx.x, b = row / a.H;
+  const int64_t b = row / a.H;
   const int head = (int)(row % a.H), n = a.n;
+  // 32 columns of a live matrix a tile
+  const int tiles = DV / 32 + (a.At_cur ? DK / 32 : 0);
   if (w == 0) {
     double lg = 0.0;
     float beta = 0.f;
@@ -145,6 +147,7 @@ __global__ __launch_bounds__(256) void tree_live_kernel(TreeArgs a) {
     }
 #pragma unroll
     for (int i = 1; i < N; ++i) {
+      if (i >= n) continue;
 #pragma unroll
       for (int j = 0; j < i; j += 4) {
         const f32x4 l = *reinterpret_cast<const f32x4*>(&sh.L[i][j]);
@@ -156,6 +159,7 @@ __global__ __launch_bounds__(256) void tree_live_kernel(TreeArgs a) {
     }
 #pragma unroll
     for (int i = N - 1; i >= 0; --i) {
+      if (i >= n) continue;
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j <= i; j += 4) {
@@ -181,25 +185,32 @@ __global__ __launch_bounds__(256) void tree_live_kernel(TreeArgs a) {
     for (int i = 0; i < N; ++i) sh.out.o[i * S::OD + tid - DK] = x[i];
   }
   __syncthreads();
-  // M^T r, 32 columns of M a tile (float32 matrix cores; M's rows come straight from memory)
-  const int tiles = DV / 32 + (a.At_cur ? DK / 32 : 0);
-  for (int t = w; t < tiles; t += 4) {
+  // M^T r on the float32 matrix cores
+#pragma unroll
+  for (int tw = 0; tw < TW; ++tw) {
+    const int t = w + 4 * tw;
+    if (t >= tiles) continue;
     const bool state = t < DV / 32;
-    const int W = state ? DV : DK, n0 = state ? 32 * t : 32 * t - DV;
+    const int n0 = state ? 32 * t : 32 * t - DV, W = state ? DV : DK;
     const float* M = (state ? a.S_cur + row * DK * DV : a.At_cur + row * DK * DK) + n0 + c;
     f32x16 acc[NT];
 #pragma unroll
     for (int I = 0; I < NT; ++I) acc[I] = zero16();
-#pragma unroll 8
-    for (int g = 0; g < DK / 8; ++g) {
-      float m[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m[e] = M[(g * 8 + h * 4 + e) * W];
+    for (int g0 = 0; g0 < DK / 8; g0 += 8) {  // 32 loads a lane at a time
+      float m[8][4];
 #pragma unroll
-      for (int I = 0; I < NT; ++I) {
-        const f32x4 r = *reinterpret_cast<const f32x4*>(sh.out.r + ((32 * I + c) % N) * S::RD + g * 8 + h * 4);
+      for (int g = 0; g < 8; ++g)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[I] = __builtin_amdgcn_mfma_f32_32x32x2f32(m[e], r[e], acc[I], 0, 0, 0);
+        for (int e = 0; e < 4; ++e) m[g][e] = M[((g0 + g) * 8 + h * 4 + e) * W];
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+#pragma unroll
+        for (int I = 0; I < NT; ++I) {
+          const f32x4 r = *reinterpret_cast<const f32x4*>(sh.out.r + ((32 * I + c) % N) * S::RD + (g0 + g) * 8 + h * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[I] = __builtin_amdgcn_mfma_f32_32x32x2f32(m[g][e], r[e], acc[I], 0, 0, 0);
+        }
       }
     }
 #pragma unroll
@@ -221,15 +232,16 @@ __global__ __launch_bounds__(256) void tree_live_kernel(TreeArgs a) {
   }
 }
 
-// Gates of every node for the held chunks, a wave a chunk: sigmoid of the log-mean-exp of the node's
-// scores over the chunk's representatives (rows of the product; nodes are its columns).
+// Gates of every node for the held chunks, a wave a chunk: sigmoid of the log-mean-exp of the node's scores
+// over the chunk's representatives, 16 of them (rows) and 16 nodes (columns) a tile.  Exponents are to base
+// 2; the next 16 representatives are asked for while these are exponentiated.
 template <class T, int DK, int NT>
-__global__ __launch_bounds__(256) void tree_gates_kernel(TreeArgs a, int per_block) {
-  using O = La<T>;
+__device__ __forceinline__ void gates_part(const TreeArgs& a, int64_t row, int part, int per_block) {
+  using O = La16<T>;
   using Frag = typename O::Frag;
-  constexpr int GN = DK / O::KG;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h = lane >> 5, c = lane & 31;
-  const int64_t row = blockIdx.x, b = row / a.H;
+  constexpr int GN = DK / O::KG, E = O::KG / 4;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, G = lane >> 4, c = lane & 15;
+  const int64_t b = row / a.H;
   const int head = (int)(row % a.H), n = a.n;
   int nc = a.n_cache[b];
   nc = nc < 0 ? 0 : (nc > a.n_cap ? a.n_cap : nc);
@@ -238,42 +250,46 @@ __global__ __launch_bounds__(256) void tree_gates_kernel(TreeArgs a, int per_blo
   if (!a.gates_in) {
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
-      const int i = 32 * I + c < n ? 32 * I + c : n - 1;
+      const int i = 16 * I + c < n ? 16 * I + c : n - 1;
 #pragma unroll
       for (int g = 0; g < GN; ++g)
-        q[I][g] = O::plain(static_cast<const T*>(a.q) + ((b * n + i) * a.H + head) * DK + g * O::KG + h * (O::KG / 2));
+        q[I][g] = O::O::plain(static_cast<const T*>(a.q) + ((b * n + i) * a.H + head) * DK + g * O::KG + G * E);
     }
   }
-  const float scale = 1.f / sqrtf((float)DK);
-  const int end = (blockIdx.y + 1) * per_block < a.n_cap ? (blockIdx.y + 1) * per_block : a.n_cap;
-  for (int j = blockIdx.y * per_block + w; j < end; j += 4) {
+  const float scale = (float)(1.4426950408889634 / sqrt((double)DK));
+  const int end = (part + 1) * per_block < a.n_cap ? (part + 1) * per_block : a.n_cap;
+  for (int j = part * per_block + w; j < end; j += 4) {
     float m[NT], sum[NT];
 #pragma unroll
     for (int I = 0; I < NT; ++I) { m[I] = -INFINITY; sum[I] = 0.f; }
     if (j < nc && !a.gates_in) {
-      const T* reps = static_cast<const T*>(a.reps_cache) + (row * a.n_cap + j) * (int64_t)a.n_rep * DK;
-      for (int r0 = 0; r0 < a.n_rep; r0 += 32) {
+      const T* reps = static_cast<const T*>(a.reps_cache) + (row * a.n_cap + j) * (int64_t)a.n_rep * DK + G * E;
+      Frag k[GN];
+      auto ask = [&](int r0) {
         const int r = r0 + c < a.n_rep ? r0 + c : a.n_rep - 1;
-        f32x16 s[NT];
 #pragma unroll
-        for (int I = 0; I < NT; ++I) s[I] = zero16();
+        for (int g = 0; g < GN; ++g) k[g] = O::O::plain(reps + (int64_t)r * DK + g * O::KG);
+      };
+      ask(0);
+      for (int r0 = 0; r0 < a.n_rep; r0 += 16) {
+        f32x4 s[NT];
 #pragma unroll
-        for (int g = 0; g < GN; ++g) {
-          const Frag k = O::plain(reps + (int64_t)r * DK + g * O::KG + h * (O::KG / 2));
+        for (int I = 0; I < NT; ++I) {
+          s[I] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int I = 0; I < NT; ++I) s[I] = O::mma(k, q[I][g], s[I]);
+          for (int g = 0; g < GN; ++g) s[I] = O::mma(k[g], q[I][g], s[I]);
         }
+        if (r0 + 16 < a.n_rep) ask(r0 + 16);
+        const int left = a.n_rep - r0 - 4 * G;
 #pragma unroll
         for (int I = 0; I < NT; ++I) {
           float top = m[I];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (r0 + acc_row(e, h) < a.n_rep) top = fmaxf(top, s[I][e] * scale);
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, e < left ? s[I][e] * scale : -INFINITY);
           float add = 0.f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (r0 + acc_row(e, h) < a.n_rep) add += expf(s[I][e] * scale - top);
-          sum[I] = (m[I] > -INFINITY ? sum[I] * expf(m[I] - top) : 0.f) + add;
+          for (int e = 0; e < 4; ++e) add += e < left ? exp2_(__builtin_fmaf(s[I][e], scale, -top)) : 0.f;
+          sum[I] = sum[I] * (m[I] > -INFINITY ? exp2_(m[I] - top) : 0.f) + add;  // a NaN stays
           m[I] = top;
         }
       }
@@ -281,23 +297,30 @@ __global__ __launch_bounds__(256) void tree_gates_kernel(TreeArgs a, int per_blo
     unsigned any = 0;
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
-      const int i = 32 * I + c;
+      const int i = 16 * I + c;
       float g = 0.f;
       if (j < nc) {
         if (a.gates_in) {
           if (i < n) g = a.gates_in[((b * n + i) * a.H + head) * a.n_cap + j];
         } else {
-          const float m2 = __shfl_xor(m[I], 32, 64), s2 = __shfl_xor(sum[I], 32, 64);
-          const float top = fmaxf(m[I], m2);
-          const float all = (m[I] > -INFINITY ? sum[I] * expf(m[I] - top) : 0.f) + (m2 > -INFINITY ? s2 * expf(m2 - top) : 0.f);
-          g = 1.f / (1.f + expf(-(top + logf(all / (float)a.n_rep))));
+          float top = m[I], all = sum[I];
+#pragma unroll
+          for (int o = 16; o <= 32; o <<= 1) {
+            const float m2 = __shfl_xor(top, o, 64), s2 = __shfl_xor(all, o, 64), t = fmaxf(top, m2);
+            all = all * (top > -INFINITY ? exp2_(top - t) : 0.f) + s2 * (m2 > -INFINITY ? exp2_(m2 - t) : 0.f);
+            top = t;
+          }
+          // 1 / (1 + e^-l) with e^l = 2^top all / n_rep
+          const float l2 = top + log2f(all / (float)a.n_rep);
+          g = 1.f / (1.f + exp2f(-l2));
+          if (all != all) g = all;  // fmaxf drops a NaN score; its sum does not
         }
       }
-      if (!((here >> (i & 63)) & 1)) g = 0.f;
-      const bool keep = j < nc && ((here >> (i & 63)) & 1) && g >= a.tau;
-      const unsigned long long kept = __ballot(keep);  // lanes 0 .. 15 and 16 .. 31 are two tiles of 16 nodes
-      any |= ((kept & 0xffff ? 1u : 0u) | (kept & 0xffff0000 ? 2u : 0u)) << (2 * I);
-      if (h == 0 && i < n) {
+      const bool on = (here >> i) & 1;
+      if (!on) g = 0.f;
+      const bool keep = j < nc && on && g >= a.tau;
+      if (__any(keep)) any |= 1u << I;
+      if (G == 0 && i < n) {
         if (a.gates_out) a.gates_out[((b * n + i) * a.H + head) * a.n_cap + j] = g;
         if (j < nc) a.gate[(row * a.n_cap + j) * n + i] = keep ? g : 0.f;
       }
@@ -306,13 +329,29 @@ __global__ __launch_bounds__(256) void tree_gates_kernel(TreeArgs a, int per_blo
   }
 }
 
+template <class T, int DK, int NT>
+__global__ __launch_bounds__(256) void tree_gates_kernel(TreeArgs a, int per_block) {
+  gates_part<T, DK, NT>(a, blockIdx.x, blockIdx.y, per_block);
+}
+
+// The two parts need nothing of each other: `parts` workgroups a row, the first the live part's and the
+// others (in a launch of few workgroups, which saves one) the gates'.
+template <class T, int DK, int DV, int N>
+__global__ __launch_bounds__(256) void tree_front_kernel(TreeArgs a, int parts, int per_block) {
+  __shared__ LiveShared<T, DK, DV, N> sh;
+  const int64_t row = blockIdx.x / parts;
+  const int part = (int)(blockIdx.x % parts);
+  if (part == 0) live_part<T, DK, DV, N>(a, sh, row);
+  else gates_part<T, DK, N / 16>(a, row, part - 1, per_block);
+}
+
 // The chain over the cached chunks, for NT tiles of 16 nodes of a row.  Each of the 8 waves owns tiles of 16
 // columns of At (their z, as accumulators: rows the columns, column the node) or of Bc (their o).  bf16 maps
 // go through LDS, which hands them out transposed, and z enters as three bf16 terms, float32 to its last
-// bit; float32 maps come straight from memory, every value to the one lane that multiplies it.  The next
-// chunk that a node here reads is asked for while this one is worked on.
-template <class T, int DK, int DV, int NT>
-__global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeArgs a, int groups) {
+// bit; float32 maps come straight from memory, every value to the one lane that multiplies it.  The chunk
+// that is AHEAD read chunks away is asked for while this one is worked on.
+template <class T, int DK, int DV, int NT, int AHEAD>
+__global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 ? 4 : 2) void tree_chain_kernel(TreeArgs a, int groups) {
   using O = La16<T>;
   using Frag = typename O::Frag;
   constexpr bool BF = sizeof(T) == 2;
@@ -338,10 +377,10 @@ __global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeAr
   if (j < 0) return;  // no node here reads a chunk: o is the live part
   const T* Ac = static_cast<const T*>(a.At_cache) + row * a.n_cap * DK * DK;
   const T* Bc = static_cast<const T*>(a.Bc_cache) + row * a.n_cap * DK * DV;
-  u32x4 raw[LD];
-  Frag m[BF ? 1 : TW][GN];
-  float gn[NT];
-  auto load_map = [&](int j) {
+  u32x4 raw[AHEAD][LD];
+  Frag m[AHEAD][BF ? 1 : TW][GN];
+  float gn[AHEAD][NT];
+  auto load_map = [&](int j, u32x4 (&raw)[LD]) {
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
       const int id = i * 512 + tid;
@@ -349,7 +388,7 @@ __global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeAr
       raw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
     }
   };
-  auto load_tile = [&](int j, int i) {
+  auto load_tile = [&](int j, int i, Frag (&m)[GN]) {
     const int t = w + 8 * i;
     if (t >= TILES) return;
     const int W = t < AT ? DK : DV;
@@ -357,20 +396,27 @@ __global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeAr
 #pragma unroll
     for (int g = 0; g < GN; ++g)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m[i][g][e] = p[(16 * g + 4 * G + e) * W];
+      for (int e = 0; e < 4; ++e) m[g][e] = p[(16 * g + 4 * G + e) * W];
   };
-  auto load_gates = [&](int j) {
+  auto load_gates = [&](int j, float (&gn)[NT]) {
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
       const int node = n0 + 16 * I + c;
       gn[I] = node < n ? a.gate[(row * a.n_cap + j) * n + node] : 0.f;
     }
   };
-  load_gates(j);
-  if constexpr (BF) load_map(j);
-  else
+  int jb[AHEAD + 1] = {j};  // the chunks in hand, and the one to ask for next
 #pragma unroll
-    for (int i = 0; i < TW; ++i) load_tile(j, i);
+  for (int k = 0; k < AHEAD; ++k) {
+    if (jb[k] >= 0) {
+      load_gates(jb[k], gn[k]);
+      if constexpr (BF) load_map(jb[k], raw[k]);
+      else
+#pragma unroll
+        for (int i = 0; i < TW; ++i) load_tile(jb[k], i, m[k][i]);
+    }
+    jb[k + 1] = jb[k] >= 0 ? next(jb[k]) : -1;
+  }
   f32x4 v[TW][NT];  // z of this wave's columns of At, or o of its columns of Bc
   auto put_z = [&](int t, int I, f32x4 r) {
 #pragma unroll
@@ -403,28 +449,30 @@ __global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeAr
 #pragma unroll
       for (int I = 0; I < NT; ++I) put_z(w + 8 * i, I, v[i][I]);
   const int rz0 = O::template row_base<DK>(lane);
-  while (j >= 0) {
+  auto step = [&](auto buf) {  // the chunk jb[0], whose values are in buffer `buf`
+    constexpr int B = decltype(buf)::value;
+    const int j = jb[0], ja = jb[AHEAD];
     float g[NT];
 #pragma unroll
-    for (int I = 0; I < NT; ++I) g[I] = gn[I];
+    for (int I = 0; I < NT; ++I) g[I] = gn[B][I];
     const unsigned read = act[j];
     if constexpr (BF) {
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
         const int id = i * 512 + tid;
         if (id < DK * DK / 8) {
-          *reinterpret_cast<u32x4*>(at + La<T>::template at<DK>(id / (DK / 8), id % (DK / 8) * 8)) = raw[i];
+          *reinterpret_cast<u32x4*>(at + La<T>::template at<DK>(id / (DK / 8), id % (DK / 8) * 8)) = raw[B][i];
         } else {
           const int k = id - DK * DK / 8;
-          *reinterpret_cast<u32x4*>(bt + La<T>::template at<DV>(k / (DV / 8), k % (DV / 8) * 8)) = raw[i];
+          *reinterpret_cast<u32x4*>(bt + La<T>::template at<DV>(k / (DV / 8), k % (DV / 8) * 8)) = raw[B][i];
         }
       }
     }
     __syncthreads();
-    const int jn = next(j), rz = own(rz0);
-    if (jn >= 0) {
-      load_gates(jn);
-      if constexpr (BF) load_map(jn);
+    const int rz = own(rz0);
+    if (ja >= 0) {
+      load_gates(ja, gn[B]);
+      if constexpr (BF) load_map(ja, raw[B]);
     }
     f32x4 acc[TW][NT];
 #pragma unroll
@@ -438,7 +486,7 @@ __global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeAr
       for (int k = 0; k < GN; ++k) {
         if constexpr (BF) f[k] = t < AT ? O::template col<DK>(at, O::template col_base<DK>(lane), t, k)
                                         : O::template col<DV>(bt, O::template col_base<DV>(lane), t - AT, k);
-        else f[k] = m[i][k];
+        else f[k] = m[B][i][k];
       }
 #pragma unroll
       for (int I = 0; I < NT; ++I) {
@@ -448,7 +496,7 @@ __global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeAr
 #pragma unroll
           for (int s = O::TERMS - 1; s >= 0; --s) acc[i][I] = O::mma(f[k], O::template row<DK>(zs[s], rz, 16 * I, k), acc[i][I]);
       }
-      if constexpr (!BF) if (jn >= 0) load_tile(jn, i);
+      if constexpr (!BF) if (ja >= 0) load_tile(ja, i, m[B][i]);
     }
     __syncthreads();
 #pragma unroll
@@ -465,7 +513,17 @@ __global__ __launch_bounds__(512, NT == 1 ? 4 : 2) void tree_chain_kernel(TreeAr
         if (isA) put_z(t, I, v[i][I]);
       }
     }
-    j = jn;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) jb[k] = jb[k + 1];
+    jb[AHEAD] = ja >= 0 ? next(ja) : -1;
+  };
+  while (true) {
+    step(std::integral_constant<int, 0>{});
+    if (jb[0] < 0) break;
+    if constexpr (AHEAD > 1) {
+      step(std::integral_constant<int, 1>{});
+      if (jb[0] < 0) break;
+    }
   }
 #pragma unroll
   for (int i = 0; i < TW; ++i) {
@@ -563,14 +621,22 @@ __global__ void tree_advance_kernel(int32_t* n_cache, const int32_t* commit, int
 template <class T, int DK, int DV, int N>
 hipError_t decode_n(const TreeArgs& a, hipStream_t s) {
   const unsigned rows = (unsigned)(a.Bs * a.H);
-  hipLaunchKernelGGL((tree_live_kernel<T, DK, DV, N>), dim3(rows), dim3(256), 0, s, a);
+  // The gates' workgroups take up to 64 chunks of a row, 16 a wave (each starts with the tree's and the
+  // queries' loads), and fewer, down to one a wave, as long as there are fewer than 1024 of them.
+  int per = 64;
+  while (per > 4 && (int64_t)rows * ((a.n_cap + per - 1) / per) < 1024) per /= 2;
+  const int gate_parts = a.At_cur ? (a.n_cap + per - 1) / per : 0;
+  // Where all fit the chip at once, both are one launch (the live part's registers and LDS would cost the
+  // gates of a large batch their place on the compute units).
+  const bool together = (int64_t)rows * (1 + gate_parts) <= 256;
+  const int parts = together ? 1 + gate_parts : 1;
+  hipLaunchKernelGGL((tree_front_kernel<T, DK, DV, N>), dim3(rows * parts), dim3(256), 0, s, a, parts, per);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.At_cur) return e;
-  // four chunks a wave, fewer where there are few rows
-  int per = 16;
-  while (per > 4 && (int64_t)rows * ((a.n_cap + per - 1) / per) < 512) per -= 4;
-  hipLaunchKernelGGL((tree_gates_kernel<T, DK, (N + 31) / 32>), dim3(rows, (a.n_cap + per - 1) / per), dim3(256), 0, s, a, per);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (!together) {
+    hipLaunchKernelGGL((tree_gates_kernel<T, DK, N / 16>), dim3(rows, gate_parts), dim3(256), 0, s, a, per);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   // A workgroup takes 1, 2 or 4 tiles of 16 nodes.  Few rows: as few as give 512 workgroups at most, so that
   // more compute units work, each reading the maps; many rows: all, so that maps are read once.
   const int tiles = (a.n + 15) / 16;
@@ -578,9 +644,12 @@ hipError_t decode_n(const TreeArgs& a, hipStream_t s) {
   while (per_wg < tiles && (int64_t)rows * ((tiles + per_wg - 1) / per_wg) > 512) per_wg *= 2;
   const int groups = (tiles + per_wg - 1) / per_wg;
   const dim3 grid(rows * groups);
-  if (per_wg == 1) hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 1>), grid, dim3(512), 0, s, a, groups);
-  else if (per_wg == 2) hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 2>), grid, dim3(512), 0, s, a, groups);
-  else hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 4>), grid, dim3(512), 0, s, a, groups);
+  // Two chunks ahead where a compute unit has one workgroup at most, whose chain waits for memory; else the
+  // registers are better spent on a second workgroup.
+  if (per_wg == 1 && grid.x <= 256) hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 1, 2>), grid, dim3(512), 0, s, a, groups);
+  else if (per_wg == 1) hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 1, 1>), grid, dim3(512), 0, s, a, groups);
+  else if (per_wg == 2) hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 2, 1>), grid, dim3(512), 0, s, a, groups);
+  else hipLaunchKernelGGL((tree_chain_kernel<T, DK, DV, 4, 1>), grid, dim3(512), 0, s, a, groups);
   return hipGetLastError();
 }
 
