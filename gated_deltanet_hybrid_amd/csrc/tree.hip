@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256) void tree_front_kernel(TreeArgs a, int parts, 
 // bit; float32 maps come straight from memory, every value to the one lane that multiplies it.  The chunk
 // that is AHEAD read chunks away is asked for while this one is worked on.
 template <class T, int DK, int DV, int NT, int AHEAD>
-__global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 ? 4 : 2) void tree_chain_kernel(TreeArgs a, int groups) {
+__global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 2) void tree_chain_kernel(TreeArgs a, int groups) {
   using O = La16<T>;
   using Frag = typename O::Frag;
   constexpr bool BF = sizeof(T) == 2;
@@ -389,8 +389,7 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 ? 4 : 2) void tree_chain
     }
   };
   auto load_tile = [&](int j, int i, Frag (&m)[GN]) {
-    const int t = w + 8 * i;
-    if (t >= TILES) return;
+    const int t = w + 8 * i < TILES ? w + 8 * i : w;
     const int W = t < AT ? DK : DV;
     const T* p = t < AT ? Ac + (int64_t)j * DK * DK + 16 * t + c : Bc + (int64_t)j * DK * DV + 16 * (t - AT) + c;
 #pragma unroll
@@ -474,29 +473,49 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 ? 4 : 2) void tree_chain
       load_gates(ja, gn[B]);
       if constexpr (BF) load_map(ja, raw[B]);
     }
+    // one chain of products a term where registers allow: a chain waits for each of its products
+    constexpr int CH = NT == 1 ? O::TERMS : 1;
     f32x4 acc[TW][NT];
+    Frag f[TW][GN];
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-      const int t = w + 8 * i;
-#pragma unroll
-      for (int I = 0; I < NT; ++I) acc[i][I] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (t >= TILES) continue;
-      Frag f[GN];
+      const int t = w + 8 * i < TILES ? w + 8 * i : w;  // a wave without its last tile works on its first again
 #pragma unroll
       for (int k = 0; k < GN; ++k) {
-        if constexpr (BF) f[k] = t < AT ? O::template col<DK>(at, O::template col_base<DK>(lane), t, k)
-                                        : O::template col<DV>(bt, O::template col_base<DV>(lane), t - AT, k);
-        else f[k] = m[B][i][k];
+        if constexpr (BF) f[i][k] = t < AT ? O::template col<DK>(at, O::template col_base<DK>(lane), t, k)
+                                           : O::template col<DV>(bt, O::template col_base<DV>(lane), t - AT, k);
+        else f[i][k] = m[B][i][k];
       }
+    }
 #pragma unroll
-      for (int I = 0; I < NT; ++I) {
-        if (NT > 1 && !((read >> I) & 1)) continue;  // no node of this tile reads the chunk
+    for (int I = 0; I < NT; ++I) {
+      f32x4 part[TW][CH];
+#pragma unroll
+      for (int i = 0; i < TW; ++i)
+#pragma unroll
+        for (int s = 0; s < CH; ++s) part[i][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (NT == 1 || ((read >> I) & 1)) {  // else no node of this tile reads the chunk
 #pragma unroll
         for (int k = 0; k < GN; ++k)
 #pragma unroll
-          for (int s = O::TERMS - 1; s >= 0; --s) acc[i][I] = O::mma(f[k], O::template row<DK>(zs[s], rz, 16 * I, k), acc[i][I]);
+          for (int s = O::TERMS - 1; s >= 0; --s) {
+            const Frag z = O::template row<DK>(zs[s], rz, 16 * I, k);
+#pragma unroll
+            for (int i = 0; i < TW; ++i) part[i][s % CH] = O::mma(f[i][k], z, part[i][s % CH]);
+          }
       }
-      if constexpr (!BF) if (ja >= 0) load_tile(ja, i, m[B][i]);
+#pragma unroll
+      for (int i = 0; i < TW; ++i) {
+        acc[i][I] = part[i][CH - 1];
+#pragma unroll
+        for (int s = CH - 2; s >= 0; --s) acc[i][I] += part[i][s];
+      }
+    }
+    if constexpr (!BF) {
+      if (ja >= 0) {
+#pragma unroll
+        for (int i = 0; i < TW; ++i) load_tile(ja, i, m[B][i]);
+      }
     }
     __syncthreads();
 #pragma unroll
