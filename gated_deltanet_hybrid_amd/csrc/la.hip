@@ -17,8 +17,8 @@
 // float32 tensors run on the float32 matrix instructions.  bf16 tensors enter exactly; what is float32
 // enters as bf16 terms, each of which takes 8 bits.  Three of them (24 bits) where the result comes out
 // as float32: the decayed values, which enter the states, and the state where the decays' gradient is
-// formed from it.  Two (2^-16 at most) for the state that outputs read, and one (2^-8) for the decayed
-// scores: these reach bf16 outputs only, which round to 2^-8 themselves.
+// formed from it.  Two (2^-16 at most) where it reaches bf16 outputs only: the state that outputs read and
+// the decayed scores.
 #include "operands.hpp"
 #include "la.hpp"
 #include "kernels.hpp"
@@ -70,7 +70,7 @@ template <class T, int DK, int DV, bool OUT, bool EXTRA> struct LaShared {
   alignas(16) T x2[O::template size<DK>()];
   alignas(16) T x3[O::template size<DV>()];
   alignas(16) T x4[EXTRA ? O::template size<DV>() : 8];
-  alignas(16) T sc[OUT ? O::P * O::PS : 8];
+  alignas(16) T sc[OUT ? O::SCORES : 8];
   Decays<O::P> d[2];
   float dot[EXTRA ? DV / 32 : 1][O::P];
 };
@@ -115,12 +115,21 @@ __device__ __forceinline__ void tile_decays(float (&D)[16], const Decays<P>& d, 
 // s D into the piece's scores (rows i, columns j); what lies behind i is zero whatever s is.
 template <class T>
 __device__ __forceinline__ void put_scores(T* sc, const f32x16& s, const float (&D)[16], int tile, int c, int h) {
-  const int ii = 32 * tile_i(tile) + c, last = ii - 32 * tile_j(tile) - 4 * h;
+  const int last = 32 * tile_i(tile) + c - 32 * tile_j(tile) - 4 * h;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    T* to = sc + ii * La<T>::PS + 32 * tile_j(tile) + q * 8 + h * 4;
+    float x[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) to[e] = (T)(acc_row(4 * q + e, 0) <= last ? s[4 * q + e] * D[4 * q + e] : 0.f);
+    for (int e = 0; e < 4; ++e) x[e] = acc_row(4 * q + e, 0) <= last ? s[4 * q + e] * D[4 * q + e] : 0.f;
+    T* to = sc + La<T>::score_at(tile, c, q, h);
+#pragma unroll
+    for (int t = 0; t < La<T>::SCORE_TERMS; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const T y = (T)x[e];
+        to[t * La<T>::SCORE_TERM + e] = y;
+        x[e] -= (float)y;
+      }
   }
 }
 
@@ -198,17 +207,12 @@ __device__ __forceinline__ void absorb(f32x16 (&M)[NM], f32x16 (&acc)[IT], const
 #pragma unroll
   for (int g = 0; g < GN; ++g) {
     typename O::Vals x;
-    Frag f[O::TERMS], k[MT], sc[IT], vn = v;
+    Frag f[O::TERMS], k[MT], vn = v;
     const int k0 = O::col_k(g, h);
 #pragma unroll
     for (int e = 0; e < O::FN; ++e) x[e] = d.w[k0 + e];
 #pragma unroll
     for (int m = 0; m < MT; ++m) k[m] = O::template col<WK>(x2, ck, m, g);
-    if constexpr (OUT) {
-#pragma unroll
-      for (int I = 0; I < IT; ++I)
-        if (g * O::KG < 32 * (I + 1)) sc[I] = O::plain(scores + (32 * I + c) * O::PS + k0);
-    }
     if (g + 1 < GN) vn = O::template col<WV>(x3, cv, w, g + 1);
     sched_fence();
 #pragma unroll
@@ -219,9 +223,16 @@ __device__ __forceinline__ void absorb(f32x16 (&M)[NM], f32x16 (&acc)[IT], const
 #pragma unroll
       for (int m = 0; m < MT; ++m) M[m] = O::mma(k[m], f[t], M[m]);
     if constexpr (OUT) {
+      sched_fence();  // the scores take the keys' registers
 #pragma unroll
       for (int I = 0; I < IT; ++I)
-        if (g * O::KG < 32 * (I + 1)) acc[I] = O::mma(sc[I], v, acc[I]);
+        if (g * O::KG < 32 * (I + 1)) {
+          Frag sc[O::SCORE_TERMS];
+#pragma unroll
+          for (int t = 0; t < O::SCORE_TERMS; ++t) sc[t] = O::score_row(scores, I, c, g, h, t);
+#pragma unroll
+          for (int t = O::SCORE_TERMS - 1; t >= 0; --t) acc[I] = O::mma(sc[t], v, acc[I]);
+        }
     }
     v = vn;
     sched_fence();
@@ -481,8 +492,8 @@ template <class T, int DK, int DV> struct LaReverseShared {
   alignas(16) T k[O::template size<DK>()];
   alignas(16) T v[O::template size<DV>()];
   alignas(16) T o[O::template size<DV>()];
-  alignas(16) T sk[O::P * O::PS];  // scores of dk: v_i . do_j
-  alignas(16) T sv[O::P * O::PS];  // of dv: k_i . q_j
+  alignas(16) T sk[O::SCORES];  // scores of dk: v_i . do_j
+  alignas(16) T sv[O::SCORES];  // of dv: k_i . q_j
   Decays<O::P> d[2];
   float dot[DK / 32][O::P];
   float erow[3][32], ecol[3][32];

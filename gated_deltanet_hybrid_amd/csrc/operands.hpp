@@ -68,7 +68,16 @@ template <> struct La<bf16> {
   }
   template <int W> static constexpr int rs() { return W; }  // elements of an LDS row
   template <int W> static constexpr int size() { return P * W; }
-  static constexpr int PS = P + 8;  // row stride of the decayed scores
+  // Decayed scores as two terms, each the 32 x 32 tiles 0: (0, 0), 1: (1, 0), 2: (1, 1) of a 64 x 64 lower
+  // triangle: rows of four 16-byte chunks, permuted by the row so that 16 rows' reads meet every bank once.
+  static constexpr int SCORE_TERMS = 2, SCORE_TERM = 3 * 1024, SCORES = SCORE_TERMS * SCORE_TERM;
+  __device__ __forceinline__ static int score_at(int tile, int c, int q, int h) {  // row c, columns 8 q + 4 h ..
+    return tile * 1024 + c * 32 + ((q ^ ((c >> 2) & 3)) << 3) + h * 4;
+  }
+  __device__ __forceinline__ static Frag score_row(const bf16* sc, int I, int c, int g, int h, int term) {
+    const int tile = I ? (g >= 2 ? 2 : 1) : 0;
+    return *reinterpret_cast<const bf16x8*>(sc + term * SCORE_TERM + tile * 1024 + c * 32 + (((2 * (g & 1) + h) ^ ((c >> 2) & 3)) << 3));
+  }
   __device__ __forceinline__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
@@ -133,7 +142,11 @@ template <> struct La<float> {
   template <int W> __device__ __forceinline__ static int at(int row, int col) { return row * (W + 8) + col; }
   template <int W> static constexpr int rs() { return W + 8; }
   template <int W> static constexpr int size() { return P * (W + 8); }
-  static constexpr int PS = P + 8;
+  static constexpr int SCORE_TERMS = 1, SCORE_TERM = P * (P + 8), SCORES = SCORE_TERM;
+  __device__ __forceinline__ static int score_at(int, int c, int q, int h) { return c * (P + 8) + q * 8 + h * 4; }
+  __device__ __forceinline__ static Frag score_row(const float* sc, int, int c, int g, int h, int) {
+    return *reinterpret_cast<const f32x4*>(sc + c * (P + 8) + g * 8 + h * 4);
+  }
   __device__ __forceinline__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);

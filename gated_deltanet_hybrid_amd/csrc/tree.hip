@@ -389,7 +389,8 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 
     }
   };
   auto load_tile = [&](int j, int i, Frag (&m)[GN]) {
-    const int t = w + 8 * i < TILES ? w + 8 * i : w;
+    const int t = w + 8 * i;
+    if (t >= TILES) return;
     const int W = t < AT ? DK : DV;
     const T* p = t < AT ? Ac + (int64_t)j * DK * DK + 16 * t + c : Bc + (int64_t)j * DK * DV + 16 * (t - AT) + c;
 #pragma unroll
@@ -479,7 +480,8 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 
     Frag f[TW][GN];
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-      const int t = w + 8 * i < TILES ? w + 8 * i : w;  // a wave without its last tile works on its first again
+      const int t = w + 8 * i;
+      if (t >= TILES) continue;
 #pragma unroll
       for (int k = 0; k < GN; ++k) {
         if constexpr (BF) f[i][k] = t < AT ? O::template col<DK>(at, O::template col_base<DK>(lane), t, k)
@@ -501,7 +503,8 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 
           for (int s = O::TERMS - 1; s >= 0; --s) {
             const Frag z = O::template row<DK>(zs[s], rz, 16 * I, k);
 #pragma unroll
-            for (int i = 0; i < TW; ++i) part[i][s % CH] = O::mma(f[i][k], z, part[i][s % CH]);
+            for (int i = 0; i < TW; ++i)
+              if (i == 0 || TILES % 8 == 0 || w + 8 * i < TILES) part[i][s % CH] = O::mma(f[i][k], z, part[i][s % CH]);
           }
       }
 #pragma unroll

@@ -674,8 +674,8 @@ hla_status_t hla_chunk_reps_backward(const hla_dims_t* d, const void* k, int32_t
  *             length are not read; outputs and gradients there are zero.
  * dtype is that of q, k, v, o and of their gradients; states, log_decay and their gradients are
  * float32.  Arithmetic: float32 sums, sums of log_decay in float64.  Over bf16 tensors what is float32
- * enters the matrix cores as bf16 terms: three (24 bits) where the result is float32, two for the
- * states and one (2^-8) for the decayed scores where it is rounded to bf16.  A number that is not
+ * enters the matrix cores as bf16 terms: three (24 bits) where the result is float32, two (2^-16)
+ * where it is rounded to bf16.  A number that is not
  * finite spreads over its own 64-token piece, to earlier tokens of the piece too.  Sums have a fixed
  * order: a call repeats its bits.
  */

@@ -4,8 +4,8 @@ Bounds.  Every output is a sum of products; A, the same recurrence over the inpu
 sum of the magnitudes.  A float32 sum of n terms is off by at most 6 standard deviations of n
 roundings of half a step (2^-24 of a partial sum, which is below A): 6 sqrt(n / 3) 2^-24 A.  A decay
 exp(x) is rounded from x in float32 and by the exponential: for the x that matter (e^-16 = 2^-24 and up)
-16 + 2 steps of 2^-24, 24 with the products by it.  Over bf16 tensors the decayed scores are rounded to
-2^-8 and the states that outputs read to 2^-16 of a term, and the output to 2^-8 of itself."""
+16 + 2 steps of 2^-24, 24 with the products by it.  Over bf16 tensors the decayed scores and
+the states that outputs read are rounded to 2^-16 of a term, and the output to 2^-8 of itself."""
 import numpy as np
 import torch
 
@@ -20,7 +20,7 @@ def steps(n):
 
 def bound(dtype, ref, mag, n):
     b = steps(n) * mag + 1e-37
-    return b + 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -16) * mag if dtype == "bf16" else b
+    return b + 2.0 ** -8 * np.abs(ref) + 2.0 ** -15 * mag if dtype == "bf16" else b
 
 
 class Case:
