@@ -8,7 +8,7 @@
 
 namespace {
 
-constexpr int64_t kMaxRows = ((int64_t)1 << 24) - 1;    // rows times segments: a launch counts its threads in 32 bits
+constexpr int64_t kMaxRows = ((int64_t)1 << 23) - 1;    // rows times segments: a launch counts its threads in 32 bits
 constexpr int64_t kMaxTokens = (int64_t)1 << 36;
 
 template <int A, class... P>
@@ -55,6 +55,8 @@ hla_status_t plan(const hla_la_dims_t* d, bool backward, Plan* p) {
   p->nseg = (int32_t)nseg;
   p->seg_pieces = (int32_t)each;
   if (rows * nseg > kMaxRows || (nseg > 1 && rows * p->n > 4294967295ll)) return HLA_ERR_BAD_SHAPE;
+  if (backward && d->Hk != d->H && (double)d->B * (double)d->T * (double)d->Hk * (d->dk / 4) > 4294967040.0)
+    return HLA_ERR_BAD_SHAPE;  // the sum over shared heads
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
     const size_t r = at;

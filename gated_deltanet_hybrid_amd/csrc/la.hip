@@ -175,6 +175,11 @@ __device__ __forceinline__ void inter(f32x16 (&acc)[IT], const f32x16 (&M)[NM], 
     for (int e = 0; e < 16; ++e) acc[I][e] *= d.gam[32 * I + acc_row(e, h)];
 }
 
+template <int IT> __device__ __forceinline__ void clear(f32x16 (&acc)[IT]) {
+#pragma unroll
+  for (int I = 0; I < IT; ++I) acc[I] = zero16();
+}
+
 // to[row] = sum over the wave's 32 columns of acc times the tile x4, for every row of the piece.
 template <int W, class T, int IT>
 __device__ __forceinline__ void row_dots(const f32x16 (&acc)[IT], const T* x4, float* to, int base, int lane, int c, int h) {
@@ -402,12 +407,13 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
   double decay = 0.0;
   float gnext = 0.f;  // two pieces ahead and in front of the tiles: memory answers in order, and the sums
   if (n) {            // of the next piece must not wait for its tiles
+    float g0 = 0.f;
     if (w == NW - 1) {
-      const float g0 = load_g(piece(0));
+      g0 = load_g(piece(0));
       if (n > 1) gnext = load_g(piece(1));
-      decays<P>(g0, lane, sh.d[0], &decay);
     }
     load(piece(0), true, true);
+    if (w == NW - 1) decays<P>(g0, lane, sh.d[0], &decay);
   }
   for (int64_t i = 0; i < n; ++i) {
     const int64_t p = piece(i);
@@ -430,7 +436,8 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
         tile_decays(D, d, tile, c, h);
         put_scores(sh.sc, s, D, tile, c, h);
       }
-      inter<DK, EXTRA || O::TERMS < 2 ? O::TERMS : 2, 1>(acc, M, sh.x1, d, rc, h);
+      if (a.init || i) inter<DK, EXTRA || O::TERMS < 2 ? O::TERMS : 2, 1>(acc, M, sh.x1, d, rc, h);
+      else clear(acc);  // the state is zero
       if constexpr (EXTRA) row_dots<DV>(acc, sh.x4, sh.dot[w], xa, lane, c, h);
     }
     if (i + 1 < n && w == NW - 1) decays<P>(gnow, lane, sh.d[(i + 1) & 1], &decay);
@@ -560,12 +567,13 @@ __global__ __launch_bounds__((DK + DV) * 2, 2) void la_reverse_kernel(LaReverse 
   double decay = 0.0;
   float gnext = 0.f;
   if (n) {
+    float g0 = 0.f;
     if (w == NW - 1) {
-      const float g0 = load_g(last - 1);
+      g0 = load_g(last - 1);
       if (n > 1) gnext = load_g(last - 2);
-      decays<P>(g0, lane, sh.d[0], &decay);
     }
     load(last - 1);
+    if (w == NW - 1) decays<P>(g0, lane, sh.d[0], &decay);
   }
   for (int64_t i = 0; i < n; ++i) {
     const int64_t p = last - 1 - i;
@@ -603,10 +611,12 @@ __global__ __launch_bounds__((DK + DV) * 2, 2) void la_reverse_kernel(LaReverse 
     }
     f32x16 acc[IT];
     if (is_k) {
-      inter<DV, O::TERMS, 1>(acc, M, sh.v, d, own(rv0), h);
+      if (a.init || i) inter<DV, O::TERMS, 1>(acc, M, sh.v, d, own(rv0), h);
+      else clear(acc);
       row_dots<DK>(acc, sh.k, sh.dot[w], own(xa0), lane, c, h);
     } else {
-      inter<DK, O::TERMS < 2 ? 1 : 2, 1>(acc, M, sh.k, d, own(rk0), h);
+      if (a.init || i) inter<DK, O::TERMS < 2 ? 1 : 2, 1>(acc, M, sh.k, d, own(rk0), h);
+      else clear(acc);
     }
     if (i + 1 < n && w == NW - 1) decays<P>(gnow, lane, sh.d[(i + 1) & 1], &decay);
     __syncthreads();

@@ -145,8 +145,11 @@ __device__ __forceinline__ void live_part(const TreeArgs& a, LiveShared<T, DK, D
       else if (sh.mask[i]) s = (float)static_cast<const T*>(a.v)[((b * n + i) * a.H + head) * DV + col];
       x[i] = s * sh.beta[i];
     }
+    // An update that is not finite belongs to its node and the nodes below it and to no other: it is kept
+    // out of the sums, where a zero of L or P would spread it, and put into their results at the end.
+    unsigned long long lost = 0;
 #pragma unroll
-    for (int i = 1; i < N; ++i) {
+    for (int i = 0; i < N; ++i) {
       if (i >= n) continue;
 #pragma unroll
       for (int j = 0; j < i; j += 4) {
@@ -154,6 +157,10 @@ __device__ __forceinline__ void live_part(const TreeArgs& a, LiveShared<T, DK, D
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (j + e < i) x[i] -= l[e] * x[j + e];
+      }
+      if (!(fabsf(x[i]) < INFINITY)) {
+        x[i] = 0.f;
+        lost |= 1ull << i;
       }
       sched_fence();
     }
@@ -168,7 +175,7 @@ __device__ __forceinline__ void live_part(const TreeArgs& a, LiveShared<T, DK, D
         for (int e = 0; e < 4; ++e)
           if (j + e <= i) s += p[e] * x[j + e];
       }
-      x[i] = s;
+      x[i] = (lost & sh.mask[i]) ? __builtin_nanf("") : s;
       sched_fence();
     }
     if (is_k) {
