@@ -4,7 +4,7 @@
 
 namespace hla {
 
-constexpr int kLaSlots = 64;  // most segments of a row
+constexpr int kLaSlots = 128;  // most segments of a row
 
 // One token tensor in a role of the recurrence: [B, ld, heads, width] of the call's dtype; heads
 // divides the call's heads, and neighbouring heads share.

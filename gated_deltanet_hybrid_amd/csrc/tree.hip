@@ -224,10 +224,13 @@ __device__ __forceinline__ void live_part(const TreeArgs& a, LiveShared<T, DK, D
     for (int I = 0; I < NT; ++I) {
       const int i = 32 * I + c;
       if (i >= n) continue;
+      const bool here = sh.mask[i] != 0;  // an absent node's r is zero, a live value need not be finite
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int at = n0 + q * 8 + h * 4;
-        f32x4 y = {acc[I][4 * q], acc[I][4 * q + 1], acc[I][4 * q + 2], acc[I][4 * q + 3]};
+        f32x4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = here ? acc[I][4 * q + e] : 0.f;
         if (state) {
           const f32x4 u = *reinterpret_cast<const f32x4*>(sh.out.o + i * S::OD + at);
           *reinterpret_cast<f32x4*>(a.o + ((b * n + i) * a.H + head) * DV + at) = y + u;
@@ -666,11 +669,15 @@ hipError_t decode_n(const TreeArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((tree_gates_kernel<T, DK, N / 16>), dim3(rows, gate_parts), dim3(256), 0, s, a, per);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  // A workgroup takes 1, 2 or 4 tiles of 16 nodes.  Few rows: as few as give 512 workgroups at most, so that
-  // more compute units work, each reading the maps; many rows: all, so that maps are read once.
+  // A workgroup takes 1, 2 or 4 tiles of 16 nodes, as few as give each compute unit a workgroup (16 nodes), so
+  // that more units work, each reading the maps; many rows: all, so that maps are read once.  40 bf16 maps of
+  // 128 x 128, us with 1, 2 and 4 tiles: 100 rows of 32 nodes 132, 144, 100 of 48 226, 180, 206, 200 of 48
+  // 351, 298, 221.  Where sequences hold 0 to 40 maps, less is lost: 100 of 32 124, 142, 100 of 48 190, 177,
+  // 205, 200 of 48 243, 256, 218.
   const int tiles = (a.n + 15) / 16;
   int per_wg = 1;
-  while (per_wg < tiles && (int64_t)rows * ((tiles + per_wg - 1) / per_wg) > 512) per_wg *= 2;
+  if (tiles > 1 && (int64_t)rows * a.n > 16 * 256) per_wg = 2;
+  if (tiles > 2 && (int64_t)rows * ((tiles + 1) / 2) > 256) per_wg = 4;
   const int groups = (tiles + per_wg - 1) / per_wg;
   const dim3 grid(rows * groups);
   // Two chunks ahead where a compute unit has one workgroup at most, whose chain waits for memory; else the

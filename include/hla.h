@@ -672,12 +672,14 @@ hla_status_t hla_chunk_reps_backward(const hla_dims_t* d, const void* k, int32_t
  *             included, it clears the state.
  *   lens      [B] int32 or NULL (T): tokens of each row, clamped to 0 .. T.  Tokens behind a row's
  *             length are not read; outputs and gradients there are zero.
+ *   sizes     dk, dv 64 or 128; H <= 65536, B H < 2^23, T <= 2^35.
+ * S_final may be S0's own buffer, and no other output may overlap an input or another output.
  * dtype is that of q, k, v, o and of their gradients; states, log_decay and their gradients are
  * float32.  Arithmetic: float32 sums, sums of log_decay in float64.  Over bf16 tensors what is float32
  * enters the matrix cores as bf16 terms: three (24 bits) where the result is float32, two (2^-16)
- * where it is rounded to bf16.  A number that is not
- * finite spreads over its own 64-token piece, to earlier tokens of the piece too.  Sums have a fixed
- * order: a call repeats its bits.
+ * where it is rounded to bf16.  A number that is not finite spreads over its own piece (64 tokens of
+ * bf16, 32 of float32), to earlier tokens of the piece too.  Sums have a fixed order: a call repeats
+ * its bits.
  */
 typedef struct {
   int64_t B, T, H, Hk, ld_T;
@@ -737,7 +739,7 @@ hla_status_t hla_la_decode(int64_t Bs, int64_t H, int64_t Hk, int32_t dk, int32_
  *   parent [Bs, n] int32 (device): -1 <= parent[i] < i.  Any other value (as -2 for the places behind a
  *          smaller tree) marks node i absent, and so are the nodes below it: their inputs are not used,
  *          their outputs and gates are zero.
- *   q, k [Bs, n, H, dk], v [Bs, n, H, dv] (dtype);  beta, alpha [Bs, n, H] float32.
+ *   q, k [Bs, n, H, dk], v [Bs, n, H, dv] (dtype);  beta, alpha [Bs, n, H] float32, alpha >= 0.
  *   S_cur, At_cur, At_cache, Bc_cache, reps_cache, n_rep, n_cache, n_cap, tau: as for hla_gdn_decode;
  *          n_cap <= 1024.  At_cur = NULL: no cache is read.
  * q, k, v, o and the caches and live matrices are 16-byte aligned, the others 4-byte.
@@ -748,8 +750,7 @@ hla_status_t hla_la_decode(int64_t Bs, int64_t H, int64_t Hk, int32_t dk, int32_
  *   gates_in  [Bs, n, H, n_cap] float32 or NULL (then n_rep >= 1): every node's own gates.
  *   o         [Bs, n, H, dv] float32 out.
  *   gates_out [Bs, n, H, n_cap] float32 out or NULL: the gates in front of the threshold, 0 behind
- *             n_cache[b] and at absent nodes.
- *   ws        hla_gdn_tree_workspace_bytes() bytes (0 without At_cur, n_cap = 0), for one call at a time.
+XX_workspace_bytes() bytes (0 without At_cur, n_cap = 0), for one call at a time.
  * Every chunk that any node reads is read once for all of them.  A NaN gate is below every threshold.
  * float32 accumulation; over bf16 maps z enters as three bf16 terms (24 bits).
  * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE (sizes, NaN tau), HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN,

@@ -380,3 +380,16 @@ def test_tree_few_and_many_rows(Bs, H, n, n_cap):
     if n_cap < 100:
         check_tree(o[:1, :, :1], ref, terms, "o")
     assert np.abs(num(gates[:1, :, :1].cpu()) - rg).max() < 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_absent_nodes_are_zero_over_any_live_state(dtype):
+    note(f"tree absent {dtype}")
+    x = make(1, 20, 2, 64, 128, dtype, 2, 2, seed=15)
+    x["parent"][0, 17:] = -2
+    x["parent"][0, 4] = 4
+    x["S_cur"][0, :, 3, 5] = float("inf")
+    x["At_cur"][0, :, 7, 9] = float("nan")
+    o = call(x, tau=0.3)
+    assert (o[0, 17:] == 0).all() and (o[0, 4] == 0).all()
+    assert not torch.isfinite(o[0, 0]).all()
