@@ -326,6 +326,16 @@ template <int IT> constexpr int kTiles = IT == 2 ? 3 : 1;  // score tiles on and
 // One workgroup of DV / 32 waves runs one segment of one row.  OUT: outputs from the state in front
 // of the segment; else the segment's state (from init, or zero).  EXTRA: the products with x4 that
 // the decays' gradient takes (`dot`).
+//
+// The next piece's tiles are asked for as this one's registers are stored to LDS, so a workgroup always has a
+// piece in flight; two workgroups a compute unit (their LDS) cover each other's barriers.  65536 tokens of 16
+// heads of 128 x 128 (bf16, 32 segments a row): the states 132 us for 540 MB (4.1 TB/s, matrix cores 40%
+// busy), the outputs 317 us for 1.1 GB (3.5 TB/s, 34%) as the profiler has them (285 and 124 in a stream of
+// calls); the loads and stores of the latter alone took 234, so memory bounds both, and the state pass is what
+// cutting the rows costs.  13 x 1531 tokens of 12 heads of 64 x 128 (float32, lengths 1 to 1531) 42 and 104
+// us: the float32 instructions have a sixteenth of bf16's rate.  What carries it: no branch in the scores
+// (504 -> 466 us in all), reads a step ahead of their products, addresses formed again in every piece instead
+// of kept (before that the registers spilled: 1640 us).
 template <class T, int DK, int DV, bool OUT, bool REV, bool EXTRA>
 __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_sweep_kernel(LaSweep a) {
   using O = La<T>;
@@ -493,6 +503,11 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
 // first DK / 32 waves hold G^T [DV, DK] and give dk (32 columns each), the others G [DK, DV] and give dv; the
 // four tiles are read once for both, and with both tiles of scores at hand, E and its sums too (see
 // la_decay_kernel).  One workgroup of (DK + DV) / 32 waves a segment.
+//
+// 4 x 4096 tokens of 16 heads of 128 x 128 (bf16): 191 us for 430 MB (2.3 TB/s), matrix cores 29% busy: eight
+// waves of 256 registers fill a compute unit, so nothing covers the two barriers and the score phase, in which
+// three of the eight waves work.  It stands for two sweeps that each read all four tiles (a training step 715
+// us with them, 563 with it).
 template <class T, int DK, int DV> struct LaReverseShared {
   using O = La<T>;
   alignas(16) T q[O::template size<DK>()];
@@ -670,7 +685,9 @@ __global__ __launch_bounds__((DK + DV) * 2, 2) void la_reverse_kernel(LaReverse 
   }
 }
 
-// The states in front of every segment from the segments' states from zero, in place.
+// The states in front of every segment from the segments' states from zero, in place.  A thread a value,
+// eight segments' loads ahead of the chain.  32 segments of 16 rows of 128 x 128: 17 us for 33 MB read and as
+// much written (3.9 TB/s).
 __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
   const int n = a.dk * a.dv;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -710,7 +727,8 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
 // and X + sum c at every other piece's.  Where gamma < 2^-24, X is zero to float32 and is taken as that,
 // so that the difference's rounding does not stand in for it; so it is in the piece that starts from a zero
 // state.  One workgroup runs one segment, a wave a
-// piece; only the chain of <dM, M> is one thread's.
+// piece; only the chain of <dM, M> is one thread's.  23 us in the step of 4 x 4096 tokens named above, most of
+// it the product of whole states (67 MB).
 constexpr int kLaChain = 64;
 template <int P>
 __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
@@ -867,7 +885,9 @@ __global__ __launch_bounds__(256) void la_group_sum_kernel(LaGroup a) {
   y[0] = (T)s.x; y[1] = (T)s.y; y[2] = (T)s.z; y[3] = (T)s.w;
 }
 
-// One token of every row: the state is read, updated and written in one pass.
+// One token of every row: the state is read, updated and written in one pass.  A thread's loads of the state
+// (16 bytes each) are all in flight before the first product.  256 sequences of 16 heads of 128 x 128: 80 us
+// for 540 MB (6.7 TB/s), at the memory's rate; one sequence 5.1 us, of which a launch is most.
 template <class T, int DK, int DV>
 __global__ __launch_bounds__(256) void la_step_kernel(LaStep a) {
   constexpr int CPR = DV / 4, RPP = 256 / CPR, NP = DK / RPP;
