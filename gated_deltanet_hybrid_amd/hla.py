@@ -1011,14 +1011,20 @@ def la_prefill(q, k, v, log_decay, S0=None, lens=None, want_o=True, want_state=T
     int32 [B] or None.  Returns (o [B, T, H, dv] in v's dtype or None, S_final [B, H, dk, dv] float32
     or None)."""
     d, dev = _la_inputs(q if want_o else None, k, v, log_decay, lens)
-    if want_o and o is None:
+    state = (d.B, d.H, d.dk, d.dv)
+    _need_on(S0, state, torch.float32, dev, "S0")
+    if not want_o:
+        o = None
+    elif o is None:
         o = torch.empty((d.B, d.T, d.H, d.dv), dtype=v.dtype, device=dev)
-    if want_state and S_final is None:
-        S_final = torch.empty((d.B, d.H, d.dk, d.dv), dtype=torch.float32, device=dev)
-    o, S_final = o if want_o else None, S_final if want_state else None
-    _need_on(S0, (d.B, d.H, d.dk, d.dv), torch.float32, dev, "S0")
-    _need_on(o, (d.B, d.T, d.H, d.dv), v.dtype, dev, "o")
-    _need_on(S_final, (d.B, d.H, d.dk, d.dv), torch.float32, dev, "S_final")
+    else:
+        _need_on(o, (d.B, d.T, d.H, d.dv), v.dtype, dev, "o")
+    if not want_state:
+        S_final = None
+    elif S_final is None:
+        S_final = torch.empty(state, dtype=torch.float32, device=dev)
+    else:
+        _need_on(S_final, state, torch.float32, dev, "S_final")
     ws = _la_workspace(LA_PREFILL, d, ws, dev)
     _call("hla_la_prefill", dev, ctypes.byref(d), _addr(q) if want_o else None, _addr(k), _addr(v), _addr(log_decay),
           _addr(lens), _addr(S0), _addr(o), _addr(S_final), _addr(ws), 0 if ws is None else ws.numel())
@@ -1051,14 +1057,16 @@ def la_decode(q, k, v, log_decay, S, o=None):
     if v.dim() != 3 or k.dim() != 3:
         raise ValueError("k and v must be [Bs, heads, width]")
     (Bs, H, dv), (_, Hk, dk), dev = v.shape, k.shape, v.device
-    _need_on(v, (Bs, H, dv), v.dtype, dev, "v")
+    if not v.is_contiguous():
+        raise ValueError("v must be contiguous")
     for t, name in ((q, "q"), (k, "k")):
         _need_on(t, (Bs, Hk, dk), v.dtype, dev, name)
     _need_on(log_decay, (H,) if log_decay.dim() == 1 else (Bs, H), torch.float32, dev, "log_decay")
     _need_on(S, (Bs, H, dk, dv), torch.float32, dev, "S")
     if o is None:
-        o = torch.empty((Bs, H, dv), dtype=v.dtype, device=dev)
-    _need_on(o, (Bs, H, dv), v.dtype, dev, "o")
+        o = torch.empty_like(v)
+    else:
+        _need_on(o, (Bs, H, dv), v.dtype, dev, "o")
     _call("hla_la_decode", dev, Bs, H, Hk, dk, dv, _dtype_code(v), _addr(q), _addr(k), _addr(v), _addr(log_decay),
           1 if log_decay.dim() == 1 else 0, _addr(S), _addr(o))
     return o
@@ -1119,7 +1127,8 @@ def gdn_tree_decode(q, k, v, beta, alpha, parent, S_cur, At_cur=None, At_cache=N
             raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
     if o is None:
         o = torch.empty((Bs, n, H, dv), dtype=torch.float32, device=dev)
-    _need_on(o, (Bs, n, H, dv), torch.float32, dev, "o")
+    else:
+        _need_on(o, (Bs, n, H, dv), torch.float32, dev, "o")
     _call("hla_gdn_tree_decode", dev, Bs, H, n, dk, dv, dt, _addr(q), _addr(k), _addr(v), _addr(beta), _addr(alpha),
           _addr(parent), _addr(S_cur), _addr(At_cur), _addr(At_cache), _addr(Bc_cache), _addr(reps_cache), n_rep,
           _addr(n_cache), n_cap, _addr(gates_in), ctypes.c_float(tau), _addr(o), _addr(gates_out), _addr(ws),
