@@ -365,8 +365,8 @@ __global__ __launch_bounds__(256) void tree_front_kernel(TreeArgs a, int parts, 
 // that is AHEAD read chunks away is asked for while this one is worked on.
 //
 // 1024 rows of 16 nodes over 64 chunks of 128 x 128 (bf16): 640 us for 4.3 GB (6.7 TB/s), bound by memory.
-// One row of 7 nodes over 8 chunks 15.5 us, 1.9 us a chunk: z goes through LDS and two barriers to the next
-// chunk.  105 rows of 33 nodes over up to 100 chunks of 64 x 128 (float32) 156 us, the longest row's chain.
+// 16 rows of 7 nodes over 8 chunks 14.7 us, 1.8 us a chunk: maps and z go through LDS and a barrier, which
+// nothing else of a lone workgroup covers.  105 rows of 33 nodes over up to 100 chunks of 64 x 128 (float32) 156 us, the longest row's chain.
 template <class T, int DK, int DV, int NT, int AHEAD>
 __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 2) void tree_chain_kernel(TreeArgs a, int groups) {
   using O = La16<T>;
@@ -374,8 +374,11 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 
   constexpr bool BF = sizeof(T) == 2;
   constexpr int N = 16 * NT, TILES = (DK + DV) / 16, AT = DK / 16, TW = (TILES + 7) / 8, GN = DK / O::KG;
   constexpr int RZ = La<T>::template rs<DK>(), LD = BF ? DK * (DK + DV) / 8 / 512 : 1;
-  __shared__ alignas(16) T at[BF ? DK * DK : 8], bt[BF ? DK * DV : 8];
-  __shared__ alignas(16) T zs[O::TERMS][N * RZ];
+  // two buffers in turn where LDS has room for them: no barrier between a wave's reads and its writes of z
+  // (7 nodes of 16 rows over 8 chunks, whole call 29.6 -> 28.9 us)
+  constexpr int BUF = !BF || AHEAD == 2 ? 2 : 1;
+  __shared__ alignas(16) T at_[BF ? BUF * DK * DK : 8], bt_[BF ? BUF * DK * DV : 8];
+  __shared__ alignas(16) T zs_[BUF][O::TERMS][N * RZ];
   __shared__ unsigned char act[kTreeSlots];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, G = lane >> 4, c = lane & 15;
   const int64_t row = blockIdx.x / groups, b = row / a.H;
@@ -435,10 +438,11 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 
     jb[k + 1] = jb[k] >= 0 ? next(jb[k]) : -1;
   }
   f32x4 v[TW][NT];  // z of this wave's columns of At, or o of its columns of Bc
+  int turn = 0;
   auto put_z = [&](int t, int I, f32x4 r) {
 #pragma unroll
     for (int s = 0; s < O::TERMS; ++s) {
-      T* to = zs[s] + La<T>::template at<DK>(16 * I + c, 16 * t + 4 * G);
+      T* to = zs_[turn][s] + La<T>::template at<DK>(16 * I + c, 16 * t + 4 * G);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const T x = (T)r[e];
@@ -473,6 +477,8 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 
 #pragma unroll
     for (int I = 0; I < NT; ++I) g[I] = gn[B][I];
     const unsigned read = act[j];
+    T *at = at_ + (BF ? turn * DK * DK : 0), *bt = bt_ + (BF ? turn * DK * DV : 0);
+    const auto& zs = zs_[turn];
     if constexpr (BF) {
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
@@ -537,7 +543,8 @@ __global__ __launch_bounds__(512, NT == 1 && AHEAD == 1 && sizeof(T) == 2 ? 4 : 
         for (int i = 0; i < TW; ++i) load_tile(ja, i, m[B][i]);
       }
     }
-    __syncthreads();
+    if constexpr (BUF == 1) __syncthreads();
+    else turn ^= 1;
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
       const int t = w + 8 * i;
