@@ -393,3 +393,26 @@ def test_absent_nodes_are_zero_over_any_live_state(dtype):
     o = call(x, tau=0.3)
     assert (o[0, 17:] == 0).all() and (o[0, 4] == 0).all()
     assert not torch.isfinite(o[0, 0]).all()
+
+
+# few distinct rows, repeated: (rows, T, repeated) so that rows stay whole, are cut into segments of several
+# pieces, and into as many segments as there are
+@pytest.mark.parametrize("B,T,times,dk,dv,dtype,lens", [
+    (3, 200, 180, 64, 128, "f32", None), (3, 330, 180, 128, 64, "bf16", [330, 0, 100]), (2, 650, 24, 128, 128, "bf16", None),
+    (2, 400, 40, 64, 64, "f32", [400, 37]), (1, 32 * 260 + 3, 1, 64, 64, "f32", None), (1, 64 * 150, 1, 64, 64, "bf16", None)])
+def test_rows_whole_and_cut(B, T, times, dk, dv, dtype, lens):
+    note(f"la rows {B} {T} {times} {dk} {dv} {dtype}")
+    c = Case(B, T, 1, 1, dk, dv, dtype, lens=lens, seed=21)
+    many = lambda t: None if t is None else t.repeat(times, *[1] * (t.dim() - 1)).contiguous()  # noqa: E731
+    q, k, v, g = map(many, c.args())
+    kw = {n: many(t) for n, t in c.kw().items()}
+    dO, dS = many(c.device("dO")), many(c.device("dS"))
+    o, S = hla.la_prefill(q, k, v, g, **kw)
+    d = hla.la_prefill_backward(q, k, v, g, dO, dS_final=dS, **kw)
+    for t in (o, S, *d.values()):
+        assert torch.equal(t, many(t[:B]))
+    (ro, rS), rd, n = c.forward(), c.backward(), T + 2 * dk
+    check(o[:B], ro[0], ro[1], dtype, n, "o")
+    check(S[:B], rS[0], rS[1], "f32", n, "S_final")
+    for m, ref in rd.items():
+        check(d[m][:B], ref[0], ref[1], dtype if m in ("dq", "dk", "dv") else "f32", 2 * T + 4 * dk, m)
