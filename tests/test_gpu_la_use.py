@@ -354,7 +354,7 @@ def test_what_is_not_finite_stays_in_its_branch(dtype, what, value):
         assert not torch.isfinite(o[0, i]).all(), i
 
 
-@pytest.mark.parametrize("Bs,H,n,n_cap", [(1, 3, 9, 1024), (40, 16, 33, 2), (300, 2, 17, 3)])
+@pytest.mark.parametrize("Bs,H,n,n_cap", [(1, 3, 9, 1024), (40, 16, 33, 2), (300, 2, 17, 3), (60, 2, 40, 3)])
 def test_tree_few_and_many_rows(Bs, H, n, n_cap):
     """The forms that the sizes choose: one launch or two in front, one or two chunks ahead, one to four
     tiles of nodes a workgroup.  Rows drawn from a few, so that the reference is quick."""
