@@ -321,6 +321,28 @@ template <int NT, int P, int W, bool REV, class T> struct Mover {
   }
 };
 
+// Columns `col` of a state of MT tiles of 32 rows, W columns wide, from memory: as it is, or turned (stored
+// [W, 32 MT]: a lane's rows come in runs of four).
+template <int MT, int W, int NM>
+__device__ __forceinline__ void load_state(f32x16 (&M)[NM], const float* s0, bool turned, int col, int h) {
+  if (turned) {
+    const float* at = s0 + col * (32 * MT) + 4 * h;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(at + 32 * m + 8 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) M[m][4 * q + e] = x[e];
+      }
+  } else {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) M[m][e] = s0[(32 * m + acc_row(e, h)) * W + col];
+  }
+}
+
 template <int IT> constexpr int kTiles = IT == 2 ? 3 : 1;  // score tiles on and below the diagonal
 
 // One workgroup of DV / 32 waves runs one segment of one row.  OUT: outputs from the state in front
@@ -397,14 +419,7 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
   f32x16 M[MT];
   const int col = 32 * w + c0;
   if (a.init) {
-    const float* s0 = a.init + row * a.init_row + (int64_t)seg * DK * DV;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = 32 * m + acc_row(e, h0);
-        M[m][e] = a.init_t ? s0[col * DK + r] : s0[r * DV + col];
-      }
+    load_state<MT, DV>(M, a.init + row * a.init_row + (int64_t)seg * DK * DV, a.init_t, col, h0);
   } else {
 #pragma unroll
     for (int m = 0; m < MT; ++m) M[m] = zero16();
@@ -565,15 +580,9 @@ __global__ __launch_bounds__((DK + DV) * 2, 2) void la_reverse_kernel(LaReverse 
   for (int m = 0; m < NM; ++m) M[m] = zero16();
   if (a.init) {
     const float* s0 = a.init + row * a.init_row + (int64_t)seg * DK * DV;
-    const int tall = is_k ? DV : DK, wide = is_k ? DK : DV;  // of this wave's state
-    const bool turned = is_k == (a.init_t != 0);             // stored [DV, DK], or [DK, DV] with init_t
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = 32 * m + acc_row(e, h0);
-        if (32 * m < tall) M[m][e] = turned ? s0[col * tall + r] : s0[r * wide + col];
-      }
+    const bool turned = is_k == (a.init_t != 0);  // stored [DV, DK], or [DK, DV] with init_t
+    if (is_k) load_state<DV / 32, DK>(M, s0, turned, col, h0);
+    else load_state<KW, DV>(M, s0, turned, col, h0);
   }
   const int fk0 = O::template row_base<DK>(lane), fv0 = O::template row_base<DV>(lane);
   const int rk0 = O::template rowc_base<DK>(lane), rv0 = O::template rowc_base<DV>(lane);
