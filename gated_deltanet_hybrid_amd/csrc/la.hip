@@ -519,7 +519,7 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
 // four tiles are read once for both, and with both tiles of scores at hand, E and its sums too (see
 // la_decay_kernel).  One workgroup of (DK + DV) / 32 waves a segment.
 //
-// 4 x 4096 tokens of 16 heads of 128 x 128 (bf16): 191 us for 430 MB (2.3 TB/s), matrix cores 29% busy: eight
+// 4 x 4096 tokens of 16 heads of 128 x 128 (bf16): 183 us for 430 MB (2.3 TB/s), matrix cores 29% busy: eight
 // waves of 256 registers fill a compute unit, so nothing covers the two barriers and the score phase, in which
 // three of the eight waves work.  It stands for two sweeps that each read all four tiles (a training step 715
 // us with them, 563 with it).
