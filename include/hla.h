@@ -749,8 +749,10 @@ hla_status_t hla_la_decode(int64_t Bs, int64_t H, int64_t Hk, int32_t dk, int32_
  * hla_gdn_tree_decode
  *   gates_in  [Bs, n, H, n_cap] float32 or NULL (then n_rep >= 1): every node's own gates.
  *   o         [Bs, n, H, dv] float32 out.
- *   gates_out [Bs, n, H, n_cap] float32 out or NULL: the gates in front of the threshold, 0 behind
-XX_workspace_bytes() bytes (0 without At_cur, n_cap = 0), for one call at a time.
+ *   gates_out [Bs, n, H, n_cap] float32 out or NULL: the gates in front of the threshold, 0 from
+ *             n_cache[b] on and at absent nodes.
+ *   ws        hla_gdn_tree_workspace_bytes() bytes (0 without At_cur, n_cap = 0), 16-byte aligned, for one
+ *             call at a time.
  * Every chunk that any node reads is read once for all of them.  A NaN gate is below every threshold.
  * float32 accumulation; over bf16 maps z enters as three bf16 terms (24 bits).
  * Errors: HLA_ERR_NULL_ARG, HLA_ERR_BAD_SHAPE (sizes, NaN tau), HLA_ERR_BAD_DTYPE, HLA_ERR_ALIGN,
