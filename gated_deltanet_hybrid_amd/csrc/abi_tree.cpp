@@ -61,6 +61,7 @@ hla_status_t hla_gdn_tree_decode(int64_t Bs, int64_t H, int32_t n, int32_t dk, i
   const hla_status_t st = check_sizes(Bs, H, n, dk, dv, dtype);
   if (st != HLA_OK) return st;
   if (!q || !k || !v || !beta || !alpha || !parent || !S_cur || !o) return HLA_ERR_NULL_ARG;
+  if (!At_cur && gates_out) return HLA_ERR_NULL_ARG;  // without a cache there are no gates to write
   if (!aligned<16>(q, k, v, S_cur, At_cur, At_cache, Bc_cache, reps_cache, o, ws) ||
       !aligned<4>(beta, alpha, parent, n_cache, gates_in, gates_out))
     return HLA_ERR_ALIGN;

@@ -1114,7 +1114,13 @@ def gdn_tree_decode(q, k, v, beta, alpha, parent, S_cur, At_cur=None, At_cache=N
     Bs, n, H, dk, dv, dt, dev = _tree_inputs(k, v, beta, alpha, parent, S_cur, At_cur)
     _need_on(q, (Bs, n, H, dk), k.dtype, dev, "q")
     n_cap, n_rep = 0, 0
-    if At_cur is not None:
+    if At_cur is None:
+        if gates_out is not None:
+            raise ValueError("gates_out needs At_cur and the cache")
+    else:
+        for t, name in ((At_cache, "At_cache"), (Bc_cache, "Bc_cache"), (n_cache, "n_cache")):
+            if t is None:
+                raise ValueError(f"At_cur needs {name}")
         n_cap = _tree_cache(At_cache, Bc_cache, n_cache, k, Bs, H, dk, dv, dev)
         if reps_cache is not None:
             n_rep = reps_cache.shape[3]

@@ -741,7 +741,8 @@ hla_status_t hla_la_decode(int64_t Bs, int64_t H, int64_t Hk, int32_t dk, int32_
  *          their outputs and gates are zero.
  *   q, k [Bs, n, H, dk], v [Bs, n, H, dv] (dtype);  beta, alpha [Bs, n, H] float32, alpha >= 0.
  *   S_cur, At_cur, At_cache, Bc_cache, reps_cache, n_rep, n_cache, n_cap, tau: as for hla_gdn_decode;
- *          n_cap <= 1024.  At_cur = NULL: no cache is read.
+ *          n_cap <= 1024.  At_cur = NULL: no cache is read, what belongs to it (gates_in too) is not used,
+ *          and there are no gates: gates_out must be NULL.
  * q, k, v, o and the caches and live matrices are 16-byte aligned, the others 4-byte.
  */
 
