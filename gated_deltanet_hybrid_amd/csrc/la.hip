@@ -735,7 +735,7 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
 // over s < t.  The first term is X = <dM, M_P> - sum b, with <dM, M_P> a product of whole states at the segment's end
 // and X + sum c at every other piece's.  Where gamma < 2^-24, X is zero to float32 and is taken as that,
 // so that the difference's rounding does not stand in for it; so it is in the piece that starts from a zero
-// state.  One workgroup runs one segment, a wave a
+// state.  A decay that clears the state (e^-104 is zero) has gradient 0, one that is NaN a NaN.  One workgroup runs one segment, a wave a
 // piece; only the chain of <dM, M> is one thread's.  23 us in the step of 4 x 4096 tokens named above, most of
 // it the product of whole states (67 MB).
 constexpr int kLaChain = 64;
@@ -825,7 +825,7 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
       if (lane == 0) {
         sum_b[p - lo] = sb;
         sum_c[p - lo] = sc;
-        gone[p - lo] = lg * kLog2e > -24.0 ? 0.f : 1.f;
+        gone[p - lo] = lg * kLog2e <= -24.0 ? 1.f : 0.f;
       }
     }
     __syncthreads();
@@ -853,7 +853,7 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
         if (lane + o < 64) behind += z;
       }
       const int64_t t = p * P + lane;
-      if (lane < P && t < a.T) *out(t) = on && g > -104.f ? (float)(at_end[p - lo] + (before - own_before) + behind) : 0.f;
+      if (lane < P && t < a.T) *out(t) = on && !(g <= -104.f) ? (float)(at_end[p - lo] + (before - own_before) + behind) : 0.f;
     }
     __syncthreads();
   }
