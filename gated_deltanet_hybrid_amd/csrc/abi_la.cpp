@@ -22,7 +22,7 @@ hla_status_t status(hipError_t e) { return e == hipSuccess ? HLA_OK : HLA_ERR_HI
 struct Plan {
   int64_t rows, n;
   int32_t nseg, seg_pieces;
-  size_t fwd, rev, dec_f, dec_r, b, c, e, dg, dq, dk, total;  // offsets
+  size_t fwd, rev, dec_f, dec_r, dS0, b, c, e, dg, dq, dk, total;  // offsets
 };
 
 hla_status_t check_dims(const hla_la_dims_t* d) {
@@ -71,11 +71,15 @@ int64_t segments(double rows, int64_t pieces, int64_t least, int dk, int dv, boo
 
 hla_status_t plan(const hla_la_dims_t* d, bool backward, bool lens, Plan* p) {
   const int64_t rows = d->B * d->H, piece = hla::la_piece(d->dtype), pieces = (d->T + piece - 1) / piece;
-  // The backward call's segments are 32 pieces at most (as long as there are no more than kLaSlots), since
-  // the decays' gradient runs a difference of sums through a segment.  The segments behind a row's length end
-  // at once: given lengths count as 0.6 of the rows (lengths drawn from 1 to T, 22 sizes: 0.6 of the rows 2 per
-  // cent faster than all of them, and 13 x 1531 tokens of 12 heads of 64 x 128, float32, 196 -> 169 us).
-  const int64_t nseg = segments((lens ? 0.6 : 1.0) * (double)rows, pieces, backward ? (pieces + 31) / 32 : 1, d->dk, d->dv, backward);
+  // The backward call's segments are 32 pieces at most, since the decays' gradient runs differences of sums
+  // through a segment; where that makes more than kLaSlots of them, they grow up to kLaChain pieces.  The segments
+  // behind a row's length end at once: given lengths count as 0.6 of the rows (lengths drawn from 1 to T, 22 sizes:
+  // 0.6 of the rows 2 per cent faster than all of them, and 13 x 1531 tokens of 12 heads of 64 x 128, float32,
+  // 196 -> 169 us).
+  const int64_t few = (pieces + hla::kLaSlots - 1) / hla::kLaSlots, long_each = few < hla::kLaChain ? few : hla::kLaChain;
+  const int64_t nseg = backward && few > 32
+      ? (pieces + long_each - 1) / long_each
+      : segments((lens ? 0.6 : 1.0) * (double)rows, pieces, backward ? (pieces + 31) / 32 : 1, d->dk, d->dv, backward);
   const int64_t each = (pieces + nseg - 1) / nseg;
   p->rows = rows;
   p->n = (int64_t)d->dk * d->dv;
@@ -103,6 +107,7 @@ hla_status_t plan(const hla_la_dims_t* d, bool backward, bool lens, Plan* p) {
       p->dec_f = take(rows * nseg * 8);
       p->dec_r = take(rows * nseg * 8);
     }
+    p->dS0 = take(state);
     p->b = take(tokens);
     p->c = take(tokens);
     p->e = take(tokens);
@@ -266,7 +271,7 @@ hla_status_t hla_la_prefill_backward(const hla_la_dims_t* d, const void* q, cons
     r.init_t = !many;
     r.dk = shared ? f(p.dk) : dk;
     r.dv = dv;
-    r.dS0 = dS0;
+    r.dS0 = dS0 ? dS0 : S0 ? f(p.dS0) : nullptr;  // the decays' gradient needs it
     r.dot = f(p.b);
     r.esum = f(p.e);
     r.B = d->B; r.T = d->T; r.H = d->H; r.Hk = d->Hk; r.ld_T = d->ld_T;
@@ -292,7 +297,8 @@ hla_status_t hla_la_prefill_backward(const hla_la_dims_t* d, const void* q, cons
   c.n = (int32_t)p.n;
   c.piece = hla::la_piece(d->dtype);
   c.w = d->dk;
-  c.from_zero = S0 == nullptr;
+  c.S0 = S0;
+  c.dS0 = dS0 ? dS0 : f(p.dS0);
   if ((e = hla::launch_la_decay(c, stream)) != hipSuccess) return status(e);
   if (d->decay_per_head && (e = hla::launch_la_head_sum(c.dg, dlog_decay, d->B, d->H, d->T, stream)) != hipSuccess)
     return status(e);

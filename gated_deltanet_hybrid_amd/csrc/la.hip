@@ -732,13 +732,18 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
 //     gamma <dM, M_0> + sum_{j<t} b_j + sum_{i>=t} c_i + sum_{i>=t>j} E_ij
 // (b_j = k_j . the part of dk_j that comes from behind the piece, c_i = q_i . the part of dq_i from in
 // front of it, E_ij the score pairs): the double sum is, with e_s row s's sum less column s's, that of -e_s
-// over s < t.  The first term is X = <dM, M_P> - sum b, with <dM, M_P> a product of whole states at the segment's end
-// and X + sum c at every other piece's.  Where gamma < 2^-24, X is zero to float32 and is taken as that,
-// so that the difference's rounding does not stand in for it; so it is in the piece that starts from a zero
-// state.  A decay that clears the state (e^-104 is zero) has gradient 0, one that is NaN a NaN.  One workgroup runs one segment, a wave a
-// piece; only the chain of <dM, M> is one thread's.  23 us in the step of 4 x 4096 tokens named above, most of
-// it the product of whole states (67 MB).
-constexpr int kLaChain = 64;
+// over s < t.  With B and C the piece's sums of b and c, the first term X is known from either side,
+//     X = <dM, M_P> - B = <gamma dM + ..., M_0> - C,
+// and X + C and X + B are the next pieces' whole products in either direction; at both ends of the segment they are
+// products of whole states.  Such a chain carries the roundings of all it has summed, where the true X shrinks
+// with every decay, and a number that is not finite, so X is taken from the chain that has summed less: m, the
+// magnitudes summed so far, stands for its error.  (From the end alone, 540 rows of 900 tokens with a loss on the
+// last 40 and decays of 0.1 to 0.3: tokens far in front had roundings of the last ones for values that are below
+// float32's range.)  Where
+// gamma < 2^-24 and the end's difference is below its roundings X is zero; so it is in the piece that starts from a
+// zero state.  A decay that clears the state (e^-104 is zero) has gradient 0, one that is NaN a NaN.  One workgroup
+// runs one segment, a wave a piece; only the chains are one thread's.
+struct Whole { double x, m; };  // a product of whole states, and its magnitudes
 template <int P>
 __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -758,48 +763,62 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
   auto out = [&](int64_t t) -> float* { return a.dg + (a.per_head ? row * a.T + t : (b * a.T + t) * a.H + head); };
   const int64_t all = (a.T + P - 1) / P, live = (Tb + P - 1) / P, first = (int64_t)seg * a.seg_pieces;
   const int64_t end = first + a.seg_pieces < all ? first + a.seg_pieces : all, last = end < live ? end : live;
-  __shared__ double part[4];
-  // <dM, M> behind the segment
-  double x = 0.0;
-  if (first < last) {
-    const float* m = a.fwd + (row * (a.nseg + 1) + seg + 1) * (int64_t)a.n;
-    const bool behind = seg + 1 < a.nseg;
-    const float* r = behind ? a.rev + (row * a.nseg + seg) * (int64_t)a.n : a.dS ? a.dS + row * a.n : nullptr;
-    if (r && behind) {
-      for (int i0 = tid; i0 < a.n; i0 += 256 * 16) {  // 4096 divides every dk dv
-        float u[16], v[16];
+  __shared__ Whole part[2][4];
+  auto add = [](Whole& s, float u, float v) {
+    const double x = (double)u * v;
+    s.x += x;
+    s.m += fabs(x);
+  };
+  auto plain = [&](Whole& s, const float* m, const float* r) {  // 4096 divides every dk dv
+    for (int i0 = tid; i0 < a.n; i0 += 256 * 16) {
+      float u[16], v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          u[e] = m[i0 + 256 * e];
-          v[e] = r[i0 + 256 * e];
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x += (double)u[e] * v[e];
+      for (int e = 0; e < 16; ++e) {
+        u[e] = m[i0 + 256 * e];
+        v[e] = r[i0 + 256 * e];
       }
-    } else if (r) {  // dS is [dk, dv], M here [dv, dk]: 16 x 16 tiles, a lane four values of a row of dS
-      const int w = a.w, tall = a.n / w, tiles = a.n / 256, k = lane & 15, c = (lane >> 4) * 4;
-      for (int t0 = wave; t0 < tiles; t0 += 16) {  // 16 divides the number of tiles
-        float4 v[4];
-        float u[4][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = t0 + 4 * e, k0 = t % (w / 16) * 16 + k, c0 = t / (w / 16) * 16 + c;
-          v[e] = *reinterpret_cast<const float4*>(r + k0 * tall + c0);
+      for (int e = 0; e < 16; ++e) add(s, u[e], v[e]);
+    }
+  };
+  auto turned = [&](Whole& s, const float* m, const float* r) {  // r [dk, dv], m [dv, dk]: 16 x 16 tiles, a lane four values of a row of r
+    const int w = a.w, tall = a.n / w, tiles = a.n / 256, k = lane & 15, c = (lane >> 4) * 4;
+    for (int t0 = wave; t0 < tiles; t0 += 16) {  // 16 divides the number of tiles
+      float4 v[4];
+      float u[4][4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) u[e][q] = m[(c0 + q) * w + k0];
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int t = t0 + 4 * e, k0 = t % (w / 16) * 16 + k, c0 = t / (w / 16) * 16 + c;
+        v[e] = *reinterpret_cast<const float4*>(r + k0 * tall + c0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x += (double)u[e][0] * v[e].x + (double)u[e][1] * v[e].y + (double)u[e][2] * v[e].z + (double)u[e][3] * v[e].w;
+        for (int q = 0; q < 4; ++q) u[e][q] = m[(c0 + q) * w + k0];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        add(s, u[e][0], v[e].x); add(s, u[e][1], v[e].y); add(s, u[e][2], v[e].z); add(s, u[e][3], v[e].w);
       }
     }
-  }
+  };
+  if (first < last) {  // <dM, M> behind the segment, and in front of it
+    Whole s[2] = {{0.0, 0.0}, {0.0, 0.0}};
+    const float *fwd = a.fwd + (row * (a.nseg + 1) + seg) * (int64_t)a.n, *rev = a.rev + (row * a.nseg + seg) * (int64_t)a.n;
+    if (seg + 1 < a.nseg) plain(s[0], fwd + a.n, rev);
+    else if (a.dS) turned(s[0], fwd + a.n, a.dS + row * a.n);
+    if (seg) plain(s[1], fwd, rev - a.n);
+    else if (a.S0) plain(s[1], a.S0 + row * a.n, a.dS0 + row * a.n);
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
-  if (lane == 0) part[wave] = x;
-  // every piece's sums, then the chain of <dM, M> over the pieces, then the pieces' outputs
-  __shared__ double sum_b[kLaChain], sum_c[kLaChain], at_end[kLaChain];
-  __shared__ float gone[kLaChain];
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) {
+        s[i].x += __shfl_xor(s[i].x, o, 64);
+        s[i].m += __shfl_xor(s[i].m, o, 64);
+      }
+      if (lane == 0) part[i][wave] = s[i];
+    }
+  }
+  // every piece's sums, then the two chains over the pieces, then the pieces' outputs
+  __shared__ double sum_b[kLaChain], sum_c[kLaChain], X[kLaChain], X_m[kLaChain];  // the segment's pieces
+  __shared__ float mag_b[kLaChain], mag_c[kLaChain], gamma[kLaChain];
   auto take = [&](int64_t p, float& bb, float& cc, float& ee, float& g) {
     const int64_t t = p * P + lane;
     const bool on = lane < P && t < Tb;
@@ -809,53 +828,83 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
     g = on ? g_at(t) : 0.f;
     return on;
   };
-  double phi = 0.0;
-  for (int64_t hi = last; hi > first; hi -= kLaChain) {  // from the end, as many pieces as the chain holds
-    const int64_t lo = hi - kLaChain > first ? hi - kLaChain : first;
-    for (int64_t p = lo + wave; p < hi; p += 4) {
-      float bb, cc, ee, g;
-      take(p, bb, cc, ee, g);
-      double sb = bb, sc = cc, lg = g;
+  auto whole = [&](int i, int64_t t) {  // the product at a boundary, as the token t behind it leaves it (its decay)
+    const double f = t < 0 || t >= Tb ? 1.0 : (double)decay_of(g_at(t));
+    Whole s{0.0, 0.0};
+    for (int w = 0; w < 4; ++w) {
+      s.x += part[i][w].x * f;
+      s.m += part[i][w].m * f;
+    }
+    return s;
+  };
+  for (int64_t p = first + wave; p < last; p += 4) {
+    float bb, cc, ee, g;
+    take(p, bb, cc, ee, g);
+    double sb = bb, sc = cc, lg = g;
+    float mb = fabsf(bb), mc = fabsf(cc);
 #pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) {
-        sb += __shfl_xor(sb, o, 64);
-        sc += __shfl_xor(sc, o, 64);
-        lg += __shfl_xor(lg, o, 64);
-      }
-      if (lane == 0) {
-        sum_b[p - lo] = sb;
-        sum_c[p - lo] = sc;
-        gone[p - lo] = lg * kLog2e <= -24.0 ? 1.f : 0.f;
-      }
+    for (int o = 32; o >= 1; o >>= 1) {
+      sb += __shfl_xor(sb, o, 64);
+      sc += __shfl_xor(sc, o, 64);
+      lg += __shfl_xor(lg, o, 64);
+      mb += __shfl_xor(mb, o, 64);
+      mc += __shfl_xor(mc, o, 64);
     }
-    __syncthreads();
-    if (tid == 0) {
-      if (hi == last) {
-        phi = part[0] + part[1] + part[2] + part[3];
-        if (last * P < Tb) phi *= decay_of(g_at(last * P));
-      }
-      for (int64_t p = hi - 1; p >= lo; --p) {
-        const double X = gone[p - lo] != 0.f || (a.from_zero && p == 0) ? 0.0 : phi - sum_b[p - lo];
-        at_end[p - lo] = X;
-        phi = X + sum_c[p - lo];
-      }
+    if (lane == 0) {
+      sum_b[p - first] = sb;
+      sum_c[p - first] = sc;
+      mag_b[p - first] = mb;
+      mag_c[p - first] = mc;
+      gamma[p - first] = exp2_((float)(lg * kLog2e));
     }
-    __syncthreads();
-    for (int64_t p = lo + wave; p < hi; p += 4) {
-      float bb, cc, ee, g;
-      const bool on = take(p, bb, cc, ee, g);
-      const double own_before = (double)bb - ee;
-      double before = own_before, behind = cc;
+  }
+  __syncthreads();
+  if (tid == 0 && first < last) {
+    const int n = (int)(last - first);
+    const bool zero = first == 0 && !a.S0;  // the first piece starts from a zero state
+    Whole s = whole(0, last * P);
+#pragma unroll 4
+    for (int i = n - 1; i >= 0; --i) {
+      const double m = s.m + mag_b[i];
+      s.x -= sum_b[i];
+      if (zero && i == 0) {
+        s = {0.0, 0.0};
+      } else if (gamma[i] < 0x1p-24f && fabs(s.x) <= 0x1p-24 * m) {
+        s.x = 0.0;
+        s.m *= gamma[i] * 0x1p24;
+      } else {
+        s.m = m;
+      }
+      X[i] = s.x;
+      X_m[i] = s.m;
+      s.x += sum_c[i];
+      s.m += mag_c[i];
+    }
+    s = whole(1, seg ? first * P : -1);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      s.x -= sum_c[i];
+      s.m += mag_c[i];
+      if ((zero && i == 0) || (X_m[i] < (double)INFINITY && !(s.m < X_m[i]))) s = {X[i], X_m[i]};
+      else X[i] = s.x;
+      s.x += sum_b[i];
+      s.m += mag_b[i];
+    }
+  }
+  __syncthreads();
+  for (int64_t p = first + wave; p < last; p += 4) {
+    float bb, cc, ee, g;
+    const bool on = take(p, bb, cc, ee, g);
+    const double own_before = (double)bb - ee;
+    double before = own_before, behind = cc;
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_up(before, o, 64), z = __shfl_down(behind, o, 64);
-        if (lane >= o) before += y;
-        if (lane + o < 64) behind += z;
-      }
-      const int64_t t = p * P + lane;
-      if (lane < P && t < a.T) *out(t) = on && !(g <= -104.f) ? (float)(at_end[p - lo] + (before - own_before) + behind) : 0.f;
+    for (int o = 1; o < 64; o <<= 1) {
+      const double y = __shfl_up(before, o, 64), z = __shfl_down(behind, o, 64);
+      if (lane >= o) before += y;
+      if (lane + o < 64) behind += z;
     }
-    __syncthreads();
+    const int64_t t = p * P + lane;
+    if (lane < P && t < a.T) *out(t) = on && !(g <= -104.f) ? (float)(X[p - first] + (before - own_before) + behind) : 0.f;
   }
   for (int64_t t = (last > first ? last : first) * P + tid; t < end * P && t < a.T; t += 256) *out(t) = 0.f;
 }

@@ -4,7 +4,8 @@
 
 namespace hla {
 
-constexpr int kLaSlots = 128;  // most segments of a row
+constexpr int kLaSlots = 128;  // most segments of a row, unless its segments of kLaChain pieces are more (backward)
+constexpr int kLaChain = 64;   // most pieces of a segment of the backward call: la_decay_kernel holds them
 
 // One token tensor in a role of the recurrence: [B, ld, heads, width] of the call's dtype; heads
 // divides the call's heads, and neighbouring heads share.
@@ -70,10 +71,10 @@ struct LaDecay {         // the gradient of g from the sweeps' dot products
   const float* fwd;           // [rows, nseg + 1, n]: states in front of each segment, and behind the last
   const float* rev;           // [rows, nseg, n]: the gradient that enters each segment from behind (but the last's)
   const float* dS;            // [rows, n transposed] or null: the final state's gradient
+  const float *S0, *dS0;      // [rows, n transposed]: the initial state and its gradient; S0 null: zero
   float* dg;                  // [B, T, H], or [rows, T] (per_head)
   int64_t B, T, H;
   int32_t per_head, nseg, seg_pieces, n, piece, w;  // n = dk dv; w: the row width of fwd and rev
-  int32_t from_zero;          // no initial state
 };
 
 struct LaGroup { const float* x; void* y; int64_t tokens; int32_t group, width, heads; };

@@ -706,7 +706,10 @@ hla_status_t hla_la_prefill(const hla_la_dims_t* d, const void* q, const void* k
  * With G_t = exp(g_{t+1}) G_{t+1} + q_t dO_t^T (dS_final behind the last token):
  *     dq_t = M_t dO_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  dg_t = exp(g_t) <G_t, M_{t-1}>,
  *     dS0 = exp(g_1) G_1; shared heads' dq and dk and a head's one dg are sums.
- * dg is the gradient of log_decay; it is 0 where a decay clears the state.
+ * dg is the gradient of log_decay; it is 0 where a decay clears the state.  It is formed from sums over
+ * tokens: its error is that of a float32 sum of the magnitudes k_j . dk_j and q_j . dq_j over the tokens
+ * in front of t's piece and in it, or behind and in it, whichever is less (so a token far from every loss
+ * has an error as small as its gradient); dg of one decay a head is the sum of these values, with their errors.
  *   dO [B, T, H, dv] (dtype);  dS_final [B, H, dk, dv] float32 or NULL (zero).
  *   dq, dk [B, T, Hk, dk], dv [B, T, H, dv] (dtype, out);  dlog_decay [B, T, H] or [H] float32 (out);
  *   dS0 [B, H, dk, dv] float32 (out) or NULL.
