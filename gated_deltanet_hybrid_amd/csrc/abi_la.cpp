@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "la.hpp"
+#include "timing.hpp"
 
 namespace {
 
@@ -164,6 +165,7 @@ hla_status_t hla_la_prefill(const hla_la_dims_t* d, const void* q, const void* k
   st = plan(d, false, lens != nullptr, &p);
   if (st != HLA_OK) return st;
   if (p.total && (!ws || ws_bytes < p.total)) return HLA_ERR_WORKSPACE;
+  const hla::TimedLaunch tl(HLA_KERNEL_LA, stream);
   char* w = static_cast<char*>(ws);
   float* states = reinterpret_cast<float*>(w + p.fwd);
   hla::LaSweep a = common(d, p, log_decay, lens);
@@ -217,6 +219,7 @@ hla_status_t hla_la_prefill_backward(const hla_la_dims_t* d, const void* q, cons
   st = plan(d, true, lens != nullptr, &p);
   if (st != HLA_OK) return st;
   if (!ws || ws_bytes < p.total) return HLA_ERR_WORKSPACE;
+  const hla::TimedLaunch tl(HLA_KERNEL_BWD_LA, stream);
   char* w = static_cast<char*>(ws);
   auto f = [w](size_t at) { return reinterpret_cast<float*>(w + at); };
   const hla::LaRole rq{q, d->ld_T, (int32_t)d->Hk}, rk{k, d->ld_T, (int32_t)d->Hk}, rv{v, d->ld_T, (int32_t)d->H},
@@ -319,6 +322,7 @@ hla_status_t hla_la_decode(int64_t Bs, int64_t H, int64_t Hk, int32_t dk, int32_
   if (st != HLA_OK) return st;
   if (!q || !k || !v || !log_decay || !S || !o) return HLA_ERR_NULL_ARG;
   if (!aligned<16>(S) || !aligned<4>(q, k, v, log_decay, o)) return HLA_ERR_ALIGN;
+  const hla::TimedLaunch tl(HLA_KERNEL_LA, stream);
   hla::LaStep a{};
   a.q = q; a.k = k; a.v = v; a.g = log_decay; a.S = S; a.o = o;
   a.Bs = Bs; a.H = H;

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "timing.hpp"
 #include "tree.hpp"
 
 namespace {
@@ -77,6 +78,7 @@ hla_status_t hla_gdn_tree_decode(int64_t Bs, int64_t H, int32_t n, int32_t dk, i
     a.gate = reinterpret_cast<float*>(w + l.gate);
     a.active = reinterpret_cast<int32_t*>(w + l.active);
   }
+  const hla::TimedLaunch tl(HLA_KERNEL_TREE, stream);
   a.q = q; a.k = k; a.v = v; a.beta = beta; a.alpha = alpha; a.parent = parent;
   a.S_cur = S_cur; a.At_cur = At_cur; a.At_cache = At_cache; a.Bc_cache = Bc_cache; a.reps_cache = reps_cache;
   a.n_cache = n_cache; a.gates_in = gates_in; a.o = o; a.gates_out = gates_out;
@@ -96,6 +98,7 @@ hla_status_t hla_gdn_tree_accept(int64_t Bs, int64_t H, int32_t n, int32_t dk, i
   if (commit && (n_cap < 1 || n_cap > hla::kTreeSlots)) return HLA_ERR_BAD_SHAPE;
   if (!aligned<16>(k, v, S_cur, At_cur, At_cache, Bc_cache) || !aligned<4>(beta, alpha, parent, node, n_cache, commit))
     return HLA_ERR_ALIGN;
+  const hla::TimedLaunch tl(HLA_KERNEL_TREE, stream);
   hla::TreeAccept a{};
   a.k = k; a.v = v; a.beta = beta; a.alpha = alpha; a.parent = parent; a.node = node;
   a.S_cur = S_cur; a.At_cur = At_cur; a.At_cache = At_cache; a.Bc_cache = Bc_cache;

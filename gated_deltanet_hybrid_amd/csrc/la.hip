@@ -19,10 +19,11 @@
 // as float32: the decayed values, which enter the states, and the state where the decays' gradient is
 // formed from it.  Two (2^-16 at most) where it reaches bf16 outputs only: the state that outputs read and
 // the decayed scores.
+#include "../../include/hla.h"
+
 #include "operands.hpp"
 #include "la.hpp"
 #include "kernels.hpp"
-#include "timing.hpp"
 
 namespace hla {
 

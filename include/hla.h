@@ -809,7 +809,10 @@ typedef enum {
   HLA_KERNEL_BWD_ROUTER = 10, /* backward: router gates to queries and keys              */
   HLA_KERNEL_PREFILL = 11,    /* one-pass native prefill (bf16): UT, outputs, state scan */
   HLA_KERNEL_BWD_REPS = 12,   /* backward: learned representatives (tiles and reduction)  */
-  HLA_KERNEL_COUNT = 13
+  HLA_KERNEL_LA = 13,         /* linear attention: a prompt's passes, or one token        */
+  HLA_KERNEL_BWD_LA = 14,     /* backward: linear attention, all passes of a call         */
+  HLA_KERNEL_TREE = 15,       /* trees of drafted tokens: answering them, or accepting    */
+  HLA_KERNEL_COUNT = 16
 } hla_kernel_t;
 
 /*
