@@ -361,6 +361,7 @@ template <int IT> constexpr int kTiles = IT == 2 ? 3 : 1;  // score tiles on and
 // of kept (before that the registers spilled: 1640 us).
 template <class T, int DK, int DV, bool OUT, bool REV, bool EXTRA>
 __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_sweep_kernel(LaSweep a) {
+  static_assert(!(OUT && REV), "outputs are made forward; la_reverse_kernel makes the reversed ones");
   using O = La<T>;
   constexpr int P = O::P, NT = DV * 2, NW = DV / 32, MT = DK / 32, IT = P / 32;
   __shared__ LaShared<T, DK, DV, OUT, EXTRA> sh;
@@ -390,12 +391,10 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
   if constexpr (EXTRA) p4 = (const T*)a.x4.p + (b * a.x4.ld * a.x4.heads + head / (int)(a.H / a.x4.heads)) * DV;
   const float* gp = a.per_head ? a.g + head : a.g + b * a.ld_g * a.H + head;
 
-  // row r of piece p is token P p + r, or counted from the piece's end
-  auto row_of = [](int r) { return REV ? P - 1 - r : r; };
-  auto token = [&](int64_t p, int r) -> int64_t { return p * P + row_of(r); };
+  // row r of piece p is token P p + r, or (reversed) counted from the piece's end, with the decay behind it
   auto load_g = [&](int64_t p) -> float {
     if (lane >= P) return 0.f;
-    const int64_t t = token(p, lane) + (REV ? 1 : 0);
+    const int64_t t = p * P + (REV ? P - lane : lane);
     return t < Tb ? (a.per_head ? gp[0] : gp[t * a.H]) : 0.f;
   };
   using ML1 = Mover<NT, P, DK, REV, T>;
@@ -474,10 +473,10 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
       const int rows = (int)(a.T - p * P < P ? a.T - p * P : P), live_rows = (int)(Tb - p * P < P ? Tb - p * P : P);
       const int64_t o0 = ((b * a.T + p * P) * a.H + head) * DV;
       void* to = a.out_f32 ? (void*)(static_cast<float*>(a.out) + o0) : (void*)(static_cast<T*>(a.out) + o0);
-      put_out<REV, P, T>(acc, to, a.out_f32, own_s((int)a.H * DV), rows, live_rows, col, h);
+      put_out<false, P, T>(acc, to, a.out_f32, own_s((int)a.H * DV), rows, live_rows, col, h);
       if constexpr (EXTRA) {
         if (tid < P) {
-          const int64_t t = token(p, tid);
+          const int64_t t = p * P + tid;
           if (t < a.T) {
             float x = 0.f;
             for (int q = 0; q < NW; ++q) x += sh.dot[q][tid];
@@ -498,19 +497,14 @@ __global__ __launch_bounds__(DV * 2, DK == 128 && DV == 64 ? 1 : 2) void la_swee
     if constexpr (EXTRA)
       for (int64_t t = t0 + tid; t < t1; t += NT) a.dot[row * a.T + t] = 0.f;
   }
-  float* to = nullptr;
-  float last_decay = 1.f;
-  if (a.loc) {
-    to = a.loc + row * a.loc_row + (int64_t)seg * DK * DV;
-  } else if (a.fin && seg == (REV ? 0 : a.nseg - 1)) {
-    to = a.fin + row * a.fin_row;
-    if (REV && Tb > 0) last_decay = decay_of(gp[0]);
-  }
+  float* to = nullptr;  // a reversed pass has `loc`
+  if (REV || a.loc) to = a.loc + row * a.loc_row + (int64_t)seg * DK * DV;
+  else if (a.fin && seg == a.nseg - 1) to = a.fin + row * a.fin_row;
   if (to) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) to[(32 * m + acc_row(e, h0)) * DV + col] = M[m][e] * last_decay;
+      for (int e = 0; e < 16; ++e) to[(32 * m + acc_row(e, h0)) * DV + col] = M[m][e];
   }
   if (a.decay && tid == NT - 64) a.decay[row * a.nseg + seg] = decay;
 }

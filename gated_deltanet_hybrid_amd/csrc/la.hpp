@@ -16,7 +16,7 @@ struct LaRole {
 };
 
 // One sweep of the recurrence M_t = exp(g_t) M_{t-1} + x2_t x3_t^T, out_t = M_t^T x1_t over the
-// tokens of every row (b, h), cut into nseg segments of seg_pieces pieces.  Reversed sweeps run from
+// tokens of every row (b, h), cut into nseg segments of seg_pieces pieces.  Reversed sweeps (states only) run from
 // the last token to the first and take the decay of the token behind (x1, x2, x3 at t; g at t + 1).
 struct LaSweep {
   LaRole x1, x2, x3, x4;
