@@ -737,7 +737,8 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
 // float32's range.)  Where
 // gamma < 2^-24 and the end's difference is below its roundings X is zero; so it is in the piece that starts from a
 // zero state.  A decay that clears the state (e^-104 is zero) has gradient 0, one that is NaN a NaN.  One workgroup
-// runs one segment, a wave a piece; only the chains are one thread's.
+// runs one segment, a wave a piece; only the chains are one thread's.  33 us in the step of 4 x 4096 tokens named
+// above, most of it the two products of whole states (124 MiB; 23.6 us with the end's alone).
 struct Whole { double x, m; };  // a product of whole states, and its magnitudes
 template <int P>
 __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
@@ -904,7 +905,10 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
   for (int64_t t = (last > first ? last : first) * P + tid; t < end * P && t < a.T; t += 256) *out(t) = 0.f;
 }
 
-// The gradient of one decay for each head: the sum over its rows' tokens, in a fixed order.
+// The gradient of one decay for each head: the sum over its rows' tokens, in a fixed order.  One workgroup a head
+// walks the batch's rows one behind another, so short rows cost it most: 4096 rows of 8 tokens of 2 heads make the
+// backward call 302 us with a decay for each token and 1051 with one a head, 1024 x 64 of 16 heads 584 and 858, 32 x 4096
+// of 16 heads 1174 and 1163.
 __global__ __launch_bounds__(1024) void la_head_sum_kernel(const float* x, float* y, int64_t B, int64_t H, int64_t T) {
   double s = 0.0;
   for (int64_t b = 0; b < B; ++b)

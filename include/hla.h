@@ -671,7 +671,8 @@ hla_status_t hla_chunk_reps_backward(const hla_dims_t* d, const void* k, int32_t
  *   log_decay g <= 0, float32: [B, ld_T, H] (decay_per_head = 0) or [H] (1).  Below -1e4, -inf
  *             included, it clears the state.
  *   lens      [B] int32 or NULL (T): tokens of each row, clamped to 0 .. T.  Tokens behind a row's
- *             length are not read; outputs and gradients there are zero.
+ *             length are not read; outputs and gradients there are zero.  Where every row is full NULL is
+ *             faster: with lengths, rows are cut into segments for a batch of which some end early.
  *   sizes     dk, dv 64 or 128; H <= 65536, B H < 2^23, T <= 2^35.
  * S_final may be S0's own buffer, and no other output may overlap an input or another output.
  * dtype is that of q, k, v, o and of their gradients; states, log_decay and their gradients are
