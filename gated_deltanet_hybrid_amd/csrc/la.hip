@@ -33,7 +33,7 @@ constexpr double kLog2e = 1.4426950408889634;
 constexpr float kLgFloor = -1.0e4f;  // stands for -inf: 2^-14427 is zero in every type used here
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
-// exp(g) by way of log 2 in float64; a NaN stays
+// exp(g) by way of log 2 in float64; a NaN stays, and below 2^-126 the instruction gives zero
 __device__ __forceinline__ float decay_of(float g) {
   return exp2_((float)((double)(g < kLgFloor ? kLgFloor : g) * kLog2e));
 }
@@ -736,7 +736,7 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScan a) {
 // last 40 and decays of 0.1 to 0.3: tokens far in front had roundings of the last ones for values that are below
 // float32's range.)  Where
 // gamma < 2^-24 and the end's difference is below its roundings X is zero; so it is in the piece that starts from a
-// zero state.  A decay that clears the state (e^-104 is zero) has gradient 0, one that is NaN a NaN.  One workgroup
+// zero state.  A decay that clears the state has gradient 0, one that is NaN a NaN.  One workgroup
 // runs one segment, a wave a piece; only the chains are one thread's.  33 us in the step of 4 x 4096 tokens named
 // above, most of it the two products of whole states (124 MiB; 23.6 us with the end's alone).
 struct Whole { double x, m; };  // a product of whole states, and its magnitudes
@@ -900,7 +900,7 @@ __global__ __launch_bounds__(256) void la_decay_kernel(LaDecay a) {
       if (lane + o < 64) behind += z;
     }
     const int64_t t = p * P + lane;
-    if (lane < P && t < a.T) *out(t) = on && !(g <= -104.f) ? (float)(X[p - first] + (before - own_before) + behind) : 0.f;
+    if (lane < P && t < a.T) *out(t) = on && decay_of(g) != 0.f ? (float)(X[p - first] + (before - own_before) + behind) : 0.f;
   }
   for (int64_t t = (last > first ? last : first) * P + tid; t < end * P && t < a.T; t += 256) *out(t) = 0.f;
 }

@@ -668,8 +668,9 @@ hla_status_t hla_chunk_reps_backward(const hla_dims_t* d, const void* k, int32_t
  *     M_t = exp(g_t) M_{t-1} + k_t v_t^T,     o_t = M_t^T q_t        (S = M^T in math orientation)
  *   q, k      [B, ld_T, Hk, dk], v [B, ld_T, H, dv] (dtype); Hk divides H, and value heads
  *             h = i H/Hk .. (i + 1) H/Hk - 1 share query and key head i.  q is not scaled.
- *   log_decay g <= 0, float32: [B, ld_T, H] (decay_per_head = 0) or [H] (1).  Below -1e4, -inf
- *             included, it clears the state.
+ *   log_decay g <= 0, float32: [B, ld_T, H] (decay_per_head = 0) or [H] (1).  A decay below float32's
+ *             smallest normal number (g below -87.33, -inf included) is zero and clears the state;
+ *             so does the product of a piece's decays where it falls below.
  *   lens      [B] int32 or NULL (T): tokens of each row, clamped to 0 .. T.  Tokens behind a row's
  *             length are not read; outputs and gradients there are zero.  Where every row is full NULL is
  *             faster: with lengths, rows are cut into segments for a batch of which some end early.
